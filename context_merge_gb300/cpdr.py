@@ -30,7 +30,8 @@ EXPORTED = ["cpdr_ctx_create", "cpdr_ctx_destroy", "cpdr_buffer_sizes", "cpdr_pl
             "cpdr_merge", "cpdr_fwd", "cpdr_host_workspace_bytes",
             "cpdr_forward_host", "cpdr_forward_noalloc", "cpdr_check_device_status", "cpdr_selftest_wait_timeout",
             "cpdr_conv1d_fwd", "cpdr_plan_conv_tokens", "cpdr_bwd_workspace_bytes", "cpdr_bwd",
-            "cpdr_last_error", "cpdr_version"]
+            "cpdr_glr_carry_bytes", "cpdr_glr_fwd", "cpdr_glr_bwd", "cpdr_glr_step", "cpdr_rmsnorm_fwd",
+            "cpdr_rmsnorm_bwd_workspace_bytes", "cpdr_rmsnorm_bwd", "cpdr_last_error", "cpdr_version"]
 
 
 class CpdrError(RuntimeError):
@@ -86,6 +87,14 @@ def load():
         lib.cpdr_bwd.argtypes = [vp] * 16 + [sz, vp]
         lib.cpdr_forward_host.argtypes = [vp] * 9 + [sz, vp]
         lib.cpdr_forward_noalloc.argtypes = [vp] * 9
+        i32, i64, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+        lib.cpdr_glr_carry_bytes.argtypes = [vp, i32, ctypes.POINTER(sz)]
+        lib.cpdr_glr_fwd.argtypes = [vp] * 4 + [i32] + [vp] * 4
+        lib.cpdr_glr_bwd.argtypes = [vp] * 6 + [i32] + [vp] * 4
+        lib.cpdr_glr_step.argtypes = [vp] * 6 + [i32] * 3 + [vp] * 2
+        lib.cpdr_rmsnorm_fwd.argtypes = [vp, i64, i32, vp, vp, vp, f32] + [vp] * 5
+        lib.cpdr_rmsnorm_bwd_workspace_bytes.argtypes = [vp, i64, i32, ctypes.POINTER(sz)]
+        lib.cpdr_rmsnorm_bwd.argtypes = [vp, i64, i32, vp, vp, f32] + [vp] * 5 + [sz, vp]
         lib.cpdr_check_device_status.argtypes = [vp, vp]
         lib.cpdr_selftest_wait_timeout.argtypes = [vp, ctypes.c_longlong, vp]
         for name in EXPORTED:
@@ -105,6 +114,18 @@ def _check(status: int):
 
 def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
+
+
+def _check_tensor(name: str, t, shape, dtype, device, nullable: bool = False):
+    """Raises ValueError unless t is a contiguous CUDA tensor of that shape, dtype and device (or None, if it may be)."""
+    if t is None:
+        if nullable:
+            return
+        raise ValueError(f"{name} is missing")
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {list(shape)} {dtype} tensor, got {list(t.shape)} {t.dtype}")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
 def _stream(stream) -> ctypes.c_void_p:
@@ -337,6 +358,128 @@ class Context:
         act = {"silu": 1, None: 0, "none": 0}[activation]
         _check(self._lib.cpdr_conv1d_fwd(self._h, _ptr(x), _ptr(weight), _ptr(bias), C, act, _ptr(y),
                                          _stream(stream)))
+
+    # ---- gated linear recurrence -------------------------------------------
+    def glr_carry_shape(self, channels):
+        """Shape of the fp32 ``carry`` that ``glr_fwd`` keeps for ``glr_bwd``:
+        the state before every 16th token of each sequence."""
+        n = ctypes.c_size_t()
+        _check(self._lib.cpdr_glr_carry_bytes(self._h, int(channels), ctypes.byref(n)))
+        return (n.value // (4 * int(channels)), int(channels))
+
+    def _glr_shapes(self, x):
+        if x.dim() != 3 or tuple(x.shape[:2]) != (self.B, self.T):
+            raise ValueError(f"x must be a [{self.B}, {self.T}, C] tensor, got {list(x.shape)}")
+        C = x.shape[2]
+        return C, (self.B, self.T, C), (self.N, C)
+
+    def glr_fwd(self, x, g, y, h0=None, hT=None, carry=None, stream=None):
+        """y_t = h_t = exp(g_t) h_{t-1} + x_t over every sequence of the
+        context: x and y [B, T, C] in its token order and input dtype, g fp32;
+        h0 and hT [N, C] fp32 or None; carry (``glr_carry_shape``) keeps what
+        ``glr_bwd`` needs."""
+        C, tok, st = self._glr_shapes(x)
+        f32, dev = torch.float32, x.device
+        _check_tensor("x", x, tok, self.torch_dtype, dev)
+        _check_tensor("g", g, tok, f32, dev)
+        _check_tensor("y", y, tok, self.torch_dtype, dev)
+        _check_tensor("h0", h0, st, f32, dev, True)
+        _check_tensor("hT", hT, st, f32, dev, True)
+        if carry is not None:
+            _check_tensor("carry", carry, self.glr_carry_shape(C), f32, dev)
+        _check(self._lib.cpdr_glr_fwd(self._h, _ptr(x), _ptr(g), _ptr(h0), C, _ptr(y), _ptr(hT), _ptr(carry),
+                                      _stream(stream)))
+
+    def glr_bwd(self, x, g, carry, dy, dhT=None, out=None, stream=None):
+        """Gradients of sum <dy, y> + sum <dhT, hT>: a dict of dx (input
+        dtype), dg and dh0 (fp32), written into ``out``'s tensors if given."""
+        C, tok, st = self._glr_shapes(x)
+        f32, dev = torch.float32, x.device
+        _check_tensor("x", x, tok, self.torch_dtype, dev)
+        _check_tensor("g", g, tok, f32, dev)
+        _check_tensor("carry", carry, self.glr_carry_shape(C), f32, dev)
+        _check_tensor("dy", dy, tok, self.torch_dtype, dev)
+        _check_tensor("dhT", dhT, st, f32, dev, True)
+        if out is None:
+            out = dict(dx=torch.empty_like(x), dg=torch.empty_like(g), dh0=torch.empty(st, dtype=f32, device=dev))
+        _check_tensor("dx", out["dx"], tok, self.torch_dtype, dev)
+        _check_tensor("dg", out["dg"], tok, f32, dev)
+        _check_tensor("dh0", out.get("dh0"), st, f32, dev, True)
+        _check(self._lib.cpdr_glr_bwd(self._h, _ptr(x), _ptr(g), _ptr(carry), _ptr(dy), _ptr(dhT), C,
+                                      _ptr(out["dx"]), _ptr(out["dg"]), _ptr(out.get("dh0")), _stream(stream)))
+        return out
+
+    def glr_step(self, x, g, state, y, slots=None, state_out=None, stream=None):
+        """One token for each row: x and y [n, C] in the input dtype, g [n, C]
+        fp32; row i continues the sequence whose state is slot ``slots[i]``
+        (int32; None: i) of state [S, C] fp32, updated in place or into
+        ``state_out``.  Rows with a slot outside 0 .. S - 1 are left alone;
+        rows of one slot are its consecutive tokens."""
+        if x.dim() != 2 or state.dim() != 2:
+            raise ValueError("x must be [n, C] and state [S, C]")
+        n, C = x.shape
+        S = state.shape[0]
+        f32, dev = torch.float32, x.device
+        _check_tensor("x", x, (n, C), self.torch_dtype, dev)
+        _check_tensor("g", g, (n, C), f32, dev)
+        _check_tensor("state", state, (S, C), f32, dev)
+        _check_tensor("y", y, (n, C), self.torch_dtype, dev)
+        _check_tensor("slots", slots, (n,), torch.int32, dev, True)
+        if state_out is None:
+            state_out = state
+        _check_tensor("state_out", state_out, (S, C), f32, dev)
+        _check(self._lib.cpdr_glr_step(self._h, _ptr(x), _ptr(g), _ptr(state), _ptr(state_out), _ptr(slots), n, S, C,
+                                       _ptr(y), _stream(stream)))
+
+    # ---- RMS norm --------------------------------------------------------
+    def _rows(self, x):
+        if x.dim() < 1:
+            raise ValueError("x must have at least one dimension")
+        width = x.shape[-1]
+        return x.numel() // width if width else 0, width
+
+    def rmsnorm_fwd(self, x, weight, residual=None, sum_out=None, y=None, y8=None, scale=None, eps=1e-6, stream=None):
+        """RMS norm of s = x + residual over the last axis, times weight
+        (fp32): s into ``sum_out``, the norm into ``y`` (input dtype) and/or
+        ``y8`` (float8_e4m3fn) with ``scale`` (fp32, one per row)."""
+        rows, width = self._rows(x)
+        dev, dt = x.device, self.torch_dtype
+        _check_tensor("x", x, x.shape, dt, dev)
+        _check_tensor("weight", weight, (width,), torch.float32, dev)
+        _check_tensor("residual", residual, x.shape, dt, dev, True)
+        _check_tensor("sum_out", sum_out, x.shape, dt, dev, True)
+        _check_tensor("y", y, x.shape, dt, dev, True)
+        _check_tensor("y8", y8, x.shape, torch.float8_e4m3fn, dev, True)
+        _check_tensor("scale", scale, x.shape[:-1], torch.float32, dev, True)
+        _check(self._lib.cpdr_rmsnorm_fwd(self._h, rows, width, _ptr(x), _ptr(residual), _ptr(weight), eps,
+                                          _ptr(sum_out), _ptr(y), _ptr(y8), _ptr(scale), _stream(stream)))
+
+    def rmsnorm_bwd_workspace_bytes(self, rows, width):
+        n = ctypes.c_size_t()
+        _check(self._lib.cpdr_rmsnorm_bwd_workspace_bytes(self._h, int(rows), int(width), ctypes.byref(n)))
+        return n.value
+
+    def rmsnorm_bwd(self, s, weight, dy, dsum=None, eps=1e-6, out=None, workspace=None, stream=None):
+        """Gradients of the norm from s (``sum_out``, or x), dy and the
+        gradient ``dsum`` that reaches s past the norm: a dict of ds (input
+        dtype; of x and residual alike) and dweight (fp32)."""
+        rows, width = self._rows(s)
+        dev, dt = s.device, self.torch_dtype
+        _check_tensor("s", s, s.shape, dt, dev)
+        _check_tensor("weight", weight, (width,), torch.float32, dev)
+        _check_tensor("dy", dy, s.shape, dt, dev)
+        _check_tensor("dsum", dsum, s.shape, dt, dev, True)
+        if out is None:
+            out = dict(ds=torch.empty_like(s), dweight=torch.empty_like(weight))
+        _check_tensor("ds", out["ds"], s.shape, dt, dev)
+        _check_tensor("dweight", out["dweight"], (width,), torch.float32, dev)
+        if workspace is None:
+            workspace = torch.empty(self.rmsnorm_bwd_workspace_bytes(rows, width), dtype=torch.uint8, device=dev)
+        _check(self._lib.cpdr_rmsnorm_bwd(self._h, rows, width, _ptr(s), _ptr(weight), eps, _ptr(dy), _ptr(dsum),
+                                          _ptr(out["ds"]), _ptr(out["dweight"]), _ptr(workspace),
+                                          ctypes.c_size_t(workspace.numel() * workspace.element_size()),
+                                          _stream(stream)))
+        return out
 
     def check_device_status(self, stream=None):
         _check(self._lib.cpdr_check_device_status(self._h, _stream(stream)))

@@ -47,6 +47,7 @@ void free_tables(cpdr::DeviceTables &t) {
     cudaFree(t.host_items);
     cudaFree(t.bwd_pre_items);
     cudaFree(t.conv_halo);
+    cudaFree(t.glr_spans);
     cudaFree(t.status);
     t = cpdr::DeviceTables();
 }
@@ -123,6 +124,14 @@ namespace cpdr {
 // Records `msg` as this thread's last error and returns `s` (for other
 // translation units of the library).
 cpdr_status fail_with(cpdr_status s, const std::string &msg) { return set_err(s, msg); }
+cpdr_status check_launch_ctx(const cpdr_ctx *c) { return check_ctx(c); }
+cpdr_status check_device_ptr(const void *p, const char *name, bool nullable) { return check_ptr(p, name, nullable); }
+cpdr_status check_launched(int rc, const char *what) { return launch_rc(rc, what); }
+int device_sms(int dev) {
+    int sms = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) sms = 152;
+    return sms;
+}
 }  // namespace cpdr
 
 extern "C" {
@@ -164,6 +173,7 @@ cpdr_status cpdr_ctx_create(const cpdr_desc *desc, cpdr_ctx **out) {
         if (e == cudaSuccess) e = upload(&t.host_items, p.host_items);
         if (e == cudaSuccess) e = upload(&t.bwd_pre_items, p.bwd_pre_items);
         if (e == cudaSuccess) e = upload(&t.conv_halo, p.conv_halo);
+        if (e == cudaSuccess) e = upload(&t.glr_spans, p.glr_spans);
         if (e == cudaSuccess) e = cudaMalloc((void **)&t.status, 64);
         if (e == cudaSuccess) e = cudaMemset(t.status, 0, 64);
         if (e == cudaSuccess) {

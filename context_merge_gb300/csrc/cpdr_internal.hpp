@@ -41,6 +41,18 @@ struct ConvTile {
     int32_t n, halo;
 };
 
+// Gated linear recurrence: one sequence (longest first).  Its tokens are row
+// coordinates start .. start + len - 1 of the batch row whose memory begins
+// at token `base`; its states before every kGlrGroup-th token are rows
+// group0 .. of the carry.
+constexpr int kGlrGroup = 16;
+struct GlrSpan {
+    int64_t base, start, len, group0;
+    int32_t seq, pad;
+};
+
+constexpr int kMaxNormWidth = 16384;   // widest row of the RMS norm
+
 // Bytes of the WY tiles of one (chunk, head): T' = T diag(beta), and
 // T'' = T diag(beta gamma) as a bf16 hi/lo pair, each a 64 x 64 bf16 tile
 // stored as the 128-byte-swizzled shared-memory image the MMA reads.
@@ -102,6 +114,8 @@ struct Plan {
     std::vector<ConvTile> conv_tiles;        // conv work units, fragment by fragment
     std::vector<int64_t> conv_halo;          // halo rows, conv_width - 1 memory positions each
     std::vector<int32_t> conv_pre_tokens;    // per segment: halo tokens inside its first sequence
+    std::vector<GlrSpan> glr_spans;          // every sequence, longest first
+    int64_t glr_groups = 0, glr_longest = 0; // carry rows of all sequences; tokens of the longest one
 
     int32_t nseg() const { return R * B; }
 };
@@ -124,6 +138,7 @@ struct DeviceTables {
     int32_t *host_items = nullptr;
     int32_t *bwd_pre_items = nullptr;
     int64_t *conv_halo = nullptr;
+    GlrSpan *glr_spans = nullptr;
     int32_t *status = nullptr;   // device status word (bounded waits)
 };
 
@@ -226,6 +241,26 @@ int launch_bwd(const cpdr_ctx *c, const void *q, const void *k, const void *v, c
                void *stream);
 int launch_conv1d(const cpdr_ctx *c, const void *x, const float *weight, const float *bias, int channels,
                   int activation, void *y, void *stream);
+// Multiprocessors of device `dev` (api.cpp).
+int device_sms(int dev);
+// Checks shared by the entry points (api.cpp): a context that can launch on
+// the current device; a 16-byte aligned pointer, NULL only where allowed.
+cpdr_status check_launch_ctx(const cpdr_ctx *c);
+cpdr_status check_device_ptr(const void *p, const char *name, bool nullable = false);
+cpdr_status check_launched(int rc, const char *what);
+// Gated linear recurrence (glr.cu).
+int launch_glr_fwd(const cpdr_ctx *c, const void *x, const float *g, const float *h0, int channels, void *y,
+                   float *hT, float *carry, void *stream);
+int launch_glr_bwd(const cpdr_ctx *c, const void *x, const float *g, const float *carry, const void *dy,
+                   const float *dhT, int channels, void *dx, float *dg, float *dh0, void *stream);
+int launch_glr_step(const cpdr_ctx *c, const void *x, const float *g, const float *state, float *state_out,
+                    const int32_t *slots, int n, int num_slots, int channels, void *y, void *stream);
+// RMS norm (rmsnorm.cu); part: rmsnorm_bwd_grid() x width floats.
+int launch_rmsnorm_fwd(const cpdr_ctx *c, int64_t rows, int width, const void *x, const void *residual,
+                       const float *weight, float eps, void *sum_out, void *y, void *y8, float *scale, void *stream);
+int rmsnorm_bwd_grid(const cpdr_ctx *c, int64_t rows, int width);
+int launch_rmsnorm_bwd(const cpdr_ctx *c, int64_t rows, int width, const void *s, const float *weight, float eps,
+                       const void *dy, const void *dsum, void *ds, float *dweight, float *part, void *stream);
 int launch_tc_fwd(const cpdr_ctx *c, const int32_t *items, int n_items, const void *q, const void *k, const void *v,
                   const float *g,
                   const void *wy, const float *S_init, void *o, float *final_state, void *stream);

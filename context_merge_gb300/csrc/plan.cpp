@@ -207,6 +207,15 @@ cpdr_status build_plan(const cpdr_desc &d, Plan &p, std::string &err) {
         acc += chunks(f.len);
     }
     p.frag_chunk0.back() = acc;
+    // whole sequences for the gated linear recurrence, longest first
+    for (int n = 0; n < p.N; n++) {
+        const int64_t base = p.packed ? 0 : (int64_t)n * p.T, len = p.cu[n + 1] - p.cu[n];
+        p.glr_spans.push_back(GlrSpan{base, p.cu[n] - base, len, p.glr_groups, n, 0});
+        p.glr_groups += (len + kGlrGroup - 1) / kGlrGroup;
+        p.glr_longest = std::max(p.glr_longest, len);
+    }
+    std::stable_sort(p.glr_spans.begin(), p.glr_spans.end(),
+                     [](const GlrSpan &a, const GlrSpan &b) { return a.len > b.len; });
     if (d.conv_width > 0) {
         for (size_t i = 0; i < p.frags.size(); i++) {
             const cpdr_fragment &f = p.frags[i];

@@ -305,6 +305,101 @@ cpdr_status cpdr_bwd(const cpdr_ctx *ctx, const void *q, const void *k, const vo
                      float *dq, float *dk, float *dv, float *dbeta, float *dgate, void *workspace,
                      size_t workspace_bytes, void *stream);
 
+/*
+ * Layer steps around the token mixers
+ * -----------------------------------
+ * The calls below are the steps a layer takes before, beside and after the
+ * delta rule (no counterpart in the article).  They take the context for its
+ * input dtype (and, for the recurrence, its sequences and token layout), its
+ * device and its status word.  Unlike cpdr_bwd, whose gradients are all fp32,
+ * the gradient of a tensor has the tensor's own type here, so that it feeds
+ * the step before it as it is.  Sums, statistics and states are fp32 and run
+ * in a fixed order: the same call on the same inputs gives the same bits.
+ * All tensors are contiguous; outputs must not overlap inputs or one another
+ * except where "in place" is said.  The calls allocate nothing, keep nothing
+ * between calls and can be captured into a graph; calls that share a
+ * workspace must not overlap on the GPU.
+ */
+
+/*
+ * Gated linear recurrence, the diagonal sibling of the delta rule: per
+ * channel c and token t of a sequence, with a_t = exp(gate_t),
+ *     h_t = a_t h_{t-1} + x_t,    y_t = h_t,
+ * from h0 (or zero) at the sequence's start; hT is the state behind its last
+ * token (h0, or zero, for an empty sequence).  gate is a natural-log gate of
+ * any finite value or -infinity (a_t = 0: the state is dropped); x and h0
+ * are finite.  Sequences and token layout are the context's (packed batches,
+ * zigzag); its segments play no part.
+ * Layout: x, y [B, T, channels] in the context's token order and input dtype;
+ * gate [B, T, channels] fp32; h0, hT [N, channels] fp32, either may be NULL
+ * (hT may be h0 itself); channels % 8 == 0.
+ * carry (NULL, or cpdr_glr_carry_bytes() bytes): what cpdr_glr_bwd needs of
+ * the forward, fp32 [groups, channels]: the state before every 16th token of
+ * each sequence (its tokens 0, 16, 32, ...), sequence after sequence.
+ */
+cpdr_status cpdr_glr_carry_bytes(const cpdr_ctx *ctx, int32_t channels, size_t *bytes);
+cpdr_status cpdr_glr_fwd(const cpdr_ctx *ctx, const void *x, const float *gate, const float *h0, int32_t channels,
+                         void *y, float *hT, float *carry, void *stream);
+
+/*
+ * Its backward: the gradients of  sum_t <dy_t, y_t> + sum_n <dhT_n, hT_n>,
+ *     dh_t = dy_t + a_{t+1} dh_{t+1}  (dhT in the place of the last product),
+ *     dx_t = dh_t,   dgate_t = dh_t a_t h_{t-1},   dh0 = a_0 dh_0.
+ * x, gate and carry as the forward took and left them; dy, dx [B, T,
+ * channels] in the input dtype; dgate [B, T, channels] fp32; dhT (NULL: zero)
+ * and dh0 (or NULL) [N, channels] fp32 (dh0 may be dhT itself).
+ */
+cpdr_status cpdr_glr_bwd(const cpdr_ctx *ctx, const void *x, const float *gate, const float *carry, const void *dy,
+                         const float *dhT, int32_t channels, void *dx, float *dgate, float *dh0, void *stream);
+
+/*
+ * Its single-token form, for decoding over a pool of state slots: row i of x,
+ * gate and y [n, channels] is the next token of the sequence whose state is
+ * slot slots[i] (int32, device; NULL: slot i) of state [num_slots, channels]
+ * fp32.  state_out gets the new states of the slots that occur; it may be
+ * state itself (in place), and its other slots are left as they were.  Rows
+ * whose slot is outside 0 .. num_slots - 1 (padding, -1) do nothing: their y
+ * is left as it was.  Rows of the same slot are consecutive tokens of its
+ * sequence, in row order.  0 <= n <= 65535.  The context's sequences play no
+ * part, only its dtype.
+ */
+cpdr_status cpdr_glr_step(const cpdr_ctx *ctx, const void *x, const float *gate, const float *state,
+                          float *state_out, const int32_t *slots, int32_t n, int32_t num_slots, int32_t channels,
+                          void *y, void *stream);
+
+/*
+ * RMS norm with the residual's addition.  Per row of `width` elements, with
+ * s = x + residual (s = x when residual is NULL),
+ *     y_i = s_i weight_i / sqrt(mean(s^2) + eps).
+ * x, residual, sum_out, y [rows, width] in the context's input dtype; weight
+ * [width] fp32.  sum_out (or NULL) receives s, rounded once; y is computed
+ * from the unrounded sum.  y8 and scale (both or neither; y may be NULL then,
+ * or given too): y in 8 bits, e4m3 [rows, width], with one fp32 scale per row,
+ *     scale = max(max_i |y_i| / 448, 2^-126),   y8_i = e4m3(y_i / scale),
+ * rounded to nearest even; a row with a NaN or an infinity has a NaN scale.
+ * sum_out and y may each be x or residual (in place; not both the same).
+ * rows >= 0, width % 8 == 0, width <= 16384, 0 <= eps <= 1.  A row is
+ * anything that is normalised as one: a token, or a head of d elements.
+ */
+cpdr_status cpdr_rmsnorm_fwd(const cpdr_ctx *ctx, int64_t rows, int32_t width, const void *x, const void *residual,
+                             const float *weight, float eps, void *sum_out, void *y, void *y8, float *scale,
+                             void *stream);
+
+/*
+ * Its backward, from s (sum_out, or x where there was no residual), dy and,
+ * unless NULL, the gradient dsum that reaches s past the norm:
+ *     ds_i = rstd (w_i dy_i - s_i rstd^2 mean(s w dy)) + dsum_i,
+ *     dweight_i = sum over rows of dy_i s_i rstd,   rstd = 1/sqrt(mean(s^2)+eps).
+ * ds is the gradient of x and of residual alike; it may be dy or dsum (in
+ * place).  dy, dsum, ds [rows, width] in the input dtype; dweight [width]
+ * fp32.  workspace: cpdr_rmsnorm_bwd_workspace_bytes() bytes, 16-byte
+ * aligned.
+ */
+cpdr_status cpdr_rmsnorm_bwd_workspace_bytes(const cpdr_ctx *ctx, int64_t rows, int32_t width, size_t *bytes);
+cpdr_status cpdr_rmsnorm_bwd(const cpdr_ctx *ctx, int64_t rows, int32_t width, const void *s, const float *weight,
+                             float eps, const void *dy, const void *dsum, void *ds, float *dweight, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
 /* pre_num_conv_tokens ([FLA-CP] §3.3) per segment, host memory: how many of
  * the W - 1 tokens before segment s's start belong to its first sequence
  * (0 when the segment starts a sequence), out[0 .. min(cap, nseg)). */
