@@ -26,8 +26,10 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "cpdr_internal.hpp"
+#include "tc_common.cuh"
 #include "vec_io.cuh"
 
 namespace cpdr {
@@ -37,11 +39,12 @@ using namespace vio;
 
 constexpr int kSlice = 64;                  // channels of a CTA
 constexpr int kMaxCluster = 8;
-constexpr int kStages = 2;                  // groups of a warp in shared memory: one in use, one on its way
+constexpr int kStages = 3;                  // groups of a warp in shared memory: going out, being mapped, on its way
 constexpr int kStepThreads = 256;
+// Warps of a CTA, one CTA per SM: what three stages leave room for.
+constexpr int kFwdWarps = 8;
 template <typename T>
-constexpr int kFwdWarps = sizeof(T) == 2 ? 8 : 4;
-constexpr int kBwdWarps = 4;
+constexpr int kBwdWarps = sizeof(T) == 2 ? 8 : 5;
 
 struct Params {
     const GlrSpan *spans;
@@ -56,6 +59,7 @@ struct Params {
     float *carry;               // forward
     int64_t L;                  // tokens per part of the zigzag layout
     int parts;                  // parts of the zigzag layout, 0 for the contiguous one
+    int32_t *status;            // the context's status word (bounded waits)
     int channels, slices;
 };
 
@@ -67,12 +71,16 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// 16 bytes into the same shared-memory place of CTA `rank` of the cluster.
-__device__ __forceinline__ void store_remote(const float4 *local, uint32_t rank, float4 v) {
-    const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(local));
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(r), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+// 16 bytes into the same shared-memory place of CTA `rank` of the cluster,
+// counted there by the same barrier.  (A plain store and the cluster's
+// barrier would need a release, which waits for the output's stores to global
+// memory too: measured 0.8 stalled warps per issue.)
+__device__ __forceinline__ void send(const float4 *place, uint64_t *bar, uint32_t rank, float4 v) {
+    uint32_t ra, rb;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(tc::smem_u32(place)), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rb) : "r"(tc::smem_u32(bar)), "r"(rank));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(ra),
+                 "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(rb)
                  : "memory");
 }
 
@@ -104,7 +112,7 @@ struct Rows {
 };
 
 __device__ __forceinline__ void cp_async16(void *dst, const void *src, bool ok) {
-    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    const uint32_t d = tc::smem_u32(dst);
     const int n = ok ? 16 : 0;   // 0: nothing is read, the 16 bytes become zero
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
 }
@@ -124,9 +132,18 @@ struct Tile {
     __device__ __forceinline__ void load(const Params &p, const Rows<ZIGZAG> &rows, const T *src, int c0, int n,
                                          int lane) {
         constexpr int E = 16 / (int)sizeof(T), CH = kSlice / E;   // elements of a copy, copies of a row
+        constexpr int PER = 32 / CH;                              // rows that a warp's copies cover at once
+        const int r0 = lane / CH, c = lane % CH * E;
+        if (!ZIGZAG && n == kGlrGroup && c0 + kSlice <= p.channels) {
+            // whole groups: one address per lane, the rest is the same for all lanes
+            const T *at = src + (rows.at(0) + r0) * p.channels + c0 + c;
 #pragma unroll
-        for (int i = 0; i < kGlrGroup * CH / 32; i++) {
-            const int row = (i * 32 + lane) / CH, c = (i * 32 + lane) % CH * E;
+            for (int i = 0; i < kGlrGroup / PER; i++) cp_async16(&v[i * PER + r0][c], at + i * PER * p.channels, true);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kGlrGroup / PER; i++) {
+            const int row = i * PER + r0;
             const bool ok = row < n && c0 + c < p.channels;
             const int64_t at = rows.at(row) * p.channels + c0 + c;
             cp_async16(&v[row][c], ok ? src + at : src, ok);
@@ -138,44 +155,75 @@ struct Tile {
 // the last to the first.
 template <int WARPS, bool REV>
 struct Exchange {
-    float4 group[WARPS][32];             // (A0, B0, A1, B1) of each group's channel pair
-    float4 cta[2][kMaxCluster][32];      // the same of each CTA of the cluster, by parity of the step
+    float4 grp[2][WARPS][32];            // (A0, B0, A1, B1) of each group's channel pair, by parity of the step
+    float4 cta[2][kMaxCluster][32];      // the same of each CTA of the cluster
 
-    // The value before this warp's group, from the value `carry` before the
-    // step, which becomes the value behind it.
-    __device__ __forceinline__ float2 step(int par, int w, int lane, uint32_t rank, uint32_t nz, float2 A, float2 B,
-                                           float2 &carry) {
-        // a cluster of one has no barrier between this step's reads and the
-        // next one's writes: it alternates between `group` and `cta`
-        float4(*grp)[32] = nz == 1 && par ? reinterpret_cast<float4(*)[32]>(&cta[0][0][0]) : group;
-        grp[w][lane] = make_float4(A.x, B.x, A.y, B.y);
+    uint64_t bar[2];                     // the CTAs' maps of a step have arrived, by parity
+    tc::Ctl ctl;
+
+    // The whole cluster calls it before the first step ...
+    __device__ __forceinline__ void open(uint32_t nz) {
+        if (nz == 1) return;
+        if (threadIdx.x == 0) {
+            ctl.abort = 0;
+            tc::mbar_init(&bar[0], 1);
+            tc::mbar_init(&bar[1], 1);
+        }
+        cluster_arrive();
+        cluster_wait();
+    }
+    // ... and behind the last: no CTA leaves while another may still send to it.
+    __device__ __forceinline__ void close(uint32_t nz) {
+        if (nz == 1) return;
+        cluster_arrive();
+        cluster_wait();
+    }
+
+    // First half: publishes this warp's map of step i; `before` becomes the
+    // map of the CTA's groups before it, `all` that of the whole CTA.  A CTA
+    // sends step i + 2 into the places of step i only when it has the maps of
+    // step i + 1 of every CTA, and a CTA sends those behind its
+    // __syncthreads, where all its warps have read step i.
+    __device__ __forceinline__ void publish(int par, int w, int lane, uint32_t rank, uint32_t nz, float2 A, float2 B,
+                                            float4 &before, float4 &all) {
+        // the next step writes the other half: its __syncthreads is behind this step's reads
+        grp[par][w][lane] = make_float4(A.x, B.x, A.y, B.y);
         __syncthreads();
-        // maps before this warp's group, and of the whole CTA
-        float4 f = make_float4(1.f, 0.f, 1.f, 0.f), before = f;
+        float4 f = make_float4(1.f, 0.f, 1.f, 0.f);
+        before = f;
 #pragma unroll
         for (int i = 0; i < WARPS; i++) {
             const int ww = REV ? WARPS - 1 - i : i;
             if (ww == w) before = f;
-            const float4 m = grp[ww][lane];
+            const float4 m = grp[par][ww][lane];
             f = make_float4(m.x * f.x, fmaf(m.x, f.y, m.y), m.z * f.z, fmaf(m.z, f.w, m.w));
         }
-        float2 start = carry;
+        all = f;
         if (nz > 1) {
-            for (uint32_t z = w; z < nz; z += WARPS) store_remote(&cta[par][rank][lane], z, f);
-            cluster_arrive();
-            cluster_wait();
+            if (threadIdx.x == 0) tc::mbar_arrive_expect_tx(&bar[par], nz * (uint32_t)sizeof(cta[0][0]));
+            for (uint32_t z = w; z < nz; z += WARPS) send(&cta[par][rank][lane], &bar[par], z, f);
+        }
+    }
+    // Second half: the value before this warp's group, from the value `carry`
+    // before the step, which becomes the value behind it.  `phase`: how often
+    // this parity's barrier has completed, modulo 2.
+    __device__ __forceinline__ float2 start(int par, uint32_t phase, int lane, uint32_t rank, uint32_t nz,
+                                            const float4 &before, const float4 &all, float2 &carry, int32_t *status) {
+        float2 s = carry;
+        if (nz > 1) {
+            tc::mbar_wait(&bar[par], phase, &ctl, status, REV ? 151 : 150);
             float2 v = carry;
             for (uint32_t i = 0; i < nz; i++) {
                 const uint32_t z = REV ? nz - 1 - i : i;
-                if (z == rank) start = v;
+                if (z == rank) s = v;
                 const float4 m = cta[par][z][lane];
                 v = make_float2(fmaf(m.x, v.x, m.y), fmaf(m.z, v.y, m.w));
             }
             carry = v;
         } else {
-            carry = make_float2(fmaf(f.x, carry.x, f.y), fmaf(f.z, carry.y, f.w));
+            carry = make_float2(fmaf(all.x, carry.x, all.y), fmaf(all.z, carry.y, all.w));
         }
-        return make_float2(fmaf(before.x, start.x, before.y), fmaf(before.z, start.y, before.w));
+        return make_float2(fmaf(before.x, s.x, before.y), fmaf(before.z, s.y, before.w));
     }
 };
 
@@ -202,9 +250,16 @@ constexpr int kPerSm = (228 * 1024) / ((int)sizeof(S) + 1024);
 
 extern __shared__ __align__(16) unsigned char smem[];
 
+// The loop of both directions, over cluster steps i: the maps of step i + 1
+// are taken and published, then step i's tokens run from their start and go
+// out while the cluster exchanges those maps, then step i + 3's copies start
+// into the place that step i leaves (so copies have a whole step and more to
+// arrive), and last the starts of step i + 1 follow from the exchanged maps.
+// A group's gates become a_t = exp(g_t) in place when its map is taken.
+//
 // grid: (span, channel slice) items x cluster CTAs; cluster (nz, 1, 1)
 template <typename T, int WARPS, bool ZIGZAG>
-__global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) glr_fwd_kernel(Params p, int nz) {
+__global__ void __launch_bounds__(32 * WARPS, 1) glr_fwd_kernel(Params p, int nz) {
     auto &sh = *reinterpret_cast<FwdShared<T, WARPS> *>(smem);
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = nz > 1 ? cluster_rank() : 0u;
@@ -216,56 +271,83 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) glr_fwd_kernel(Params 
     float2 carry = make_float2(0.f, 0.f);
     if (live && p.h0) carry = *reinterpret_cast<const float2 *>(p.h0 + (int64_t)sp.seq * p.channels + c);
     const int64_t step = (int64_t)nz * WARPS * kGlrGroup;
-    const int64_t mine = ((int64_t)rank * WARPS + w) * kGlrGroup;
-    auto tokens = [&](int64_t p0) { return (int)max((int64_t)0, min((int64_t)kGlrGroup, sp.len - p0)); };
-    auto fetch = [&](int64_t p0, int stage) {
-        const int n = tokens(p0);
-        const Rows<ZIGZAG> rows(p, sp, p0, lane);
+    int64_t p0 = ((int64_t)rank * WARPS + w) * kGlrGroup;   // this warp's first token of step i
+    auto tokens = [&](int64_t at) { return (int)max((int64_t)0, min((int64_t)kGlrGroup, sp.len - at)); };
+    auto fetch = [&](int64_t at, int stage) {
+        const Rows<ZIGZAG> rows(p, sp, at, lane);
+        const int n = tokens(at);
         auto &r = sh.ring[w][stage];
         r.x.load(p, rows, (const T *)p.x, c0, n, lane);
         r.g.load(p, rows, p.g, c0, n, lane);
         cp_commit();
     };
-    fetch(mine, 0);
-    int par = 0;
-    for (int64_t t0 = 0; t0 < sp.len; t0 += step, par ^= 1) {
-        const int64_t p0 = t0 + mine;
-        const int n = live ? tokens(p0) : 0;
-        fetch(p0 + step, par ^ 1);
-        cp_wait<1>();
-        __syncwarp();
-        const auto &r = sh.ring[w][par];
-        Raw2<T> xr[kGlrGroup];
-        float2 a[kGlrGroup];
+    float4 before, all;
+    auto map = [&](int stage, int par) {
+        auto &r = sh.ring[w][stage];
         float2 A = make_float2(1.f, 1.f), B = make_float2(0.f, 0.f);
 #pragma unroll
         for (int u = 0; u < kGlrGroup; u++) {
-            xr[u] = load2(&r.x.v[u][2 * lane]);
-            const float2 gv = *reinterpret_cast<const float2 *>(&r.g.v[u][2 * lane]);
-            a[u] = make_float2(expf(gv.x), expf(gv.y));   // behind the tokens g = 0: the state stays as it is
-            const float2 xv = widen(xr[u]);
-            A = make_float2(A.x * a[u].x, A.y * a[u].y);
-            B = make_float2(fmaf(a[u].x, B.x, xv.x), fmaf(a[u].y, B.y, xv.y));
+            const float2 xv = widen(load2(&r.x.v[u][2 * lane]));
+            float2 *g = reinterpret_cast<float2 *>(&r.g.v[u][2 * lane]);
+            const float2 a = make_float2(expf(g->x), expf(g->y));   // behind the tokens g = 0: the state stays
+            *g = a;
+            A = make_float2(A.x * a.x, A.y * a.y);
+            B = make_float2(fmaf(a.x, B.x, xv.x), fmaf(a.y, B.y, xv.y));
         }
-        float2 h = sh.ex.step(par, w, lane, rank, (uint32_t)nz, A, B, carry);
+        sh.ex.publish(par, w, lane, rank, (uint32_t)nz, A, B, before, all);
+    };
+    const int64_t steps = (sp.len + step - 1) / step;
+    float2 h = make_float2(0.f, 0.f);
+    sh.ex.open((uint32_t)nz);
+    if (steps > 0) {
+#pragma unroll
+        for (int s = 0; s < kStages; s++) fetch(p0 + s * step, s);
+        cp_wait<kStages - 1>();
+        __syncwarp();
+        map(0, 0);
+        h = sh.ex.start(0, 0, lane, rank, (uint32_t)nz, before, all, carry, p.status);
+    }
+    int stage = 0, par = 0;
+    for (int64_t i = 0; i < steps; i++, p0 += step) {
+        const int next = stage + 1 == kStages ? 0 : stage + 1;
+        if (i + 1 < steps) {
+            cp_wait<kStages - 2>();
+            __syncwarp();
+            map(next, par ^ 1);
+        }
+        const int n = live ? tokens(p0) : 0;
         if (n > 0 && p.carry)
             *reinterpret_cast<float2 *>(p.carry + (sp.group0 + p0 / kGlrGroup) * p.channels + c) = h;
         const Rows<ZIGZAG> rows(p, sp, p0, lane);
+        const auto &r = sh.ring[w][stage];
+        auto run = [&](auto whole) {
+            T *o = y + rows.at(0) * p.channels;
 #pragma unroll
-        for (int u = 0; u < kGlrGroup; u++) {
-            const float2 xv = widen(xr[u]);
-            h = make_float2(fmaf(a[u].x, h.x, xv.x), fmaf(a[u].y, h.y, xv.y));
-            const int64_t o = rows.at(u) * p.channels;
-            if (u < n) store2(y + o, h);
-        }
+            for (int u = 0; u < kGlrGroup; u++) {
+                const float2 xv = widen(load2(&r.x.v[u][2 * lane]));
+                const float2 a = *reinterpret_cast<const float2 *>(&r.g.v[u][2 * lane]);
+                h = make_float2(fmaf(a.x, h.x, xv.x), fmaf(a.y, h.y, xv.y));
+                if (ZIGZAG) o = y + rows.at(u) * p.channels;
+                if (decltype(whole)::value || u < n) store2(ZIGZAG ? o : o + u * p.channels, h);
+            }
+        };
+        if (!ZIGZAG && n == kGlrGroup) run(std::true_type());
+        else run(std::false_type());
+        __syncwarp();   // the group is read to the end before its place is filled again
+        fetch(p0 + kStages * step, stage);
+        stage = next;
+        par ^= 1;
+        if (i + 1 < steps)
+            h = sh.ex.start(par, (uint32_t)((i + 1) >> 1) & 1u, lane, rank, (uint32_t)nz, before, all, carry, p.status);
     }
     cp_wait<0>();
+    sh.ex.close((uint32_t)nz);
     if (live && p.hT && rank == 0 && w == 0)
         *reinterpret_cast<float2 *>(p.hT + (int64_t)sp.seq * p.channels + c) = carry;
 }
 
 template <typename T, int WARPS, bool ZIGZAG>
-__global__ void __launch_bounds__(32 * WARPS, 12 / WARPS) glr_bwd_kernel(Params p, int nz) {
+__global__ void __launch_bounds__(32 * WARPS, 1) glr_bwd_kernel(Params p, int nz) {
     auto &sh = *reinterpret_cast<BwdShared<T, WARPS> *>(smem);
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = nz > 1 ? cluster_rank() : 0u;
@@ -278,71 +360,100 @@ __global__ void __launch_bounds__(32 * WARPS, 12 / WARPS) glr_bwd_kernel(Params 
     float2 carry = make_float2(0.f, 0.f);
     if (live && p.h0) carry = *reinterpret_cast<const float2 *>(p.h0 + (int64_t)sp.seq * p.channels + c);
     const int64_t step = (int64_t)nz * WARPS * kGlrGroup;
-    const int64_t mine = ((int64_t)rank * WARPS + w) * kGlrGroup;
-    auto tokens = [&](int64_t p0) { return (int)max((int64_t)0, min((int64_t)kGlrGroup, sp.len - p0)); };
-    auto fetch = [&](int64_t p0, int stage) {
-        const int n = p0 < 0 ? 0 : tokens(p0);
-        const Rows<ZIGZAG> rows(p, sp, p0, lane);
+    const int64_t steps = (sp.len + step - 1) / step;
+    // this warp's first token of step i; below zero there is nothing
+    int64_t p0 = (steps - 1) * step + ((int64_t)rank * WARPS + w) * kGlrGroup;
+    auto tokens = [&](int64_t at) {
+        return at < 0 ? 0 : (int)max((int64_t)0, min((int64_t)kGlrGroup, sp.len - at));
+    };
+    auto fetch = [&](int64_t at, int stage) {
+        const Rows<ZIGZAG> rows(p, sp, at, lane);
+        const int n = tokens(at);
         auto &r = sh.ring[w][stage];
         r.x.load(p, rows, (const T *)p.x, c0, n, lane);
-        r.g.load(p, rows, p.g, c0, n, lane);
         r.dy.load(p, rows, (const T *)p.dy, c0, n, lane);
+        r.g.load(p, rows, p.g, c0, n, lane);
         cp_commit();
     };
-    const int64_t last = sp.len > 0 ? (sp.len - 1) / step * step : -1;
-    auto start_of = [&](int64_t p0) {
-        return live && p0 >= 0 && tokens(p0) > 0
-                   ? *reinterpret_cast<const float2 *>(p.carry_in + (sp.group0 + p0 / kGlrGroup) * p.channels + c)
+    // the state before the group's first token
+    auto kept = [&](int64_t at) {
+        return live && tokens(at) > 0
+                   ? *reinterpret_cast<const float2 *>(p.carry_in + (sp.group0 + at / kGlrGroup) * p.channels + c)
                    : make_float2(0.f, 0.f);
     };
-    float2 h_next = make_float2(0.f, 0.f);
-    if (last >= 0) {
-        fetch(last + mine, 0);
-        h_next = start_of(last + mine);
-    }
-    int par = 0;
-    for (int64_t t0 = last; t0 >= 0; t0 -= step, par ^= 1) {
-        const int64_t p0 = t0 + mine;
-        const int n = live ? tokens(p0) : 0;
-        float2 h = h_next;
-        // the step before this one; the first step has none (a position below zero: no rows)
-        fetch(t0 >= step ? p0 - step : -1, par ^ 1);
-        h_next = start_of(t0 >= step ? p0 - step : -1);
-        cp_wait<1>();
-        __syncwarp();
-        const auto &r = sh.ring[w][par];
-        float2 a[kGlrGroup], hp[kGlrGroup];
+    float4 before, all;
+    auto map = [&](int stage, int par) {
+        auto &r = sh.ring[w][stage];
         float2 A = make_float2(1.f, 1.f), B = make_float2(0.f, 0.f);
 #pragma unroll
+        for (int u = kGlrGroup - 1; u >= 0; u--) {
+            const float2 d = widen(load2(&r.dy.v[u][2 * lane]));
+            float2 *g = reinterpret_cast<float2 *>(&r.g.v[u][2 * lane]);
+            const float2 a = make_float2(expf(g->x), expf(g->y));
+            *g = a;
+            A = make_float2(A.x * a.x, A.y * a.y);
+            B = make_float2(a.x * (d.x + B.x), a.y * (d.y + B.y));
+        }
+        sh.ex.publish(par, w, lane, rank, (uint32_t)nz, A, B, before, all);
+    };
+    float2 q = make_float2(0.f, 0.f), h = q, h_next = q;
+    sh.ex.open((uint32_t)nz);
+    if (steps > 0) {
+#pragma unroll
+        for (int s = 0; s < kStages; s++) fetch(p0 - s * step, s);
+        h = kept(p0);
+        cp_wait<kStages - 1>();
+        __syncwarp();
+        map(0, 0);
+        q = sh.ex.start(0, 0, lane, rank, (uint32_t)nz, before, all, carry, p.status);
+    }
+    int stage = 0, par = 0;
+    for (int64_t i = 0; i < steps; i++, p0 -= step) {
+        const int next = stage + 1 == kStages ? 0 : stage + 1;
+        h_next = kept(p0 - step);
+        if (i + 1 < steps) {
+            cp_wait<kStages - 2>();
+            __syncwarp();
+            map(next, par ^ 1);
+        }
+        const int n = live ? tokens(p0) : 0;
+        const Rows<ZIGZAG> rows(p, sp, p0, lane);
+        const auto &r = sh.ring[w][stage];
+        float2 a[kGlrGroup], hp[kGlrGroup];
+#pragma unroll
         for (int u = 0; u < kGlrGroup; u++) {
-            const float2 gv = *reinterpret_cast<const float2 *>(&r.g.v[u][2 * lane]);
             const float2 xv = widen(load2(&r.x.v[u][2 * lane]));
-            a[u] = make_float2(expf(gv.x), expf(gv.y));
+            a[u] = *reinterpret_cast<const float2 *>(&r.g.v[u][2 * lane]);
             hp[u] = h;
             h = make_float2(fmaf(a[u].x, h.x, xv.x), fmaf(a[u].y, h.y, xv.y));
-            A = make_float2(A.x * a[u].x, A.y * a[u].y);
         }
+        auto run = [&](auto whole) {
+            const int64_t first = rows.at(0) * p.channels;
 #pragma unroll
-        for (int u = kGlrGroup - 1; u >= 0; u--) {
-            const float2 d = widen(load2(&r.dy.v[u][2 * lane]));
-            B = make_float2(a[u].x * (d.x + B.x), a[u].y * (d.y + B.y));
-        }
-        float2 q = sh.ex.step(par, w, lane, rank, (uint32_t)nz, A, B, carry);
-        const Rows<ZIGZAG> rows(p, sp, p0, lane);
-#pragma unroll
-        for (int u = kGlrGroup - 1; u >= 0; u--) {
-            const float2 d = widen(load2(&r.dy.v[u][2 * lane]));
-            const float2 dh = make_float2(d.x + q.x, d.y + q.y);
-            q = make_float2(a[u].x * dh.x, a[u].y * dh.y);
-            const int64_t o = rows.at(u) * p.channels;
-            if (u < n) {
-                store2(dx + o, dh);
-                *reinterpret_cast<float2 *>(dg + o) = make_float2(q.x * hp[u].x, q.y * hp[u].y);
+            for (int u = kGlrGroup - 1; u >= 0; u--) {
+                const float2 d = widen(load2(&r.dy.v[u][2 * lane]));
+                const float2 dh = make_float2(d.x + q.x, d.y + q.y);
+                q = make_float2(a[u].x * dh.x, a[u].y * dh.y);
+                const int64_t o = ZIGZAG ? rows.at(u) * p.channels : first;
+                const int more = ZIGZAG ? 0 : u * p.channels;
+                if (decltype(whole)::value || u < n) {
+                    store2(dx + o + more, dh);
+                    *reinterpret_cast<float2 *>(dg + o + more) = make_float2(q.x * hp[u].x, q.y * hp[u].y);
+                }
             }
-        }
-        __syncwarp();   // the group's dy is read to the end before its place is filled again
+        };
+        if (!ZIGZAG && n == kGlrGroup) run(std::true_type());
+        else run(std::false_type());
+        __syncwarp();   // the group is read to the end before its place is filled again
+        fetch(p0 - kStages * step, stage);
+        stage = next;
+        par ^= 1;
+        h = h_next;
+        if (i + 1 < steps)
+            q = sh.ex.start(par, (uint32_t)((i + 1) >> 1) & 1u, lane, rank, (uint32_t)nz, before, all, carry, p.status);
     }
     cp_wait<0>();
+    sh.ex.close((uint32_t)nz);
     if (live && p.hT && rank == 0 && w == 0)
         *reinterpret_cast<float2 *>(p.hT + (int64_t)sp.seq * p.channels + c) = carry;
 }
@@ -398,6 +509,7 @@ template <typename K>
 int launch(const cpdr_ctx *c, K kernel, int warps, int per_sm, size_t bytes, Params p, void *stream) {
     const auto &pl = c->plan;
     p.spans = c->dev.glr_spans;
+    p.status = c->dev.status;
     p.L = pl.L;
     p.parts = (pl.flags & CPDR_FLAG_LAYOUT_ZIGZAG) ? pl.R : 0;
     p.slices = (p.channels + kSlice - 1) / kSlice;
@@ -420,15 +532,19 @@ int launch(const cpdr_ctx *c, K kernel, int warps, int per_sm, size_t bytes, Par
     return (int)cudaLaunchKernelEx(&cfg, kernel, p, nz);
 }
 
+static_assert(sizeof(FwdShared<float, kFwdWarps>) <= 227 * 1024 && sizeof(BwdShared<float, kBwdWarps<float>>) <= 227 * 1024 &&
+                  sizeof(BwdShared<__nv_bfloat16, kBwdWarps<__nv_bfloat16>>) <= 227 * 1024,
+              "a CTA's stages fit its shared memory");
+
 template <typename T>
 int fwd(const cpdr_ctx *c, const Params &p, void *stream) {
-    constexpr int W = kFwdWarps<T>;
+    constexpr int W = kFwdWarps;
     auto kernel = c->plan.flags & CPDR_FLAG_LAYOUT_ZIGZAG ? glr_fwd_kernel<T, W, true> : glr_fwd_kernel<T, W, false>;
     return launch(c, kernel, W, kPerSm<FwdShared<T, W>>, sizeof(FwdShared<T, W>), p, stream);
 }
 template <typename T>
 int bwd(const cpdr_ctx *c, const Params &p, void *stream) {
-    constexpr int W = kBwdWarps;
+    constexpr int W = kBwdWarps<T>;
     auto kernel = c->plan.flags & CPDR_FLAG_LAYOUT_ZIGZAG ? glr_bwd_kernel<T, W, true> : glr_bwd_kernel<T, W, false>;
     return launch(c, kernel, W, kPerSm<BwdShared<T, W>>, sizeof(BwdShared<T, W>), p, stream);
 }

@@ -59,6 +59,7 @@ size_t elem_bytes(const cpdr_ctx *c) { return c->plan.in_dtype == CPDR_DTYPE_F32
 cpdr_status check_channels(const char *what, int32_t channels) {
     if (channels < 1 || channels % 8 != 0)
         return fail_with(CPDR_ERR_INVALID, std::string(what) + ": channels must be a positive multiple of 8");
+    if (channels > (1 << 24)) return fail_with(CPDR_ERR_UNSUPPORTED, std::string(what) + ": channels are at most 2^24");
     return CPDR_OK;
 }
 
