@@ -71,16 +71,59 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
+// Both channels of a lane in one instruction (round to nearest, as the scalar forms).
+__device__ __forceinline__ uint64_t pair(float2 v) { return *reinterpret_cast<uint64_t *>(&v); }
+__device__ __forceinline__ float2 unpair(uint64_t r) { return *reinterpret_cast<float2 *>(&r); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)), "l"(pair(c)));
+    return unpair(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)));
+    return unpair(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)));
+    return unpair(r);
+}
+
+// exp(g) = 2^t (1 + e ln 2) with t = g log2(e) rounded and e = g log2(e) - t,
+// which the fused product gives exactly: 2^t alone would be off by |g| half
+// steps.  Gates below -128 (and -infinity) give 2^-185, flushed to zero; a
+// NaN stays one.  Eight instructions for two gates, where expf takes about
+// seventeen.
+__device__ __forceinline__ float2 exp2_of_gate(float2 g) {
+    constexpr float kL = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
+    asm("max.NaN.f32 %0, %0, 0fC3000000;" : "+f"(g.x));   // -128
+    asm("max.NaN.f32 %0, %0, 0fC3000000;" : "+f"(g.y));
+    const float2 t = mul2(g, make_float2(kL, kL));
+    const float2 e = fma2(g, make_float2(-kL, -kL), t);   // minus the rest
+    float2 r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(t.y));
+    return fma2(mul2(r, make_float2(-kLn2, -kLn2)), e, r);
+}
+
+// A pair of maps h -> A h + B.
+struct Map {
+    float2 A, B;
+};
+__device__ __forceinline__ float2 apply(const Map &m, float2 h) { return fma2(m.A, h, m.B); }
+__device__ __forceinline__ Map after(const Map &m, const Map &f) { return Map{mul2(m.A, f.A), fma2(m.A, f.B, m.B)}; }
+
 // 16 bytes into the same shared-memory place of CTA `rank` of the cluster,
 // counted there by the same barrier.  (A plain store and the cluster's
 // barrier would need a release, which waits for the output's stores to global
 // memory too: measured 0.8 stalled warps per issue.)
-__device__ __forceinline__ void send(const float4 *place, uint64_t *bar, uint32_t rank, float4 v) {
+__device__ __forceinline__ void send(const Map *place, uint64_t *bar, uint32_t rank, const Map &v) {
     uint32_t ra, rb;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(tc::smem_u32(place)), "r"(rank));
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rb) : "r"(tc::smem_u32(bar)), "r"(rank));
     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(ra),
-                 "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(rb)
+                 "f"(v.A.x), "f"(v.A.y), "f"(v.B.x), "f"(v.B.y), "r"(rb)
                  : "memory");
 }
 
@@ -155,10 +198,10 @@ struct Tile {
 // the last to the first.
 template <int WARPS, bool REV>
 struct Exchange {
-    float4 grp[2][WARPS][32];            // (A0, B0, A1, B1) of each group's channel pair, by parity of the step
-    float4 cta[2][kMaxCluster][32];      // the same of each CTA of the cluster
+    Map grp[2][WARPS][32];          // each group's, for every channel pair, by parity of the step
+    Map cta[2][kMaxCluster][32];    // each CTA's of the cluster
+    uint64_t bar[2];                // the CTAs' maps of a step have arrived, by parity
 
-    uint64_t bar[2];                     // the CTAs' maps of a step have arrived, by parity
     tc::Ctl ctl;
 
     // The whole cluster calls it before the first step ...
@@ -184,19 +227,18 @@ struct Exchange {
     // sends step i + 2 into the places of step i only when it has the maps of
     // step i + 1 of every CTA, and a CTA sends those behind its
     // __syncthreads, where all its warps have read step i.
-    __device__ __forceinline__ void publish(int par, int w, int lane, uint32_t rank, uint32_t nz, float2 A, float2 B,
-                                            float4 &before, float4 &all) {
+    __device__ __forceinline__ void publish(int par, int w, int lane, uint32_t rank, uint32_t nz, const Map &m,
+                                            Map &before, Map &all) {
         // the next step writes the other half: its __syncthreads is behind this step's reads
-        grp[par][w][lane] = make_float4(A.x, B.x, A.y, B.y);
+        grp[par][w][lane] = m;
         __syncthreads();
-        float4 f = make_float4(1.f, 0.f, 1.f, 0.f);
+        Map f{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
         before = f;
 #pragma unroll
         for (int i = 0; i < WARPS; i++) {
             const int ww = REV ? WARPS - 1 - i : i;
             if (ww == w) before = f;
-            const float4 m = grp[par][ww][lane];
-            f = make_float4(m.x * f.x, fmaf(m.x, f.y, m.y), m.z * f.z, fmaf(m.z, f.w, m.w));
+            f = after(grp[par][ww][lane], f);
         }
         all = f;
         if (nz > 1) {
@@ -208,7 +250,7 @@ struct Exchange {
     // before the step, which becomes the value behind it.  `phase`: how often
     // this parity's barrier has completed, modulo 2.
     __device__ __forceinline__ float2 start(int par, uint32_t phase, int lane, uint32_t rank, uint32_t nz,
-                                            const float4 &before, const float4 &all, float2 &carry, int32_t *status) {
+                                            const Map &before, const Map &all, float2 &carry, int32_t *status) {
         float2 s = carry;
         if (nz > 1) {
             tc::mbar_wait(&bar[par], phase, &ctl, status, REV ? 151 : 150);
@@ -216,14 +258,13 @@ struct Exchange {
             for (uint32_t i = 0; i < nz; i++) {
                 const uint32_t z = REV ? nz - 1 - i : i;
                 if (z == rank) s = v;
-                const float4 m = cta[par][z][lane];
-                v = make_float2(fmaf(m.x, v.x, m.y), fmaf(m.z, v.y, m.w));
+                v = apply(cta[par][z][lane], v);
             }
             carry = v;
         } else {
-            carry = make_float2(fmaf(all.x, carry.x, all.y), fmaf(all.z, carry.y, all.w));
+            carry = apply(all, carry);
         }
-        return make_float2(fmaf(before.x, s.x, before.y), fmaf(before.z, s.y, before.w));
+        return apply(before, s);
     }
 };
 
@@ -281,20 +322,19 @@ __global__ void __launch_bounds__(32 * WARPS, 1) glr_fwd_kernel(Params p, int nz
         r.g.load(p, rows, p.g, c0, n, lane);
         cp_commit();
     };
-    float4 before, all;
+    Map before, all;
     auto map = [&](int stage, int par) {
         auto &r = sh.ring[w][stage];
-        float2 A = make_float2(1.f, 1.f), B = make_float2(0.f, 0.f);
+        Map m{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int u = 0; u < kGlrGroup; u++) {
             const float2 xv = widen(load2(&r.x.v[u][2 * lane]));
             float2 *g = reinterpret_cast<float2 *>(&r.g.v[u][2 * lane]);
-            const float2 a = make_float2(expf(g->x), expf(g->y));   // behind the tokens g = 0: the state stays
+            const float2 a = exp2_of_gate(*g);   // behind the tokens g = 0: the state stays
             *g = a;
-            A = make_float2(A.x * a.x, A.y * a.y);
-            B = make_float2(fmaf(a.x, B.x, xv.x), fmaf(a.y, B.y, xv.y));
+            m = after(Map{a, xv}, m);
         }
-        sh.ex.publish(par, w, lane, rank, (uint32_t)nz, A, B, before, all);
+        sh.ex.publish(par, w, lane, rank, (uint32_t)nz, m, before, all);
     };
     const int64_t steps = (sp.len + step - 1) / step;
     float2 h = make_float2(0.f, 0.f);
@@ -326,7 +366,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) glr_fwd_kernel(Params p, int nz
             for (int u = 0; u < kGlrGroup; u++) {
                 const float2 xv = widen(load2(&r.x.v[u][2 * lane]));
                 const float2 a = *reinterpret_cast<const float2 *>(&r.g.v[u][2 * lane]);
-                h = make_float2(fmaf(a.x, h.x, xv.x), fmaf(a.y, h.y, xv.y));
+                h = fma2(a, h, xv);
                 if (ZIGZAG) o = y + rows.at(u) * p.channels;
                 if (decltype(whole)::value || u < n) store2(ZIGZAG ? o : o + u * p.channels, h);
             }
@@ -381,20 +421,19 @@ __global__ void __launch_bounds__(32 * WARPS, 1) glr_bwd_kernel(Params p, int nz
                    ? *reinterpret_cast<const float2 *>(p.carry_in + (sp.group0 + at / kGlrGroup) * p.channels + c)
                    : make_float2(0.f, 0.f);
     };
-    float4 before, all;
+    Map before, all;
     auto map = [&](int stage, int par) {
         auto &r = sh.ring[w][stage];
-        float2 A = make_float2(1.f, 1.f), B = make_float2(0.f, 0.f);
+        Map m{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int u = kGlrGroup - 1; u >= 0; u--) {
             const float2 d = widen(load2(&r.dy.v[u][2 * lane]));
             float2 *g = reinterpret_cast<float2 *>(&r.g.v[u][2 * lane]);
-            const float2 a = make_float2(expf(g->x), expf(g->y));
+            const float2 a = exp2_of_gate(*g);
             *g = a;
-            A = make_float2(A.x * a.x, A.y * a.y);
-            B = make_float2(a.x * (d.x + B.x), a.y * (d.y + B.y));
+            m = Map{mul2(m.A, a), mul2(a, add2(d, m.B))};
         }
-        sh.ex.publish(par, w, lane, rank, (uint32_t)nz, A, B, before, all);
+        sh.ex.publish(par, w, lane, rank, (uint32_t)nz, m, before, all);
     };
     float2 q = make_float2(0.f, 0.f), h = q, h_next = q;
     sh.ex.open((uint32_t)nz);
@@ -425,20 +464,20 @@ __global__ void __launch_bounds__(32 * WARPS, 1) glr_bwd_kernel(Params p, int nz
             const float2 xv = widen(load2(&r.x.v[u][2 * lane]));
             a[u] = *reinterpret_cast<const float2 *>(&r.g.v[u][2 * lane]);
             hp[u] = h;
-            h = make_float2(fmaf(a[u].x, h.x, xv.x), fmaf(a[u].y, h.y, xv.y));
+            h = fma2(a[u], h, xv);
         }
         auto run = [&](auto whole) {
             const int64_t first = rows.at(0) * p.channels;
 #pragma unroll
             for (int u = kGlrGroup - 1; u >= 0; u--) {
                 const float2 d = widen(load2(&r.dy.v[u][2 * lane]));
-                const float2 dh = make_float2(d.x + q.x, d.y + q.y);
-                q = make_float2(a[u].x * dh.x, a[u].y * dh.y);
+                const float2 dh = add2(d, q);
+                q = mul2(a[u], dh);
                 const int64_t o = ZIGZAG ? rows.at(u) * p.channels : first;
                 const int more = ZIGZAG ? 0 : u * p.channels;
                 if (decltype(whole)::value || u < n) {
                     store2(dx + o + more, dh);
-                    *reinterpret_cast<float2 *>(dg + o + more) = make_float2(q.x * hp[u].x, q.y * hp[u].y);
+                    *reinterpret_cast<float2 *>(dg + o + more) = mul2(q, hp[u]);
                 }
             }
         };
@@ -489,7 +528,7 @@ glr_step_kernel(const T *__restrict__ x, const float *__restrict__ g, const floa
         const int64_t o = (int64_t)j * channels + c;
         const float2 gv = *reinterpret_cast<const float2 *>(g + o);
         const float2 xv = widen(load2(x + o));
-        h = make_float2(fmaf(expf(gv.x), h.x, xv.x), fmaf(expf(gv.y), h.y, xv.y));
+        h = fma2(exp2_of_gate(gv), h, xv);
         store2(y + o, h);
         if (!more) break;
     }
