@@ -41,8 +41,11 @@ constexpr int kSlice = 64;                  // channels of a CTA
 constexpr int kMaxCluster = 8;
 constexpr int kStages = 3;                  // groups of a warp in shared memory: going out, being mapped, on its way
 constexpr int kStepThreads = 256;
-// Warps of a CTA, one CTA per SM: what three stages leave room for.
-constexpr int kFwdWarps = 8;
+// Warps of a CTA.  Forward: two CTAs of four per SM, whose steps hide one
+// another's (262144 x 2048 bf16, one sequence: 732 us; one CTA of eight:
+// 790; two of five: 755; two stages: 985).  Backward: one CTA of what the
+// stages leave room for (packed 65536 x 2048 bf16: 313 us; two of four: 319).
+constexpr int kFwdWarps = 4;
 template <typename T>
 constexpr int kBwdWarps = sizeof(T) == 2 ? 8 : 5;
 
@@ -300,7 +303,7 @@ extern __shared__ __align__(16) unsigned char smem[];
 //
 // grid: (span, channel slice) items x cluster CTAs; cluster (nz, 1, 1)
 template <typename T, int WARPS, bool ZIGZAG>
-__global__ void __launch_bounds__(32 * WARPS, 1) glr_fwd_kernel(Params p, int nz) {
+__global__ void __launch_bounds__(32 * WARPS, 2) glr_fwd_kernel(Params p, int nz) {
     auto &sh = *reinterpret_cast<FwdShared<T, WARPS> *>(smem);
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = nz > 1 ? cluster_rank() : 0u;
@@ -535,12 +538,19 @@ glr_step_kernel(const T *__restrict__ x, const float *__restrict__ g, const floa
     *reinterpret_cast<float2 *>(state_out + so) = h;
 }
 
-// CTAs of a cluster: as many as keep the items' clusters within what runs at
-// once, and no more than the longest sequence has tiles.
-int pick_cluster(const cpdr_ctx *c, int64_t items, int tile, int per_sm) {
-    const int64_t room = (int64_t)per_sm * device_sms(c->device);
+// CTAs of a cluster.  One CTA's share of the longest sequence should be no
+// more than half of what a CTA slot gets of all tokens, or it runs alone in
+// the end (packed 65536 x 2048 in 12 ragged sequences, backward: 308 us; all
+// of it 316, a quarter 340; 313 with a cluster of one); and a cluster has no
+// more CTAs than that sequence has tiles.
+int pick_cluster(const cpdr_ctx *c, int slices, int tile, int per_sm) {
+    const auto &pl = c->plan;
+    const int64_t slots = (int64_t)per_sm * device_sms(c->device);
+    const int64_t tokens = (int64_t)pl.B * pl.T;
     int z = 1;
-    while (z < kMaxCluster && items * 2 * z <= room && c->plan.glr_longest > (int64_t)z * tile) z *= 2;
+    while (z < kMaxCluster && pl.glr_longest > (int64_t)z * tile &&
+           (double)pl.glr_longest / z > 0.5 * (double)tokens * slices / (double)slots)
+        z *= 2;
     return z;
 }
 
@@ -553,7 +563,7 @@ int launch(const cpdr_ctx *c, K kernel, int warps, int per_sm, size_t bytes, Par
     p.parts = (pl.flags & CPDR_FLAG_LAYOUT_ZIGZAG) ? pl.R : 0;
     p.slices = (p.channels + kSlice - 1) / kSlice;
     const int64_t items = (int64_t)pl.glr_spans.size() * p.slices;
-    const int nz = pick_cluster(c, items, warps * kGlrGroup, per_sm);
+    const int nz = pick_cluster(c, p.slices, warps * kGlrGroup, per_sm);
     if (items * nz > (int64_t)0x7fffffff) return (int)cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return (int)e;
