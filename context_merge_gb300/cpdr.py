@@ -31,7 +31,11 @@ EXPORTED = ["cpdr_ctx_create", "cpdr_ctx_destroy", "cpdr_buffer_sizes", "cpdr_pl
             "cpdr_forward_host", "cpdr_forward_noalloc", "cpdr_check_device_status", "cpdr_selftest_wait_timeout",
             "cpdr_conv1d_fwd", "cpdr_plan_conv_tokens", "cpdr_bwd_workspace_bytes", "cpdr_bwd",
             "cpdr_glr_carry_bytes", "cpdr_glr_fwd", "cpdr_glr_bwd", "cpdr_glr_step", "cpdr_rmsnorm_fwd",
-            "cpdr_rmsnorm_bwd_workspace_bytes", "cpdr_rmsnorm_bwd", "cpdr_last_error", "cpdr_version"]
+            "cpdr_rmsnorm_bwd_workspace_bytes", "cpdr_rmsnorm_bwd", "cpdr_linear_fwd",
+            "cpdr_linear_bwd_workspace_bytes", "cpdr_linear_bwd", "cpdr_last_error", "cpdr_version"]
+
+
+ACTIVATIONS = {None: 0, "none": 0, "silu": 1, "gelu": 2}
 
 
 class CpdrError(RuntimeError):
@@ -95,6 +99,9 @@ def load():
         lib.cpdr_rmsnorm_fwd.argtypes = [vp, i64, i32, vp, vp, vp, f32] + [vp] * 5
         lib.cpdr_rmsnorm_bwd_workspace_bytes.argtypes = [vp, i64, i32, ctypes.POINTER(sz)]
         lib.cpdr_rmsnorm_bwd.argtypes = [vp, i64, i32, vp, vp, f32] + [vp] * 5 + [sz, vp]
+        lib.cpdr_linear_fwd.argtypes = [vp, i64, i32, i32] + [vp] * 5 + [i32] + [vp] * 4
+        lib.cpdr_linear_bwd_workspace_bytes.argtypes = [vp, i64, i32, i32, i32, ctypes.POINTER(sz)]
+        lib.cpdr_linear_bwd.argtypes = [vp, i64, i32, i32] + [vp] * 4 + [i32] + [vp] * 4 + [sz, vp]
         lib.cpdr_check_device_status.argtypes = [vp, vp]
         lib.cpdr_selftest_wait_timeout.argtypes = [vp, ctypes.c_longlong, vp]
         for name in EXPORTED:
@@ -479,6 +486,65 @@ class Context:
                                           _ptr(out["ds"]), _ptr(out["dweight"]), _ptr(workspace),
                                           ctypes.c_size_t(workspace.numel() * workspace.element_size()),
                                           _stream(stream)))
+        return out
+
+    # ---- matrix product with its epilogue ----------------------------------
+    def linear_fwd(self, x, w, y, bias=None, activation=None, residual=None, z=None, x_scale=None, w_scale=None,
+                   stream=None):
+        """y = act(x w^T + bias) + residual over the last axis of x: x [.., K]
+        and w [N, K] bf16, or float8_e4m3fn with ``x_scale`` [..] and
+        ``w_scale`` [N]; y, residual and z (the value before the activation)
+        [.., N] bf16; bias [N] fp32; activation None, "silu" or "gelu"."""
+        rows, K = self._rows(x)
+        dev, f32, bf16 = x.device, torch.float32, torch.bfloat16
+        it = bf16 if x_scale is None else torch.float8_e4m3fn
+        if w.dim() != 2:
+            raise ValueError(f"w must be a [N, {K}] tensor, got {list(w.shape)}")
+        N = w.shape[0]
+        out = (*x.shape[:-1], N)
+        _check_tensor("x", x, x.shape, it, dev)
+        _check_tensor("w", w, (N, K), it, dev)
+        _check_tensor("x_scale", x_scale, x.shape[:-1], f32, dev, True)
+        _check_tensor("w_scale", w_scale, (N,), f32, dev, True)
+        _check_tensor("bias", bias, (N,), f32, dev, True)
+        _check_tensor("residual", residual, out, bf16, dev, True)
+        _check_tensor("z", z, out, bf16, dev, True)
+        _check_tensor("y", y, out, bf16, dev)
+        _check(self._lib.cpdr_linear_fwd(self._h, rows, K, N, _ptr(x), _ptr(w), _ptr(x_scale), _ptr(w_scale),
+                                         _ptr(bias), ACTIVATIONS[activation], _ptr(residual), _ptr(z), _ptr(y),
+                                         _stream(stream)))
+
+    def linear_bwd_workspace_bytes(self, rows, K, N, activation=None):
+        n = ctypes.c_size_t()
+        _check(self._lib.cpdr_linear_bwd_workspace_bytes(self._h, int(rows), int(K), int(N), ACTIVATIONS[activation],
+                                                         ctypes.byref(n)))
+        return n.value
+
+    def linear_bwd(self, x, w, dy, z=None, activation=None, out=None, workspace=None, stream=None):
+        """Gradients from dy [.., N] (also the residual's): a dict of dx and dw
+        (bf16) and dbias (fp32).  Of a given ``out`` only the entries that it
+        holds are computed."""
+        rows, K = self._rows(x)
+        N = w.shape[0]
+        dev, bf16 = x.device, torch.bfloat16
+        _check_tensor("x", x, x.shape, bf16, dev)
+        _check_tensor("w", w, (N, K), bf16, dev)
+        _check_tensor("dy", dy, (*x.shape[:-1], N), bf16, dev)
+        _check_tensor("z", z, dy.shape, bf16, dev, ACTIVATIONS[activation] == 0)
+        if out is None:
+            out = dict(dx=torch.empty_like(x), dw=torch.empty_like(w),
+                       dbias=torch.empty(N, dtype=torch.float32, device=dev))
+        _check_tensor("dx", out.get("dx"), x.shape, bf16, dev, True)
+        _check_tensor("dw", out.get("dw"), w.shape, bf16, dev, True)
+        _check_tensor("dbias", out.get("dbias"), (N,), torch.float32, dev, True)
+        if workspace is None:
+            workspace = torch.empty(self.linear_bwd_workspace_bytes(rows, K, N, activation), dtype=torch.uint8,
+                                    device=dev)
+        _check(self._lib.cpdr_linear_bwd(self._h, rows, K, N, _ptr(x), _ptr(w), _ptr(z), _ptr(dy),
+                                         ACTIVATIONS[activation], _ptr(out.get("dx")), _ptr(out.get("dw")),
+                                         _ptr(out.get("dbias")), _ptr(workspace),
+                                         ctypes.c_size_t(workspace.numel() * workspace.element_size()),
+                                         _stream(stream)))
         return out
 
     def check_device_status(self, stream=None):

@@ -255,6 +255,16 @@ int launch_glr_bwd(const cpdr_ctx *c, const void *x, const float *g, const float
                    const float *dhT, int channels, void *dx, float *dg, float *dh0, void *stream);
 int launch_glr_step(const cpdr_ctx *c, const void *x, const float *g, const float *state, float *state_out,
                     const int32_t *slots, int n, int num_slots, int channels, void *y, void *stream);
+// out[col] = sum over parts of part[:, col] (rmsnorm.cu).
+int launch_column_sums(const float *part, int nparts, int width, float *out, void *stream);
+// Matrix product with its epilogue (linear.cu).  dz: rows x N bf16 (where
+// there is an activation); part: linear_dz_parts() x N floats (for dbias).
+int launch_linear_fwd(const cpdr_ctx *c, int64_t rows, int K, int N, const void *x, const void *w, const float *x_scale,
+                      const float *w_scale, const float *bias, int act, const void *residual, void *z, void *y,
+                      void *stream);
+size_t linear_dz_parts(const cpdr_ctx *c, int64_t rows, int N);
+int launch_linear_bwd(const cpdr_ctx *c, int64_t rows, int K, int N, const void *x, const void *w, const void *z,
+                      const void *dy, int act, void *dx, void *dw, float *dbias, void *dz, float *part, void *stream);
 // RMS norm (rmsnorm.cu); part: rmsnorm_bwd_grid() x width floats.
 int launch_rmsnorm_fwd(const cpdr_ctx *c, int64_t rows, int width, const void *x, const void *residual,
                        const float *weight, float eps, void *sum_out, void *y, void *y8, float *scale, void *stream);

@@ -1,6 +1,8 @@
 // C-ABI layer of the layer steps around the token mixers: the gated linear
-// recurrence and the RMS norm.  Argument validation and dispatch; contracts
+// recurrence, the RMS norm and the matrix product.  Argument validation and dispatch; contracts
 // in include/cpdr.h.
+#include <cuda_runtime.h>
+
 #include <cstdint>
 #include <initializer_list>
 #include <string>
@@ -71,6 +73,29 @@ cpdr_status check_norm(const char *what, int64_t rows, int32_t width, float eps)
         return fail_with(CPDR_ERR_UNSUPPORTED, std::string(what) + ": width is at most 16384");
     if (!(eps >= 0.f) || eps > 1.f) return fail_with(CPDR_ERR_INVALID, std::string(what) + ": eps must be in [0, 1]");
     return CPDR_OK;
+}
+
+size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
+
+cpdr_status check_linear(const char *what, const cpdr_ctx *c, int64_t rows, int32_t K, int32_t N, int32_t act, bool e4m3) {
+    if (c->plan.in_dtype != CPDR_DTYPE_BF16)
+        return fail_with(CPDR_ERR_UNSUPPORTED, std::string(what) + ": only bf16 contexts (the products run on the tensor cores)");
+    if (rows < 0 || rows > (int64_t)INT32_MAX - 512)
+        return fail_with(CPDR_ERR_INVALID, std::string(what) + ": rows must be 0 .. 2^31 - 513");
+    const int mult = e4m3 ? 16 : 8;
+    if (K < 1 || K % mult != 0)
+        return fail_with(CPDR_ERR_INVALID, std::string(what) + ": K must be a positive multiple of " + std::to_string(mult));
+    if (N < 1 || N % 8 != 0) return fail_with(CPDR_ERR_INVALID, std::string(what) + ": N must be a positive multiple of 8");
+    if (K > (1 << 24) || N > (1 << 24)) return fail_with(CPDR_ERR_UNSUPPORTED, std::string(what) + ": K and N are at most 2^24");
+    if (act < 0 || act > 2)
+        return fail_with(CPDR_ERR_INVALID, std::string(what) + ": activation must be 0 (none), 1 (SiLU) or 2 (GELU)");
+    return CPDR_OK;
+}
+
+// The backward's workspace: dz (with an activation), then the row blocks' column sums.
+size_t linear_dz_bytes(int64_t rows, int32_t N, int32_t act) { return act ? round256((size_t)rows * (size_t)N * 2) : 0; }
+size_t linear_workspace(const cpdr_ctx *c, int64_t rows, int32_t N, int32_t act) {
+    return linear_dz_bytes(rows, N, act) + cpdr::linear_dz_parts(c, rows, N) * (size_t)N * sizeof(float);
 }
 
 size_t norm_workspace(const cpdr_ctx *c, int64_t rows, int width) {
@@ -208,6 +233,72 @@ cpdr_status cpdr_rmsnorm_bwd(const cpdr_ctx *c, int64_t rows, int32_t width, con
                            {{ds, dy}, {ds, dsum}}));
     return check_launched(cpdr::launch_rmsnorm_bwd(c, rows, width, s, weight, eps, dy, dsum, ds, dweight, (float *)ws, stream),
                           "cpdr_rmsnorm_bwd");
+}
+
+cpdr_status cpdr_linear_fwd(const cpdr_ctx *c, int64_t rows, int32_t K, int32_t N, const void *x, const void *w,
+                            const float *x_scale, const float *w_scale, const float *bias, int32_t activation,
+                            const void *residual, void *z, void *y, void *stream) {
+    CPDR_TRY(check_launch_ctx(c));
+    if ((x_scale == nullptr) != (w_scale == nullptr) && rows > 0)
+        return fail_with(CPDR_ERR_INVALID, "cpdr_linear_fwd: x_scale and w_scale come together");
+    const bool e4m3 = w_scale != nullptr;
+    CPDR_TRY(check_linear("cpdr_linear_fwd", c, rows, K, N, activation, e4m3));
+    if (rows == 0) return CPDR_OK;
+    CPDR_TRY(check_device_ptr(x, "x"));
+    CPDR_TRY(check_device_ptr(w, "w"));
+    CPDR_TRY(check_device_ptr(x_scale, "x_scale", true));
+    CPDR_TRY(check_device_ptr(w_scale, "w_scale", true));
+    CPDR_TRY(check_device_ptr(bias, "bias", true));
+    CPDR_TRY(check_device_ptr(residual, "residual", true));
+    CPDR_TRY(check_device_ptr(z, "z", true));
+    CPDR_TRY(check_device_ptr(y, "y"));
+    const size_t es = e4m3 ? 1 : 2, ny = (size_t)rows * (size_t)N * 2;
+    CPDR_TRY(check_outputs("cpdr_linear_fwd", {{y, ny, "y"}, {z, ny, "z"}},
+                           {{x, (size_t)rows * (size_t)K * es, "x"}, {w, (size_t)N * (size_t)K * es, "w"},
+                            {x_scale, (size_t)rows * 4, "x_scale"}, {w_scale, (size_t)N * 4, "w_scale"},
+                            {bias, (size_t)N * 4, "bias"}, {residual, ny, "residual"}},
+                           {{y, residual}}));
+    return check_launched(cpdr::launch_linear_fwd(c, rows, K, N, x, w, x_scale, w_scale, bias, activation, residual, z, y, stream),
+                          "cpdr_linear_fwd");
+}
+
+cpdr_status cpdr_linear_bwd_workspace_bytes(const cpdr_ctx *c, int64_t rows, int32_t K, int32_t N, int32_t activation,
+                                            size_t *bytes) {
+    CPDR_TRY(check_launch_ctx(c));
+    if (!bytes) return fail_with(CPDR_ERR_INVALID, "null argument");
+    CPDR_TRY(check_linear("cpdr_linear_bwd_workspace_bytes", c, rows, K, N, activation, false));
+    *bytes = linear_workspace(c, rows, N, activation);
+    return CPDR_OK;
+}
+
+cpdr_status cpdr_linear_bwd(const cpdr_ctx *c, int64_t rows, int32_t K, int32_t N, const void *x, const void *w,
+                            const void *z, const void *dy, int32_t activation, void *dx, void *dw, float *dbias,
+                            void *ws, size_t ws_bytes, void *stream) {
+    CPDR_TRY(check_launch_ctx(c));
+    CPDR_TRY(check_linear("cpdr_linear_bwd", c, rows, K, N, activation, false));
+    const bool none = rows == 0;
+    CPDR_TRY(check_device_ptr(x, "x", none || !dw));
+    CPDR_TRY(check_device_ptr(w, "w", !dx));
+    CPDR_TRY(check_device_ptr(z, "z", none || activation == 0));
+    CPDR_TRY(check_device_ptr(dy, "dy", none));
+    CPDR_TRY(check_device_ptr(dx, "dx", true));
+    CPDR_TRY(check_device_ptr(dw, "dw", true));
+    CPDR_TRY(check_device_ptr(dbias, "dbias", true));
+    const size_t need = linear_workspace(c, rows, N, activation);
+    CPDR_TRY(check_device_ptr(ws, "workspace", need == 0));
+    if (ws_bytes < need) return fail_with(CPDR_ERR_WORKSPACE, "cpdr_linear_bwd: workspace too small");
+    const size_t nx = (size_t)rows * (size_t)K * 2, nw = (size_t)N * (size_t)K * 2, ny = (size_t)rows * (size_t)N * 2;
+    CPDR_TRY(check_outputs("cpdr_linear_bwd", {{dx, nx, "dx"}, {dw, nw, "dw"}, {dbias, (size_t)N * 4, "dbias"}, {ws, need, "workspace"}},
+                           {{x, nx, "x"}, {w, nw, "w"}, {activation ? z : nullptr, ny, "z"}, {dy, ny, "dy"}}));
+    if (none) {   // sums over no rows
+        cudaStream_t st = (cudaStream_t)stream;
+        cudaError_t e = dw ? cudaMemsetAsync(dw, 0, nw, st) : cudaSuccess;
+        if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, (size_t)N * 4, st);
+        return check_launched((int)e, "cpdr_linear_bwd: zero fill");
+    }
+    float *part = (float *)((char *)ws + linear_dz_bytes(rows, N, activation));
+    return check_launched(cpdr::launch_linear_bwd(c, rows, K, N, x, w, z, dy, activation, dx, dw, dbias, ws, part, stream),
+                          "cpdr_linear_bwd");
 }
 
 }  // extern "C"

@@ -1,0 +1,751 @@
+// Matrix product with bias, activation and residual in its epilogue,
+//     y = act(x w^T + bias) + residual,
+// and its gradients  dz = dy act'(z),  dx = dz w,  dw = dz^T x,
+// dbias = sum over rows of dz.  Operands are bf16, or (forward) e4m3 with one
+// scale per row of x and one per row of w; products are accumulated in fp32
+// in tensor memory and rounded once, behind the epilogue (dz is rounded to
+// bf16 before the two gradient products: it is an operand of the tensor
+// cores there; dbias is summed from the unrounded values).
+//
+// All of them are one product D[p, q] = sum_r A[p, r] B[q, r], whose operands
+// lie in memory either along r (K-major: x, w, and dz for dx) or along p or q
+// (MN-major: w for dx, dz and x for dw); the tensor maps and descriptors
+// differ, nothing is transposed or copied.
+//
+// Two kernels:
+//  * wide_kernel, bound by the tensor cores: pairs of CTAs (cta_group::2) own
+//    256 x 256 tiles.  Per 128 bytes of r each CTA fetches 128 rows of A and
+//    128 of B, 32 KiB per 512 tensor-core cycles: half of what a single CTA
+//    with a 128 x 256 tile would draw from the L2, which could not keep up.
+//    Six stages of TMA loads, one issuing thread, two accumulators of 256
+//    TMEM columns, so that eight epilogue warps empty one while the other
+//    fills; outputs leave through swizzled staging tiles by TMA, which also
+//    cuts what lies outside the matrix.
+//  * narrow_kernel, for few rows of x, bound by reading w: 128 rows of w (the
+//    128 lanes) by 16 to 128 rows of x (the columns) per CTA, with r split
+//    over a cluster of up to 8 CTAs, whose partial sums meet in distributed
+//    shared memory in the order of the CTAs.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "cpdr_internal.hpp"
+#include "tc_common.cuh"
+#include "vec_io.cuh"
+
+namespace cpdr {
+namespace {
+
+using namespace tc;
+
+constexpr int kRBytes = 128;   // bytes of r in a stage: 64 bf16 or 128 e4m3
+
+struct Epilogue {
+    const float *bias;       // [q] or NULL
+    const float *xs, *ws;    // scales of e4m3 rows, or NULL
+    const __nv_bfloat16 *residual;   // [p, q] or NULL
+    int act;                 // 0 none, 1 SiLU, 2 GELU
+    int has_z;               // the value before the activation is an output too
+};
+
+struct Args {
+    Epilogue e;
+    int64_t P, Q;            // rows and columns of D
+    int blocks;              // stages of r
+    int tiles_p, tiles_q;
+    __nv_bfloat16 *y, *z;    // narrow_kernel
+    int32_t *status;
+};
+
+// ------------------------------------------------------------------ helpers
+__device__ __forceinline__ uint32_t ctarank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The shared-memory address of the same place in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t remote(const void *p, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Tile load {x, y}, completing on the barrier at cluster address `bar`.
+template <int GROUP>
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x, int y) {
+    if (GROUP == 2)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
+            "{%3, %4}], [%2];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+            "[%2];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y)
+            : "memory");
+}
+__device__ __forceinline__ void tma_store(const CUtensorMap *m, uint32_t src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)),
+                 "r"(src), "r"(x), "r"(y)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
+template <int GROUP, bool E4M3>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    if (GROUP == 2 && !E4M3)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+    else if (GROUP == 2)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+    else if (!E4M3)
+        mma_bf16(d, a, b, idesc, acc);
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+// Arrives, when all products issued so far are done, on the barrier at this
+// place in both CTAs of the pair.
+__device__ __forceinline__ void commit_pair(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// Instruction descriptor: fp32 accumulator; bf16 (format 1) or e4m3 (format 0) operands.
+template <bool E4M3, bool A_MN, bool B_MN>
+__host__ __device__ constexpr uint32_t idesc_of(int M, int N) {
+    return (1u << 4) | ((E4M3 ? 0u : 1u) << 7) | ((E4M3 ? 0u : 1u) << 10) | ((A_MN ? 1u : 0u) << 15) |
+           ((B_MN ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// An operand's stage of 128 rows (or of `rows` rows, K-major) by 128 bytes of
+// r, 128-byte swizzle.  K-major: rows of 128 bytes, a 32-byte step of r is 32
+// bytes on.  MN-major: two columns of 64 rows by 64 r, 8 KiB apart, a step of
+// 16 r is 2 KiB on.
+template <bool MN>
+__device__ __forceinline__ uint64_t stage_desc(uint32_t addr) {
+    return MN ? sdesc(addr, 8192, 1024) : sdesc(addr, 16, 1024);
+}
+template <bool MN>
+constexpr uint64_t kStep = MN ? 2048 >> 4 : 32 >> 4;
+template <int GROUP, bool MN, bool E4M3>
+__device__ __forceinline__ void load_stage(uint32_t dst, const CUtensorMap *m, uint32_t bar, int row, int block) {
+    const int r = block * (E4M3 ? 128 : 64);
+    if (MN) {
+        tma_load<GROUP>(dst, m, bar, row, r);
+        tma_load<GROUP>(dst + 8192, m, bar, row + 64, r);
+    } else {
+        tma_load<GROUP>(dst, m, bar, r, row);
+    }
+}
+
+// SiLU z sigmoid(z); the fast divide returns 0 once the denominator passes
+// 2^126, where the exact quotient is below 1e-36.  GELU z Phi(z), by erf.
+__device__ __forceinline__ float act_of(float z, int act) {
+    if (act == 1) return __fdividef(z, 1.f + __expf(-z));
+    if (act == 2) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+    return z;
+}
+__device__ __forceinline__ float act_grad(float z, int act) {
+    if (act == 1) {
+        const float s = __fdividef(1.f, 1.f + __expf(-z));
+        return s * fmaf(z, 1.f - s, 1.f);
+    }
+    const float phi = 0.39894228040143268f * __expf(-0.5f * z * z);
+    return fmaf(z, phi, 0.5f * (1.f + erff(z * 0.70710678118654752f)));
+}
+
+// ------------------------------------------------------------------ wide
+constexpr int kTile = 256;               // rows and columns of a pair's tile
+constexpr int kWideStages = 6;
+constexpr int kHalfStage = 128 * kRBytes;
+constexpr int kWideStage = 2 * kHalfStage;
+constexpr int kEpiWarps = 8;
+constexpr int kStaging = 32 * 128;       // a warp's 32 rows of 64 bf16
+constexpr int kWideThreads = 32 * (kEpiWarps + 2);
+constexpr size_t kWideBytes = (size_t)kWideStages * kWideStage + kEpiWarps * kStaging + 256 + 1024;
+static_assert(kWideBytes <= 227 * 1024, "a CTA's stages and staging fit its shared memory");
+
+struct WideBars {
+    uint64_t full[kWideStages], empty[kWideStages], acc_full[2], acc_empty[2];
+    Ctl ctl;
+    uint32_t tmem;
+};
+static_assert(sizeof(WideBars) <= 256, "barriers");
+
+// Tiles in groups of 8 rows of tiles, column by column inside a group, so
+// that the tiles that run together share their operands in the L2.
+__device__ __forceinline__ void tile_at(const Args &a, int i, int &tp, int &tq) {
+    const int per = 8 * a.tiles_q, g = i / per, r = i - g * per;
+    const int rows = min(8, a.tiles_p - 8 * g);
+    tq = r / rows;
+    tp = 8 * g + (r - tq * rows);
+}
+
+template <bool E4M3, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(kWideThreads, 1)
+wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
+            const __grid_constant__ CUtensorMap my, const __grid_constant__ CUtensorMap mz, Args a) {
+    extern __shared__ unsigned char raw[];
+    unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    unsigned char *staging = base + kWideStages * kWideStage;
+    WideBars &b = *reinterpret_cast<WideBars *>(staging + kEpiWarps * kStaging);
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = ctarank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, tiles = a.tiles_p * a.tiles_q;
+    if (threadIdx.x == 0) {
+        b.ctl.abort = 0;
+        for (int s = 0; s < kWideStages; s++) {
+            mbar_init(&b.full[s], 1);
+            mbar_init(&b.empty[s], 1);
+        }
+        for (int s = 0; s < 2; s++) {
+            mbar_init(&b.acc_full[s], 1);
+            mbar_init(&b.acc_empty[s], 2 * kEpiWarps);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (w == 8) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&b.tmem)), "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = b.tmem;
+
+    if (w == kEpiWarps) {
+        // -------------------------------------------------------- loads
+        if (lane == 0) {
+            tma_prefetch_desc(&ma);
+            tma_prefetch_desc(&mb);
+            uint32_t full0 = remote(&b.full[0], 0);
+            int it = 0;
+            for (int t = pair; t < tiles && !b.ctl.abort; t += pairs) {
+                int tp, tq;
+                tile_at(a, t, tp, tq);
+                const int p0 = tp * kTile + (int)rank * 128, q0 = tq * kTile + (int)rank * 128;
+                for (int k = 0; k < a.blocks; k++, it++) {
+                    const int s = it % kWideStages;
+                    if (!mbar_wait(&b.empty[s], (uint32_t)(it / kWideStages + 1) & 1u, &b.ctl, a.status, 160)) break;
+                    if (rank == 0) mbar_arrive_expect_tx(&b.full[s], 2 * kWideStage);
+                    const uint32_t dst = smem_u32(base + s * kWideStage), bar = full0 + 8u * s;
+                    load_stage<2, A_MN, E4M3>(dst, &ma, bar, p0, k);
+                    load_stage<2, B_MN, E4M3>(dst + kHalfStage, &mb, bar, q0, k);
+                }
+            }
+        }
+    } else if (w == kEpiWarps + 1) {
+        // -------------------------------------------------------- products
+        if (rank == 0 && lane == 0) {
+            constexpr uint32_t id = idesc_of<E4M3, A_MN, B_MN>(256, 256);
+            const uint64_t ad = stage_desc<A_MN>(smem_u32(base)), bd = stage_desc<B_MN>(smem_u32(base + kHalfStage));
+            int it = 0, n = 0;
+            for (int t = pair; t < tiles && !b.ctl.abort; t += pairs, n++) {
+                const int acc = n & 1;
+                if (!mbar_wait(&b.acc_empty[acc], (uint32_t)((n >> 1) + 1) & 1u, &b.ctl, a.status, 161)) break;
+                tc_fence_after();
+                for (int k = 0; k < a.blocks; k++, it++) {
+                    const int s = it % kWideStages;
+                    if (!mbar_wait(&b.full[s], (uint32_t)(it / kWideStages) & 1u, &b.ctl, a.status, 162)) break;
+                    tc_fence_after();
+                    const uint64_t so = (uint64_t)(s * kWideStage) >> 4;
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        mma<2, E4M3>(tmem + acc * 256, ad + so + j * kStep<A_MN>, bd + so + j * kStep<B_MN>, id,
+                                     (k | j) ? 1u : 0u);
+                    commit_pair(&b.empty[s]);
+                }
+                commit_pair(&b.acc_full[acc]);
+            }
+        }
+    } else {
+        // -------------------------------------------------------- epilogue
+        // warp w: TMEM lanes (rows) 32 (w % 4) .. + 31, columns 128 (w / 4) .. + 127, 64 at a time
+        const int quad = w & 3, half = w >> 2;
+        unsigned char *mine = staging + w * kStaging;
+        const uint32_t empty0 = remote(&b.acc_empty[0], 0);
+        int n = 0;
+        for (int t = pair; t < tiles; t += pairs, n++) {
+            const int acc = n & 1;
+            int tp, tq;
+            tile_at(a, t, tp, tq);
+            const int64_t p0 = (int64_t)tp * kTile + rank * 128 + quad * 32, p = p0 + lane;
+            const bool row = p < a.P;
+            const float xs = a.e.xs && row ? a.e.xs[p] : 1.f;
+            if (!warp_wait_all(&b.acc_full[acc], (uint32_t)(n >> 1) & 1u, &b.ctl, a.status, 163)) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int ch = 0; ch < 2; ch++) {
+                const int col = half * 128 + ch * 64;
+                const int64_t q0 = (int64_t)tq * kTile + col;
+                float v[2][32];
+                const uint32_t at = tmem + acc * 256 + col + ((uint32_t)(32 * quad) << 16);
+                tmem_ld32(at, v[0]);
+                tmem_ld32(at + 32, v[1]);
+                tmem_ld_wait();
+                if (ch == 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_remote(empty0 + 8u * acc);
+                }
+                if (p0 >= a.P || q0 >= a.Q) continue;
+#pragma unroll
+                for (int g = 0; g < 8; g++) {
+                    float *u = &v[g >> 2][(g & 3) * 8];
+                    const int64_t q = q0 + 8 * g;
+                    const bool in = q < a.Q;   // Q % 8 == 0
+                    if (a.e.ws) {
+                        float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f), s1 = s0;
+                        if (in) {
+                            s0 = *reinterpret_cast<const float4 *>(a.e.ws + q);
+                            s1 = *reinterpret_cast<const float4 *>(a.e.ws + q + 4);
+                        }
+                        u[0] *= xs * s0.x; u[1] *= xs * s0.y; u[2] *= xs * s0.z; u[3] *= xs * s0.w;
+                        u[4] *= xs * s1.x; u[5] *= xs * s1.y; u[6] *= xs * s1.z; u[7] *= xs * s1.w;
+                    }
+                    if (a.e.bias && in) {
+                        const float4 s0 = *reinterpret_cast<const float4 *>(a.e.bias + q);
+                        const float4 s1 = *reinterpret_cast<const float4 *>(a.e.bias + q + 4);
+                        u[0] += s0.x; u[1] += s0.y; u[2] += s0.z; u[3] += s0.w;
+                        u[4] += s1.x; u[5] += s1.y; u[6] += s1.z; u[7] += s1.w;
+                    }
+                }
+                auto put = [&](const CUtensorMap *m) {
+                    if (lane == 0) tma_store_wait();   // the staging tile has been read
+                    __syncwarp();
+#pragma unroll
+                    for (int g = 0; g < 8; g++) {
+                        const float *u = &v[g >> 2][(g & 3) * 8];
+                        *reinterpret_cast<uint4 *>(mine + sw128(lane, g)) =
+                            make_uint4(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]), pack_bf16(u[4], u[5]), pack_bf16(u[6], u[7]));
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) tma_store(m, smem_u32(mine), (int)q0, (int)p0);
+                };
+                if (a.e.has_z) put(&mz);
+                if (a.e.act) {
+#pragma unroll
+                    for (int i = 0; i < 64; i++) v[i >> 5][i & 31] = act_of(v[i >> 5][i & 31], a.e.act);
+                }
+                if (a.e.residual && row) {
+                    const __nv_bfloat16 *res = a.e.residual + p * a.Q + q0;
+#pragma unroll
+                    for (int g = 0; g < 8; g++) {
+                        if (q0 + 8 * g >= a.Q) break;
+                        float r[8];
+                        vio::widen16(vio::load16(res + 8 * g), r);
+#pragma unroll
+                        for (int i = 0; i < 8; i++) v[g >> 2][(g & 3) * 8 + i] += r[i];
+                    }
+                }
+                put(&my);
+            }
+        }
+        if (lane == 0) tma_store_wait();
+    }
+    __syncwarp();
+    // After a wait that gave up, copies of this CTA may still be on their way.
+    if (b.ctl.abort)
+        for (int i = 0; i < 1000; i++) __nanosleep(1000);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    if (w == 8) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+}
+
+// ------------------------------------------------------------------ narrow
+constexpr int kNarrowThreads = 32 * 6;
+constexpr int kMaxSplit = 8;
+template <int QN>
+constexpr int kNarrowStage = (128 + QN) * kRBytes;
+template <int QN>
+constexpr int kNarrowStages = (200 * 1024) / kNarrowStage<QN> < 12 ? (200 * 1024) / kNarrowStage<QN> : 12;
+template <int QN>
+constexpr size_t kNarrowBytes = (size_t)kNarrowStages<QN> * kNarrowStage<QN> + 512 + 1024;
+static_assert(kNarrowBytes<16> <= 227 * 1024 && kNarrowBytes<128> <= 227 * 1024, "stages fit");
+static_assert(128 * 128 * 4 <= kNarrowStages<128> * kNarrowStage<128> && 128 * 64 * 4 <= kNarrowStages<64> * kNarrowStage<64>,
+              "the partial sums fit the stages' place");
+
+struct NarrowBars {
+    uint64_t full[12], empty[12], done;
+    Ctl ctl;
+    uint32_t tmem;
+};
+static_assert(sizeof(NarrowBars) <= 512, "barriers");
+
+// D here is transposed: lanes are rows of w (q of y), columns rows of x (p of
+// y).  grid: (split, tiles of 128 rows of w, tiles of QN rows of x), cluster (split, 1, 1)
+template <int QN, bool E4M3, bool A_MN>
+__global__ void __launch_bounds__(kNarrowThreads, 1)
+narrow_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx, Args a) {
+    constexpr int STAGES = kNarrowStages<QN>, STAGE = kNarrowStage<QN>;
+    constexpr int COLS = QN < 32 ? 32 : QN;
+    extern __shared__ unsigned char raw[];
+    unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    NarrowBars &b = *reinterpret_cast<NarrowBars *>(base + STAGES * STAGE);
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = gridDim.x, rank = blockIdx.x;
+    const int64_t q0 = (int64_t)blockIdx.y * 128, p0 = (int64_t)blockIdx.z * QN;
+    const int k0 = (int)((int64_t)a.blocks * rank / split), k1 = (int)((int64_t)a.blocks * (rank + 1) / split);
+    if (threadIdx.x == 0) {
+        b.ctl.abort = 0;
+        for (int s = 0; s < STAGES; s++) {
+            mbar_init(&b.full[s], 1);
+            mbar_init(&b.empty[s], 1);
+        }
+        mbar_init(&b.done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (w == 5) {
+        tmem_alloc(&b.tmem, COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = b.tmem;
+    bool ok = true;
+    float v[QN];
+    if (w == 4) {
+        if (lane == 0) {
+            int it = 0;
+            for (int k = k0; k < k1; k++, it++) {
+                const int s = it % STAGES;
+                if (!mbar_wait(&b.empty[s], (uint32_t)(it / STAGES + 1) & 1u, &b.ctl, a.status, 170)) break;
+                mbar_arrive_expect_tx(&b.full[s], STAGE);
+                const uint32_t dst = smem_u32(base + s * STAGE), bar = smem_u32(&b.full[s]);
+                load_stage<1, A_MN, E4M3>(dst, &mw, bar, (int)q0, k);
+                load_stage<1, false, E4M3>(dst + 128 * kRBytes, &mx, bar, (int)p0, k);
+            }
+        }
+        __syncwarp();
+    } else if (w == 5) {
+        if (lane == 0) {
+            constexpr uint32_t id = idesc_of<E4M3, A_MN, false>(128, QN);
+            const uint64_t ad = stage_desc<A_MN>(smem_u32(base)), bd = stage_desc<false>(smem_u32(base + 128 * kRBytes));
+            int it = 0;
+            for (int k = k0; k < k1; k++, it++) {
+                const int s = it % STAGES;
+                if (!mbar_wait(&b.full[s], (uint32_t)(it / STAGES) & 1u, &b.ctl, a.status, 171)) break;
+                tc_fence_after();
+                const uint64_t so = (uint64_t)(s * STAGE) >> 4;
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    mma<1, E4M3>(tmem, ad + so + j * kStep<A_MN>, bd + so + j * kStep<false>, id, (it | j) ? 1u : 0u);
+                mma_commit(&b.empty[s]);
+            }
+            mma_commit(&b.done);
+        }
+        __syncwarp();
+    } else {
+        ok = warp_wait_all(&b.done, 0, &b.ctl, a.status, 172);
+        tc_fence_after();
+        const uint32_t at = tmem + ((uint32_t)(32 * w) << 16);
+#pragma unroll
+        for (int i = 0; i < QN; i += 16) tmem_ld16(at + i, *reinterpret_cast<float(*)[16]>(&v[i]));
+        tmem_ld_wait();
+    }
+    // the stages are free: every load was waited for by the products, and
+    // those by `done` (after a wait that gave up: time to land instead)
+    if (b.ctl.abort)
+        for (int i = 0; i < 1000; i++) __nanosleep(1000);
+    const int row = threadIdx.x;   // of the 128 rows of w, threads 0 .. 127
+    const int64_t q = q0 + row;
+    float *part = reinterpret_cast<float *>(base);   // [QN][128]
+    if (split > 1) {
+        __syncthreads();
+        if (w < 4) {
+#pragma unroll
+            for (int i = 0; i < QN; i++) part[i * 128 + row] = v[i];
+        }
+        cluster_sync();
+    }
+    if (w < 4 && q < a.Q && ok) {
+        const float bias = a.e.bias ? a.e.bias[q] : 0.f, ws = a.e.ws ? a.e.ws[q] : 1.f;
+        auto out = [&](int i, float d) {
+            const int64_t p = p0 + i;
+            if (p >= a.P) return;
+            if (a.e.ws) d *= a.e.xs[p] * ws;
+            if (a.e.bias) d += bias;
+            const int64_t o = p * a.Q + q;
+            if (a.e.has_z) a.z[o] = __float2bfloat16_rn(d);
+            d = act_of(d, a.e.act);
+            if (a.e.residual) d += __bfloat162float(a.e.residual[o]);
+            a.y[o] = __float2bfloat16_rn(d);
+        };
+        if (split > 1) {
+            // this CTA's share of the columns, summed in the order of the CTAs
+            const int i1 = QN * (rank + 1) / split;
+            for (int i = QN * rank / split; i < i1 && p0 + i < a.P; i++) {
+                float d = 0.f;
+                for (int z = 0; z < split; z++) {
+                    float t;
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(t) : "r"(remote(&part[i * 128 + row], z)));
+                    d += t;
+                }
+                out(i, d);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < QN; i++) out(i, v[i]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (split > 1) cluster_sync();   // no CTA leaves while another may read its sums
+    tc_fence_after();
+    if (w == 5) tmem_dealloc(tmem, COLS);
+}
+
+// ------------------------------------------------------------------ dz
+// dz = dy act'(z), rounded once, and its column sums over blocks of rows
+// (from the unrounded values).  A block is 256 columns by `per` rows, a
+// thread 8 columns of every 8th row.
+__global__ void __launch_bounds__(256)
+dz_kernel(const __nv_bfloat16 *__restrict__ dy, const __nv_bfloat16 *__restrict__ z, int act, int64_t rows, int width,
+          int per, __nv_bfloat16 *__restrict__ dz, float *__restrict__ part) {
+    __shared__ float sh[8][256];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int col = blockIdx.y * 256 + tx * 8;
+    const int64_t r0 = (int64_t)blockIdx.x * per, r1 = min(rows, r0 + per);
+    float sum[8] = {};
+    if (col < width) {
+#pragma unroll 4
+        for (int64_t r = r0 + ty; r < r1; r += 8) {
+            float d[8];
+            vio::widen16(vio::load16(dy + r * width + col), d);
+            if (act) {
+                float u[8];
+                vio::widen16(vio::load16(z + r * width + col), u);
+#pragma unroll
+                for (int i = 0; i < 8; i++) d[i] *= act_grad(u[i], act);
+                vio::store16(dz + r * width + col, d);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; i++) sum[i] += d[i];
+        }
+    }
+    if (!part) return;
+#pragma unroll
+    for (int i = 0; i < 8; i++) sh[ty][tx * 8 + i] = sum[i];
+    __syncthreads();
+    const int c = blockIdx.y * 256 + threadIdx.x;
+    if (c < width) {
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; i++) v += sh[i][threadIdx.x];
+        part[(int64_t)blockIdx.x * width + c] = v;
+    }
+}
+
+// ------------------------------------------------------------------ host
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encoder() {
+    static EncodeTiledFn fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        return cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                       q == cudaDriverEntryPointSuccess
+                   ? reinterpret_cast<EncodeTiledFn>(ptr)
+                   : nullptr;
+    }();
+    return fn;
+}
+
+// [rows, cols] row-major, box {bx, by}, 128-byte swizzle; what lies outside reads as zero.
+bool encode(CUtensorMap *m, const void *p, bool e4m3, int64_t rows, int64_t cols, int bx, int by) {
+    EncodeTiledFn fn = encoder();
+    if (!fn) return false;
+    const int es = e4m3 ? 1 : 2;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)(cols * es)};
+    cuuint32_t box[2] = {(cuuint32_t)bx, (cuuint32_t)by};
+    cuuint32_t one[2] = {1, 1};
+    return fn(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), dims,
+              strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One operand of a product: `rows` rows (of p or q) by `red` elements of r,
+// stored [rows, red] (K-major) or [red, rows] (MN-major).
+struct Operand {
+    const void *p;
+    int64_t rows, red;
+    bool mn;
+};
+bool encode(CUtensorMap *m, const Operand &o, bool e4m3, int tile_rows) {
+    return o.mn ? encode(m, o.p, e4m3, o.red, o.rows, 64, 64) : encode(m, o.p, e4m3, o.rows, o.red, e4m3 ? 128 : 64, tile_rows);
+}
+
+template <typename K>
+int launch_cluster(K kernel, dim3 grid, int threads, int cluster, size_t bytes, cudaStream_t st, void **args) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return (int)e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)cluster;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    return (int)cudaLaunchKernelExC(&cfg, (const void *)kernel, args);
+}
+
+template <bool E4M3, bool A_MN, bool B_MN>
+int wide(const Operand &A, const Operand &B, Args a, void *y, void *z, int sms, cudaStream_t st) {
+    CUtensorMap ma, mb, my, mz;
+    if (!encode(&ma, A, E4M3, 128) || !encode(&mb, B, E4M3, 128) || !encode(&my, y, false, a.P, a.Q, 64, 32) ||
+        !encode(&mz, z ? z : y, false, a.P, a.Q, 64, 32))
+        return (int)cudaErrorInvalidValue;
+    a.tiles_p = (int)((a.P + kTile - 1) / kTile);
+    a.tiles_q = (int)((a.Q + kTile - 1) / kTile);
+    const int64_t tiles = (int64_t)a.tiles_p * a.tiles_q;
+    if (tiles > (int64_t)0x3fffffff) return (int)cudaErrorInvalidValue;
+    const int pairs = (int)std::min<int64_t>(tiles, sms / 2);
+    void *args[] = {&ma, &mb, &my, &mz, &a};
+    return launch_cluster(wide_kernel<E4M3, A_MN, B_MN>, dim3(2 * pairs), kWideThreads, 2, kWideBytes, st, args);
+}
+
+template <int QN, bool E4M3, bool A_MN>
+int narrow(const Operand &W, const Operand &X, Args a, int split, cudaStream_t st) {
+    CUtensorMap mw, mx;
+    if (!encode(&mw, W, E4M3, 128) || !encode(&mx, X, E4M3, QN)) return (int)cudaErrorInvalidValue;
+    void *args[] = {&mw, &mx, &a};
+    const dim3 grid((unsigned)split, (unsigned)((a.Q + 127) / 128), (unsigned)((a.P + QN - 1) / QN));
+    return launch_cluster(narrow_kernel<QN, E4M3, A_MN>, grid, kNarrowThreads, split, kNarrowBytes<QN>, st, args);
+}
+
+// Which kernel runs a product whose rows p are rows of x, by an estimate of
+// its cycles: waves of tiles times what a tile costs.
+struct Choice {
+    int qn = 0, split = 1;   // qn 0: wide_kernel
+};
+Choice choose(int64_t P, int64_t Q, int blocks, int sms) {
+    auto up = [](int64_t x, int64_t d) { return (x + d - 1) / d; };
+    Choice best;
+    double cost = (double)up(up(P, kTile) * up(Q, kTile), sms / 2) * (blocks * 520.0 + 4000.0);
+    for (int qn = 16; qn <= 128; qn *= 2) {
+        if (qn < 128 && P > qn) continue;
+        if (up(Q, 128) > 65535 || up(P, qn) > 65535) continue;
+        const double block = std::max(2.0 * qn, (128 + qn) * kRBytes / 45.0);
+        for (int split = 1; split <= kMaxSplit && split <= blocks; split *= 2) {
+            const double waves = (double)up(up(P, qn) * up(Q, 128) * split, sms);
+            const double c = waves * (up(blocks, split) * block + 4000.0 + (split > 1 ? 1500.0 : 0.0));
+            if (c < cost) {
+                cost = c;
+                best.qn = qn;
+                best.split = split;
+            }
+        }
+        if (P <= qn) break;
+    }
+    return best;
+}
+
+// D = X W^T for rows of x (K-major) and rows of w (K- or MN-major).
+template <bool E4M3, bool W_MN>
+int product(const Operand &X, const Operand &W, Args a, void *y, void *z, int sms, cudaStream_t st) {
+    const Choice c = choose(a.P, a.Q, a.blocks, sms);
+    a.y = (__nv_bfloat16 *)y;
+    a.z = (__nv_bfloat16 *)z;
+    switch (c.qn) {
+        case 16: return narrow<16, E4M3, W_MN>(W, X, a, c.split, st);
+        case 32: return narrow<32, E4M3, W_MN>(W, X, a, c.split, st);
+        case 64: return narrow<64, E4M3, W_MN>(W, X, a, c.split, st);
+        case 128: return narrow<128, E4M3, W_MN>(W, X, a, c.split, st);
+        default: return wide<E4M3, false, W_MN>(X, W, a, y, z, sms, st);
+    }
+}
+
+// Row blocks of dz_kernel: enough for eight blocks per SM, of 64 rows or more.
+int dz_rows_per_block(int64_t rows, int width, int sms) {
+    const int64_t want = std::max<int64_t>(1, (int64_t)sms * 8 / ((width + 255) / 256));
+    return (int)std::max<int64_t>(64, (rows + want - 1) / want);
+}
+
+}  // namespace
+
+int launch_linear_fwd(const cpdr_ctx *c, int64_t rows, int K, int N, const void *x, const void *w, const float *x_scale,
+                      const float *w_scale, const float *bias, int act, const void *residual, void *z, void *y,
+                      void *stream) {
+    const bool e4m3 = x_scale != nullptr;
+    Args a{};
+    a.e = Epilogue{bias, x_scale, w_scale, (const __nv_bfloat16 *)residual, act, z ? 1 : 0};
+    a.P = rows;
+    a.Q = N;
+    a.blocks = (K * (e4m3 ? 1 : 2) + kRBytes - 1) / kRBytes;
+    a.status = c->dev.status;
+    const Operand X{x, rows, K, false}, W{w, N, K, false};
+    const int sms = device_sms(c->device);
+    cudaStream_t st = (cudaStream_t)stream;
+    return e4m3 ? product<true, false>(X, W, a, y, z, sms, st) : product<false, false>(X, W, a, y, z, sms, st);
+}
+
+size_t linear_dz_parts(const cpdr_ctx *c, int64_t rows, int N) {
+    const int per = dz_rows_per_block(rows, N, device_sms(c->device));
+    return (size_t)((rows + per - 1) / per);
+}
+
+int launch_linear_bwd(const cpdr_ctx *c, int64_t rows, int K, int N, const void *x, const void *w, const void *z,
+                      const void *dy, int act, void *dx, void *dw, float *dbias, void *dz, float *part, void *stream) {
+    const int sms = device_sms(c->device);
+    cudaStream_t st = (cudaStream_t)stream;
+    int rc = 0;
+    if (act || dbias) {
+        const int per = dz_rows_per_block(rows, N, sms);
+        const int64_t parts = (rows + per - 1) / per;
+        dz_kernel<<<dim3((unsigned)parts, (unsigned)((N + 255) / 256)), 256, 0, st>>>(
+            (const __nv_bfloat16 *)dy, (const __nv_bfloat16 *)z, act, rows, N, per, (__nv_bfloat16 *)dz, dbias ? part : nullptr);
+        rc = (int)cudaGetLastError();
+        if (rc) return rc;
+        if (dbias) rc = launch_column_sums(part, (int)parts, N, dbias, stream);
+        if (rc) return rc;
+    }
+    const void *g = act ? dz : dy;
+    Args a{};
+    a.status = c->dev.status;
+    if (dx) {
+        a.P = rows;
+        a.Q = K;
+        a.blocks = (N + 63) / 64;
+        rc = product<false, true>(Operand{g, rows, N, false}, Operand{w, K, N, true}, a, dx, nullptr, sms, st);
+        if (rc) return rc;
+    }
+    if (dw) {
+        a.P = N;
+        a.Q = K;
+        a.blocks = (int)((rows + 63) / 64);
+        rc = wide<false, true, true>(Operand{g, N, rows, true}, Operand{x, K, rows, true}, a, dw, nullptr, sms, st);
+    }
+    return rc;
+}
+
+}  // namespace cpdr

@@ -276,10 +276,10 @@ __global__ void __launch_bounds__(kBlock<TPR>) rmsnorm_bwd_kernel(BwdParams p) {
 
 constexpr int kSumCols = 32, kSumRows = 16;
 
-// dw[col] = sum of part[:, col], in a fixed order: 16 strided sums per
+// out[col] = sum of part[:, col], in a fixed order: 16 strided sums per
 // column, then those 16.
 __global__ void __launch_bounds__(kSumCols *kSumRows)
-rmsnorm_dw_kernel(const float *__restrict__ part, int nparts, int width, float *__restrict__ dw) {
+column_sums_kernel(const float *__restrict__ part, int nparts, int width, float *__restrict__ out) {
     __shared__ float sh[kSumRows][kSumCols + 1];
     const int cx = threadIdx.x % kSumCols, ry = threadIdx.x / kSumCols;
     const int col = blockIdx.x * kSumCols + cx;
@@ -292,7 +292,7 @@ rmsnorm_dw_kernel(const float *__restrict__ part, int nparts, int width, float *
         v = sh[0][cx];
 #pragma unroll
         for (int r = 1; r < kSumRows; r++) v += sh[r][cx];
-        dw[col] = v;
+        out[col] = v;
     }
 }
 
@@ -316,8 +316,7 @@ int bwd(const BwdParams &p, int grid, float *dw, cudaStream_t st) {
     rmsnorm_bwd_kernel<T, TPR, NV><<<grid, kBlock<TPR>, smem, st>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return (int)e;
-    rmsnorm_dw_kernel<<<(p.width + kSumCols - 1) / kSumCols, kSumCols * kSumRows, 0, st>>>(p.part, grid, p.width, dw);
-    return (int)cudaGetLastError();
+    return launch_column_sums(p.part, grid, p.width, dw, st);
 }
 
 // Threads per row: two 16-byte vectors each where that gives a group of 16 to
@@ -346,6 +345,12 @@ int rows_per_block(int width, bool f32) {
 }  // namespace
 
 static_assert(kMaxNormWidth <= 1024 * 4 * kVecOf<float> && kMaxNormWidth <= 1024 * 2 * kVecOf<__nv_bfloat16>, "a row fits the registers of one block");
+
+int launch_column_sums(const float *part, int nparts, int width, float *out, void *stream) {
+    column_sums_kernel<<<(width + kSumCols - 1) / kSumCols, kSumCols * kSumRows, 0, (cudaStream_t)stream>>>(part, nparts,
+                                                                                                            width, out);
+    return (int)cudaGetLastError();
+}
 
 int launch_rmsnorm_fwd(const cpdr_ctx *c, int64_t rows, int width, const void *x, const void *residual,
                        const float *weight, float eps, void *sum_out, void *y, void *y8, float *scale, void *stream) {

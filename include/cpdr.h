@@ -400,6 +400,41 @@ cpdr_status cpdr_rmsnorm_bwd(const cpdr_ctx *ctx, int64_t rows, int32_t width, c
                              float eps, const void *dy, const void *dsum, void *ds, float *dweight, void *workspace,
                              size_t workspace_bytes, void *stream);
 
+/*
+ * Matrix product with bias, activation and residual in its epilogue:
+ *     z = x w^T + bias,   y = act(z) + residual,
+ * x [rows, K], w [N, K], y and residual [rows, N], z [rows, N] or NULL (the
+ * value before the activation, which cpdr_linear_bwd takes), bias [N] fp32 or
+ * NULL, residual or NULL (y may be residual: in place); act = identity (0),
+ * SiLU (1) or GELU z Phi(z) (2).  bf16 contexts only; x and w are bf16, or,
+ * when x_scale [rows] and w_scale [N] (fp32, both or neither) are given,
+ * e4m3, standing for x[i, k] x_scale[i] and w[n, k] w_scale[n] (what
+ * cpdr_rmsnorm_fwd leaves in y8 and scale is such an x).  The products are
+ * accumulated in fp32; y and z are rounded once.
+ * rows >= 0; K % 8 == 0 (e4m3: K % 16 == 0); N % 8 == 0.
+ * Errors: CPDR_ERR_UNSUPPORTED (an fp32 context), CPDR_ERR_INVALID,
+ * CPDR_ERR_CUDA.
+ */
+cpdr_status cpdr_linear_fwd(const cpdr_ctx *ctx, int64_t rows, int32_t K, int32_t N, const void *x, const void *w,
+                            const float *x_scale, const float *w_scale, const float *bias, int32_t activation,
+                            const void *residual, void *z, void *y, void *stream);
+
+/*
+ * Its backward for bf16 operands, from dy [rows, N] bf16 (which is also the
+ * residual's gradient):
+ *     dz = dy act'(z),   dx = dz w,   dw = dz^T x,   dbias = sum over rows of dz.
+ * z as the forward left it (NULL without an activation); dx [rows, K] and dw
+ * [N, K] bf16, dbias [N] fp32, each NULL where it is not wanted (then the
+ * operand that it alone needs may be NULL too).  dz is rounded to bf16 for
+ * the two products; dbias is summed from the unrounded dz.  workspace:
+ * cpdr_linear_bwd_workspace_bytes() bytes, 16-byte aligned.
+ */
+cpdr_status cpdr_linear_bwd_workspace_bytes(const cpdr_ctx *ctx, int64_t rows, int32_t K, int32_t N,
+                                            int32_t activation, size_t *bytes);
+cpdr_status cpdr_linear_bwd(const cpdr_ctx *ctx, int64_t rows, int32_t K, int32_t N, const void *x, const void *w,
+                            const void *z, const void *dy, int32_t activation, void *dx, void *dw, float *dbias,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
 /* pre_num_conv_tokens ([FLA-CP] §3.3) per segment, host memory: how many of
  * the W - 1 tokens before segment s's start belong to its first sequence
  * (0 when the segment starts a sequence), out[0 .. min(cap, nseg)). */

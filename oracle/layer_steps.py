@@ -1,5 +1,6 @@
 """fp64 oracle of the layer steps around the token mixers: the gated linear
-recurrence and the RMS norm, with their gradients.
+recurrence, the RMS norm and the matrix product with its epilogue, with their
+gradients.
 
 TEST INFRASTRUCTURE ONLY, like the rest of ``oracle``: the CUDA library
 shares nothing with it.  Everything is written token by token or row by row
@@ -9,6 +10,8 @@ computation in fp32 may be off: the roundings along its path, added up in
 absolute values (derived at each place).
 """
 from __future__ import annotations
+
+import math
 
 import numpy as np
 
@@ -138,3 +141,75 @@ def rmsnorm_backward(s, weight, eps, dy, dsum=None):
     t = dy * s * rstd
     return dict(ds=ds, dweight=t.sum(axis=0), e_ds=2 * ROW * mag,
                 e_dweight=(ROW + (s.shape[0] + 32) * U32) * np.abs(t).sum(axis=0))
+
+
+def _erf(x):
+    return np.vectorize(math.erf, otypes=[np.float64])(x)
+
+
+def activation(z, act):
+    if act == "silu":
+        return z / (1.0 + np.exp(-z))
+    if act == "gelu":
+        return 0.5 * z * (1.0 + _erf(z / math.sqrt(2.0)))
+    return z
+
+
+def activation_grad(z, act):
+    if act == "silu":
+        s = 1.0 / (1.0 + np.exp(-z))
+        return s * (1.0 + z * (1.0 - s))
+    if act == "gelu":
+        return 0.5 * (1.0 + _erf(z / math.sqrt(2.0))) + z * np.exp(-0.5 * z * z) / math.sqrt(2.0 * math.pi)
+    return np.ones_like(z)
+
+
+# A sum of n products in fp32: the tensor cores add 16 (bf16) or 32 (e4m3)
+# exact products at once to the running sum, each time with an error of at most
+# one unit in the last place (2 U32; they may cut instead of rounding) of what
+# the absolute values add up to; 16 more for the roundings inside an addition
+# and for the sums of a split.
+def _sum_error(n):
+    return (n / 16 + 16) * 2 * U32
+
+
+# exp, the quotient or erf, and the products around them, in fp32: 16 U32 of
+# what the value is made of (z act terms of size |z|, gradients of size 1 + |z|).
+ACT = 16 * U32
+
+
+def linear_forward(x, w, bias=None, act=None, residual=None, x_scale=None, w_scale=None):
+    """z = (x w^T) x_scale w_scale + bias, y = act(z) + residual, and the
+    error bounds of both (|act'| is at most 1.13)."""
+    x, w = as64(x), as64(w)
+    z, mag = x @ w.T, np.abs(x) @ np.abs(w).T
+    if x_scale is not None:
+        s = as64(x_scale)[:, None] * as64(w_scale)[None, :]
+        z, mag = z * s, mag * s
+    e_z = mag * (_sum_error(x.shape[1]) + 4 * U32)
+    if bias is not None:
+        z = z + as64(bias)
+        e_z = e_z + 2 * U32 * np.abs(z)
+    y, e_y = activation(z, act), 1.13 * e_z + ACT * np.abs(z)
+    if residual is not None:
+        y = y + as64(residual)
+        e_y = e_y + 2 * U32 * np.abs(y)
+    return dict(z=z, y=y, e_z=e_z, e_y=e_y)
+
+
+def linear_backward(x, w, dy, z=None, act=None):
+    """dx, dw, dbias and their error bounds: dz is an operand rounded to bf16
+    (half a step of each value), dbias a sum of unrounded values."""
+    x, w, dy = as64(x), as64(w), as64(dy)
+    if act in ("silu", "gelu"):
+        z = as64(z)
+        dz, e = dy * activation_grad(z, act), ACT * np.abs(dy) * (1 + np.abs(z))
+    else:
+        dz, e = dy, np.zeros_like(dy)
+    step = HALF_STEP["bf16"] * np.abs(dz) + e if act in ("silu", "gelu") else e
+    rows, N = dz.shape
+    A = np.abs(dz) + step
+    return dict(dx=dz @ w, dw=dz.T @ x, dbias=dz.sum(0),
+                e_dx=step @ np.abs(w) + _sum_error(N) * (A @ np.abs(w)),
+                e_dw=step.T @ np.abs(x) + _sum_error(rows) * (A.T @ np.abs(x)),
+                e_dbias=e.sum(0) + (rows + 32) * U32 * np.abs(dz).sum(0))

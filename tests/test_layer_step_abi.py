@@ -28,6 +28,8 @@ def test_host_only_context_rejects_launches(cpdr_lib):
         lambda: cpdr_lib.cpdr_glr_step(c._h, P(16), P(32), P(48), P(48), None, 1, 1, 8, P(64), None),
         lambda: cpdr_lib.cpdr_rmsnorm_fwd(c._h, 1, 8, P(16), None, P(32), 1e-6, None, P(48), None, None, None),
         lambda: cpdr_lib.cpdr_rmsnorm_bwd(c._h, 1, 8, P(16), P(32), 1e-6, P(48), None, P(64), P(80), P(96), 1 << 20, None),
+        lambda: cpdr_lib.cpdr_linear_fwd(c._h, 1, 8, 8, P(16), P(32), None, None, None, 0, None, None, P(48), None),
+        lambda: cpdr_lib.cpdr_linear_bwd(c._h, 1, 8, 8, P(16), P(32), None, P(48), 0, P(64), None, None, None, 0, None),
     ]
     for call in calls:
         assert call() == cpdr.ERR_INVALID

@@ -94,3 +94,45 @@ def test_rmsnorm_gradients_equal_differences(eps):
         d[i] = 1e-5
         num = (loss(s, w + d) - loss(s, w - d)) / 2e-5
         assert abs(num - r["dweight"][i]) <= 1e-7 * (1 + abs(num))
+
+
+def test_linear_is_the_sum_of_products():
+    x = np.arange(6.0).reshape(2, 3)
+    w = np.array([[1.0, 0, 0], [0, 2, 0], [1, 1, 1], [-1, 0, 1]])
+    r = ol.linear_forward(x, w, bias=np.array([0.0, 1, 0, -1]), residual=np.ones((2, 4)),
+                          x_scale=np.array([1.0, 2.0]), w_scale=np.array([1.0, 1, 10, 1]))
+    np.testing.assert_allclose(r["y"], [[1, 4, 31, 2], [7, 18, 241, 4]])
+
+
+def test_activations_closed_forms():
+    z = np.array([0.0, 1.0, -1.0, 30.0, -30.0])
+    np.testing.assert_allclose(ol.activation(z, "silu"), [0, 1 / (1 + np.exp(-1)), -1 / (1 + np.exp(1)), 30, -30 * np.exp(-30)],
+                               rtol=1e-12)
+    # Phi(1) = 0.8413447460685429
+    np.testing.assert_allclose(ol.activation(z[:3], "gelu"), [0, 0.8413447460685429, -0.15865525393145707], rtol=1e-12)
+    for act in ("silu", "gelu"):
+        v = np.linspace(-6, 6, 41)
+        num = (ol.activation(v + 1e-6, act) - ol.activation(v - 1e-6, act)) / 2e-6
+        np.testing.assert_allclose(ol.activation_grad(v, act), num, atol=1e-8)
+        assert np.abs(ol.activation_grad(v, act)).max() <= 1.13
+
+
+@pytest.mark.parametrize("act", [None, "silu", "gelu"])
+def test_linear_gradients_equal_differences(act):
+    rng = np.random.default_rng(6)
+    x, w, b, dy = (rng.standard_normal(s) for s in ((3, 5), (4, 5), (4,), (3, 4)))
+    f = ol.linear_forward(x, w, bias=b, act=act)
+    r = ol.linear_backward(x, w, dy, z=f["z"], act=act)
+
+    def loss(x, w, b):
+        return (ol.linear_forward(x, w, bias=b, act=act)["y"] * dy).sum()
+
+    for name, at, grad in (("x", x, r["dx"]), ("w", w, r["dw"]), ("b", b, r["dbias"])):
+        for i in range(at.size):
+            d = np.zeros(at.size)
+            d[i] = 1e-5
+            d = d.reshape(at.shape)
+            hi, lo = dict(x=x, w=w, b=b), dict(x=x, w=w, b=b)
+            hi[name], lo[name] = at + d, at - d
+            num = (loss(**hi) - loss(**lo)) / 2e-5
+            assert abs(num - grad.reshape(-1)[i]) <= 1e-7 * (1 + abs(num)), name
