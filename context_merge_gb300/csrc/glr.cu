@@ -39,12 +39,13 @@ using namespace vio;
 
 constexpr int kSlice = 64;                  // channels of a CTA
 constexpr int kMaxCluster = 8;
-constexpr int kStages = 3;                  // groups of a warp in shared memory: going out, being mapped, on its way
+constexpr int kFwdStages = 2;               // groups of a warp in shared memory, both on their way
+constexpr int kStages = 3;                  // backward: going out, being mapped, on its way
 constexpr int kStepThreads = 256;
 // Warps of a CTA.  Forward: two CTAs of four per SM, whose steps hide one
-// another's (262144 x 2048 bf16, one sequence: 732 us; one CTA of eight:
-// 790; two of five: 755; two stages: 985).  Backward: one CTA of what the
-// stages leave room for (packed 65536 x 2048 bf16: 313 us; two of four: 319).
+// another's (262144 x 2048 bf16, one sequence: 677 us; of six warps 709; three
+// of four 729).  Backward: one CTA of what three stages leave room for (packed
+// 65536 x 2048 bf16: 311 us; two of four: 319).
 constexpr int kFwdWarps = 4;
 template <typename T>
 constexpr int kBwdWarps = sizeof(T) == 2 ? 8 : 5;
@@ -93,21 +94,50 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return unpair(r);
 }
 
-// exp(g) = 2^t (1 + e ln 2) with t = g log2(e) rounded and e = g log2(e) - t,
-// which the fused product gives exactly: 2^t alone would be off by |g| half
-// steps.  Gates below -128 (and -infinity) give 2^-185, flushed to zero; a
-// NaN stays one.  Eight instructions for two gates, where expf takes about
-// seventeen.
-__device__ __forceinline__ float2 exp2_of_gate(float2 g) {
-    constexpr float kL = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
-    asm("max.NaN.f32 %0, %0, 0fC3000000;" : "+f"(g.x));   // -128
-    asm("max.NaN.f32 %0, %0, 0fC3000000;" : "+f"(g.y));
-    const float2 t = mul2(g, make_float2(kL, kL));
-    const float2 e = fma2(g, make_float2(-kL, -kL), t);   // minus the rest
-    float2 r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(t.x));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(t.y));
-    return fma2(mul2(r, make_float2(-kLn2, -kLn2)), e, r);
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// a = exp(g) for a group's gates, in place.
+// Gates next to 0 make a long memory, which adds the errors of many steps up:
+// they need an a that leans to no side.  Where every channel's squares sum to
+// at most 1/16 over the group (so |g| <= 1/4), a = 1 + g + g^2 q(g), q of
+// degree 3 interpolated at Chebyshev points (off by 0.7 half steps of a at
+// 1/4, by 0.1 up to 1/10), rounded once: six instructions for two channels.
+// Elsewhere the state forgets in a few steps, and the fast power of two does
+// (off by up to 3 half steps, leaning by 0.4: alone, it cost the states of a
+// long memory 1e-6): a = 2^t (1 + e ln 2) with t = g log2(e) rounded and e what
+// the fused product finds missing.  Gates from -87.4 down give 0; a NaN stays
+// one.  (One polynomial with a reduction for all gates: 18 instructions, the
+// forward at 262144 x 2048 in 0.79 instead of 0.68 ms.)
+__device__ __forceinline__ void exp_of_gates(float2 (&g)[kGlrGroup]) {
+    float2 sq[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
+#pragma unroll
+    for (int u = 0; u < kGlrGroup; u++) sq[u & 3] = fma2(g[u], g[u], sq[u & 3]);
+    const float2 sum = add2(add2(sq[0], sq[1]), add2(sq[2], sq[3]));
+    if (__all_sync(0xffffffffu, sum.x <= 0.0625f && sum.y <= 0.0625f)) {
+        constexpr float kC[4] = {0.49999931454658508f, 0.16666656732559204f, 0.041753556579351425f, 0.0083457436412572861f};
+#pragma unroll
+        for (int u = 0; u < kGlrGroup; u++) {
+            float2 r = fma2(g[u], both(kC[3]), both(kC[2]));
+            r = fma2(g[u], r, both(kC[1]));
+            r = fma2(g[u], r, both(kC[0]));
+            r = fma2(g[u], r, both(1.f));
+            g[u] = fma2(g[u], r, both(1.f));
+        }
+    } else {
+        constexpr float kL = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
+#pragma unroll
+        for (int u = 0; u < kGlrGroup; u++) {
+            // -infinity would meet itself in e; 2^-185 is flushed to zero
+            asm("max.NaN.f32 %0, %0, %1;" : "+f"(g[u].x) : "f"(-128.f));
+            asm("max.NaN.f32 %0, %0, %1;" : "+f"(g[u].y) : "f"(-128.f));
+            const float2 t = mul2(g[u], both(kL));
+            const float2 e = fma2(g[u], both(-kL), t);   // minus what is missing
+            float2 r;
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(t.x));
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(t.y));
+            g[u] = fma2(mul2(r, both(-kLn2)), e, r);
+        }
+    }
 }
 
 // A pair of maps h -> A h + B.
@@ -277,7 +307,7 @@ struct FwdShared {
     struct {
         Tile<T> x;
         Tile<float> g;
-    } ring[WARPS][kStages];
+    } ring[WARPS][kFwdStages];
 };
 template <typename T, int WARPS>
 struct BwdShared {
@@ -296,10 +326,12 @@ extern __shared__ __align__(16) unsigned char smem[];
 
 // The loop of both directions, over cluster steps i: the maps of step i + 1
 // are taken and published, then step i's tokens run from their start and go
-// out while the cluster exchanges those maps, then step i + 3's copies start
-// into the place that step i leaves (so copies have a whole step and more to
-// arrive), and last the starts of step i + 1 follow from the exchanged maps.
-// A group's gates become a_t = exp(g_t) in place when its map is taken.
+// out while the cluster exchanges those maps, and last the starts of step
+// i + 1 follow from the exchanged maps.  Forward, a group is held in registers
+// from its map to its output (two groups in turn), so that its place in shared
+// memory takes the next copies at once; backward, three tensors and the
+// recomputed states leave no registers for that: the group stays where it is,
+// with its gates made to a_t = exp(g_t) in place.
 //
 // grid: (span, channel slice) items x cluster CTAs; cluster (nz, 1, 1)
 template <typename T, int WARPS, bool ZIGZAG>
@@ -325,63 +357,65 @@ __global__ void __launch_bounds__(32 * WARPS, 2) glr_fwd_kernel(Params p, int nz
         r.g.load(p, rows, p.g, c0, n, lane);
         cp_commit();
     };
+    struct Group {
+        float2 a[kGlrGroup];
+        Raw2<T> x[kGlrGroup];
+    };
     Map before, all;
-    auto map = [&](int stage, int par) {
-        auto &r = sh.ring[w][stage];
-        Map m{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
+    // Takes step i's group into registers, starts step i + 2's copies into its
+    // place, and publishes its map.
+    auto take = [&](Group &v, int64_t at, int stage) {
+        cp_wait<1>();
+        __syncwarp();
+        const auto &r = sh.ring[w][stage];
 #pragma unroll
         for (int u = 0; u < kGlrGroup; u++) {
-            const float2 xv = widen(load2(&r.x.v[u][2 * lane]));
-            float2 *g = reinterpret_cast<float2 *>(&r.g.v[u][2 * lane]);
-            const float2 a = exp2_of_gate(*g);   // behind the tokens g = 0: the state stays
-            *g = a;
-            m = after(Map{a, xv}, m);
+            v.a[u] = *reinterpret_cast<const float2 *>(&r.g.v[u][2 * lane]);
+            v.x[u] = load2(&r.x.v[u][2 * lane]);
         }
-        sh.ex.publish(par, w, lane, rank, (uint32_t)nz, m, before, all);
+        __syncwarp();
+        fetch(at + 2 * step, stage);
+        exp_of_gates(v.a);   // behind the tokens g = 0: the state stays
+        Map m{both(1.f), both(0.f)};
+#pragma unroll
+        for (int u = 0; u < kGlrGroup; u++) m = after(Map{v.a[u], widen(v.x[u])}, m);
+        sh.ex.publish(stage, w, lane, rank, (uint32_t)nz, m, before, all);
     };
     const int64_t steps = (sp.len + step - 1) / step;
-    float2 h = make_float2(0.f, 0.f);
-    sh.ex.open((uint32_t)nz);
-    if (steps > 0) {
-#pragma unroll
-        for (int s = 0; s < kStages; s++) fetch(p0 + s * step, s);
-        cp_wait<kStages - 1>();
-        __syncwarp();
-        map(0, 0);
-        h = sh.ex.start(0, 0, lane, rank, (uint32_t)nz, before, all, carry, p.status);
-    }
-    int stage = 0, par = 0;
-    for (int64_t i = 0; i < steps; i++, p0 += step) {
-        const int next = stage + 1 == kStages ? 0 : stage + 1;
-        if (i + 1 < steps) {
-            cp_wait<kStages - 2>();
-            __syncwarp();
-            map(next, par ^ 1);
-        }
+    float2 h = both(0.f);
+    // One step: the next one's maps, this one's outputs, the next one's starts.
+    auto turn = [&](const Group &v, Group &next, int64_t i, int parity) {
+        if (i + 1 < steps) take(next, p0 + step, parity ^ 1);
         const int n = live ? tokens(p0) : 0;
         if (n > 0 && p.carry)
             *reinterpret_cast<float2 *>(p.carry + (sp.group0 + p0 / kGlrGroup) * p.channels + c) = h;
         const Rows<ZIGZAG> rows(p, sp, p0, lane);
-        const auto &r = sh.ring[w][stage];
         auto run = [&](auto whole) {
             T *o = y + rows.at(0) * p.channels;
 #pragma unroll
             for (int u = 0; u < kGlrGroup; u++) {
-                const float2 xv = widen(load2(&r.x.v[u][2 * lane]));
-                const float2 a = *reinterpret_cast<const float2 *>(&r.g.v[u][2 * lane]);
-                h = fma2(a, h, xv);
+                h = fma2(v.a[u], h, widen(v.x[u]));
                 if (ZIGZAG) o = y + rows.at(u) * p.channels;
                 if (decltype(whole)::value || u < n) store2(ZIGZAG ? o : o + u * p.channels, h);
             }
         };
         if (!ZIGZAG && n == kGlrGroup) run(std::true_type());
         else run(std::false_type());
-        __syncwarp();   // the group is read to the end before its place is filled again
-        fetch(p0 + kStages * step, stage);
-        stage = next;
-        par ^= 1;
         if (i + 1 < steps)
-            h = sh.ex.start(par, (uint32_t)((i + 1) >> 1) & 1u, lane, rank, (uint32_t)nz, before, all, carry, p.status);
+            h = sh.ex.start(parity ^ 1, (uint32_t)((i + 1) >> 1) & 1u, lane, rank, (uint32_t)nz, before, all, carry, p.status);
+        p0 += step;
+    };
+    sh.ex.open((uint32_t)nz);
+    if (steps > 0) {
+        Group even, odd;
+        fetch(p0, 0);
+        fetch(p0 + step, 1);
+        take(even, p0, 0);
+        h = sh.ex.start(0, 0, lane, rank, (uint32_t)nz, before, all, carry, p.status);
+        for (int64_t i = 0; i < steps; i += 2) {
+            turn(even, odd, i, 0);
+            if (i + 1 < steps) turn(odd, even, i + 1, 1);
+        }
     }
     cp_wait<0>();
     sh.ex.close((uint32_t)nz);
@@ -428,13 +462,19 @@ __global__ void __launch_bounds__(32 * WARPS, 1) glr_bwd_kernel(Params p, int nz
     auto map = [&](int stage, int par) {
         auto &r = sh.ring[w][stage];
         Map m{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
+        // everything is loaded before the first a is stored
+        float2 g[kGlrGroup];
+        Raw2<T> dy[kGlrGroup];
+#pragma unroll
+        for (int u = 0; u < kGlrGroup; u++) {
+            g[u] = *reinterpret_cast<const float2 *>(&r.g.v[u][2 * lane]);
+            dy[u] = load2(&r.dy.v[u][2 * lane]);
+        }
+        exp_of_gates(g);
 #pragma unroll
         for (int u = kGlrGroup - 1; u >= 0; u--) {
-            const float2 d = widen(load2(&r.dy.v[u][2 * lane]));
-            float2 *g = reinterpret_cast<float2 *>(&r.g.v[u][2 * lane]);
-            const float2 a = exp2_of_gate(*g);
-            *g = a;
-            m = Map{mul2(m.A, a), mul2(a, add2(d, m.B))};
+            *reinterpret_cast<float2 *>(&r.g.v[u][2 * lane]) = g[u];
+            m = Map{mul2(m.A, g[u]), mul2(g[u], add2(widen(dy[u]), m.B))};
         }
         sh.ex.publish(par, w, lane, rank, (uint32_t)nz, m, before, all);
     };
@@ -531,7 +571,7 @@ glr_step_kernel(const T *__restrict__ x, const float *__restrict__ g, const floa
         const int64_t o = (int64_t)j * channels + c;
         const float2 gv = *reinterpret_cast<const float2 *>(g + o);
         const float2 xv = widen(load2(x + o));
-        h = fma2(exp2_of_gate(gv), h, xv);
+        h = fma2(make_float2(expf(gv.x), expf(gv.y)), h, xv);
         store2(y + o, h);
         if (!more) break;
     }
