@@ -123,22 +123,44 @@ def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
 
 
-def _check_tensor(name: str, t, shape, dtype, device, nullable: bool = False):
-    """Raises ValueError unless t is a contiguous CUDA tensor of that shape, dtype and device (or None, if it may be)."""
+def _bad_tensor(name: str, t, shape, dtype, dev):
     if t is None:
-        if nullable:
-            return
         raise ValueError(f"{name} is missing")
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {list(shape)} {dtype} tensor, got {list(t.shape)} {t.dtype}")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    raise ValueError(f"{name} must be on the context's device {dev}, got {t.device}")
+
+
+def _addr(name: str, t, shape, dtype, dev):
+    """The address of t, which must be a contiguous CUDA tensor of that shape
+    and dtype on device index ``dev`` (a decoding step is bound by what the
+    host does, so the checks are few and cheap)."""
+    if t is None or t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev:
+        _bad_tensor(name, t, shape, dtype, dev)
+    return t.data_ptr()
+
+
+def _opt(name: str, t, shape, dtype, dev):
+    """_addr of a tensor that may be None (NULL)."""
+    return None if t is None else _addr(name, t, shape, dtype, dev)
 
 
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _space(t, dev):
+    """Address and bytes of a workspace tensor."""
+    if not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"workspace must be a contiguous tensor on the context's device {dev}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _raw_stream(stream, dev):
+    """cudaStream_t of ``stream``, or of torch's current stream on device ``dev``."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 class Context:
@@ -188,6 +210,8 @@ class Context:
         _check(lib.cpdr_ctx_create(ctypes.byref(desc), ctypes.byref(h)))
         self._h = h
         self._lib = lib
+        # the device of every tensor that a call takes (none: a host-only context launches nothing)
+        self._dev = None if host_only else torch.cuda.current_device()
 
     def close(self):
         if getattr(self, "_h", None):
@@ -378,7 +402,7 @@ class Context:
         if x.dim() != 3 or tuple(x.shape[:2]) != (self.B, self.T):
             raise ValueError(f"x must be a [{self.B}, {self.T}, C] tensor, got {list(x.shape)}")
         C = x.shape[2]
-        return C, (self.B, self.T, C), (self.N, C)
+        return C, x.shape, (self.N, C)
 
     def glr_fwd(self, x, g, y, h0=None, hT=None, carry=None, stream=None):
         """y_t = h_t = exp(g_t) h_{t-1} + x_t over every sequence of the
@@ -386,34 +410,27 @@ class Context:
         h0 and hT [N, C] fp32 or None; carry (``glr_carry_shape``) keeps what
         ``glr_bwd`` needs."""
         C, tok, st = self._glr_shapes(x)
-        f32, dev = torch.float32, x.device
-        _check_tensor("x", x, tok, self.torch_dtype, dev)
-        _check_tensor("g", g, tok, f32, dev)
-        _check_tensor("y", y, tok, self.torch_dtype, dev)
-        _check_tensor("h0", h0, st, f32, dev, True)
-        _check_tensor("hT", hT, st, f32, dev, True)
-        if carry is not None:
-            _check_tensor("carry", carry, self.glr_carry_shape(C), f32, dev)
-        _check(self._lib.cpdr_glr_fwd(self._h, _ptr(x), _ptr(g), _ptr(h0), C, _ptr(y), _ptr(hT), _ptr(carry),
-                                      _stream(stream)))
+        f32, dt, dev = torch.float32, self.torch_dtype, self._dev
+        keep = None if carry is None else _addr("carry", carry, self.glr_carry_shape(C), f32, dev)
+        _check(self._lib.cpdr_glr_fwd(self._h, _addr("x", x, tok, dt, dev), _addr("g", g, tok, f32, dev),
+                                      _opt("h0", h0, st, f32, dev), C, _addr("y", y, tok, dt, dev),
+                                      _opt("hT", hT, st, f32, dev), keep, _raw_stream(stream, dev)))
 
     def glr_bwd(self, x, g, carry, dy, dhT=None, out=None, stream=None):
         """Gradients of sum <dy, y> + sum <dhT, hT>: a dict of dx (input
-        dtype), dg and dh0 (fp32), written into ``out``'s tensors if given."""
+        dtype), dg and dh0 (fp32), written into ``out``'s tensors if given
+        (dh0 may be None there)."""
         C, tok, st = self._glr_shapes(x)
-        f32, dev = torch.float32, x.device
-        _check_tensor("x", x, tok, self.torch_dtype, dev)
-        _check_tensor("g", g, tok, f32, dev)
-        _check_tensor("carry", carry, self.glr_carry_shape(C), f32, dev)
-        _check_tensor("dy", dy, tok, self.torch_dtype, dev)
-        _check_tensor("dhT", dhT, st, f32, dev, True)
+        f32, dt, dev = torch.float32, self.torch_dtype, self._dev
+        args = (_addr("x", x, tok, dt, dev), _addr("g", g, tok, f32, dev),
+                _addr("carry", carry, self.glr_carry_shape(C), f32, dev), _addr("dy", dy, tok, dt, dev),
+                _opt("dhT", dhT, st, f32, dev))
         if out is None:
-            out = dict(dx=torch.empty_like(x), dg=torch.empty_like(g), dh0=torch.empty(st, dtype=f32, device=dev))
-        _check_tensor("dx", out["dx"], tok, self.torch_dtype, dev)
-        _check_tensor("dg", out["dg"], tok, f32, dev)
-        _check_tensor("dh0", out.get("dh0"), st, f32, dev, True)
-        _check(self._lib.cpdr_glr_bwd(self._h, _ptr(x), _ptr(g), _ptr(carry), _ptr(dy), _ptr(dhT), C,
-                                      _ptr(out["dx"]), _ptr(out["dg"]), _ptr(out.get("dh0")), _stream(stream)))
+            out = dict(dx=torch.empty_like(x), dg=torch.empty_like(g),
+                       dh0=torch.empty(st, dtype=f32, device=x.device))
+        _check(self._lib.cpdr_glr_bwd(self._h, *args, C, _addr("dx", out["dx"], tok, dt, dev),
+                                      _addr("dg", out["dg"], tok, f32, dev), _opt("dh0", out.get("dh0"), st, f32, dev),
+                                      _raw_stream(stream, dev)))
         return out
 
     def glr_step(self, x, g, state, y, slots=None, state_out=None, stream=None):
@@ -424,22 +441,20 @@ class Context:
         rows of one slot are its consecutive tokens."""
         if x.dim() != 2 or state.dim() != 2:
             raise ValueError("x must be [n, C] and state [S, C]")
-        n, C = x.shape
-        S = state.shape[0]
-        f32, dev = torch.float32, x.device
-        _check_tensor("x", x, (n, C), self.torch_dtype, dev)
-        _check_tensor("g", g, (n, C), f32, dev)
-        _check_tensor("state", state, (S, C), f32, dev)
-        _check_tensor("y", y, (n, C), self.torch_dtype, dev)
-        _check_tensor("slots", slots, (n,), torch.int32, dev, True)
-        if state_out is None:
-            state_out = state
-        _check_tensor("state_out", state_out, (S, C), f32, dev)
-        _check(self._lib.cpdr_glr_step(self._h, _ptr(x), _ptr(g), _ptr(state), _ptr(state_out), _ptr(slots), n, S, C,
-                                       _ptr(y), _stream(stream)))
+        rows, st = x.shape, state.shape
+        f32, dt, dev = torch.float32, self.torch_dtype, self._dev
+        if st[1] != rows[1]:
+            raise ValueError(f"state must have {rows[1]} channels, got {st[1]}")
+        old = _addr("state", state, st, f32, dev)
+        _check(self._lib.cpdr_glr_step(self._h, _addr("x", x, rows, dt, dev), _addr("g", g, rows, f32, dev), old,
+                                       old if state_out is None else _addr("state_out", state_out, st, f32, dev),
+                                       _opt("slots", slots, rows[:1], torch.int32, dev), rows[0], st[0], rows[1],
+                                       _addr("y", y, rows, dt, dev), _raw_stream(stream, dev)))
 
     # ---- RMS norm --------------------------------------------------------
-    def _rows(self, x):
+    @staticmethod
+    def _rows(x):
+        """Rows and width of x, whose last axis is the row."""
         if x.dim() < 1:
             raise ValueError("x must have at least one dimension")
         width = x.shape[-1]
@@ -450,16 +465,13 @@ class Context:
         (fp32): s into ``sum_out``, the norm into ``y`` (input dtype) and/or
         ``y8`` (float8_e4m3fn) with ``scale`` (fp32, one per row)."""
         rows, width = self._rows(x)
-        dev, dt = x.device, self.torch_dtype
-        _check_tensor("x", x, x.shape, dt, dev)
-        _check_tensor("weight", weight, (width,), torch.float32, dev)
-        _check_tensor("residual", residual, x.shape, dt, dev, True)
-        _check_tensor("sum_out", sum_out, x.shape, dt, dev, True)
-        _check_tensor("y", y, x.shape, dt, dev, True)
-        _check_tensor("y8", y8, x.shape, torch.float8_e4m3fn, dev, True)
-        _check_tensor("scale", scale, x.shape[:-1], torch.float32, dev, True)
-        _check(self._lib.cpdr_rmsnorm_fwd(self._h, rows, width, _ptr(x), _ptr(residual), _ptr(weight), eps,
-                                          _ptr(sum_out), _ptr(y), _ptr(y8), _ptr(scale), _stream(stream)))
+        f32, dt, dev, sh = torch.float32, self.torch_dtype, self._dev, x.shape
+        _check(self._lib.cpdr_rmsnorm_fwd(self._h, rows, width, _addr("x", x, sh, dt, dev),
+                                          _opt("residual", residual, sh, dt, dev),
+                                          _addr("weight", weight, sh[-1:], f32, dev), eps,
+                                          _opt("sum_out", sum_out, sh, dt, dev), _opt("y", y, sh, dt, dev),
+                                          _opt("y8", y8, sh, torch.float8_e4m3fn, dev),
+                                          _opt("scale", scale, sh[:-1], f32, dev), _raw_stream(stream, dev)))
 
     def rmsnorm_bwd_workspace_bytes(self, rows, width):
         n = ctypes.c_size_t()
@@ -471,21 +483,16 @@ class Context:
         gradient ``dsum`` that reaches s past the norm: a dict of ds (input
         dtype; of x and residual alike) and dweight (fp32)."""
         rows, width = self._rows(s)
-        dev, dt = s.device, self.torch_dtype
-        _check_tensor("s", s, s.shape, dt, dev)
-        _check_tensor("weight", weight, (width,), torch.float32, dev)
-        _check_tensor("dy", dy, s.shape, dt, dev)
-        _check_tensor("dsum", dsum, s.shape, dt, dev, True)
+        f32, dt, dev, sh = torch.float32, self.torch_dtype, self._dev, s.shape
+        args = (_addr("s", s, sh, dt, dev), _addr("weight", weight, sh[-1:], f32, dev), eps,
+                _addr("dy", dy, sh, dt, dev), _opt("dsum", dsum, sh, dt, dev))
         if out is None:
             out = dict(ds=torch.empty_like(s), dweight=torch.empty_like(weight))
-        _check_tensor("ds", out["ds"], s.shape, dt, dev)
-        _check_tensor("dweight", out["dweight"], (width,), torch.float32, dev)
         if workspace is None:
-            workspace = torch.empty(self.rmsnorm_bwd_workspace_bytes(rows, width), dtype=torch.uint8, device=dev)
-        _check(self._lib.cpdr_rmsnorm_bwd(self._h, rows, width, _ptr(s), _ptr(weight), eps, _ptr(dy), _ptr(dsum),
-                                          _ptr(out["ds"]), _ptr(out["dweight"]), _ptr(workspace),
-                                          ctypes.c_size_t(workspace.numel() * workspace.element_size()),
-                                          _stream(stream)))
+            workspace = torch.empty(self.rmsnorm_bwd_workspace_bytes(rows, width), dtype=torch.uint8, device=s.device)
+        _check(self._lib.cpdr_rmsnorm_bwd(self._h, rows, width, *args, _addr("ds", out["ds"], sh, dt, dev),
+                                          _addr("dweight", out["dweight"], sh[-1:], f32, dev), *_space(workspace, dev),
+                                          _raw_stream(stream, dev)))
         return out
 
     # ---- matrix product with its epilogue ----------------------------------
@@ -496,23 +503,20 @@ class Context:
         ``w_scale`` [N]; y, residual and z (the value before the activation)
         [.., N] bf16; bias [N] fp32; activation None, "silu" or "gelu"."""
         rows, K = self._rows(x)
-        dev, f32, bf16 = x.device, torch.float32, torch.bfloat16
+        f32, bf16, dev, sh = torch.float32, torch.bfloat16, self._dev, x.shape
         it = bf16 if x_scale is None else torch.float8_e4m3fn
         if w.dim() != 2:
             raise ValueError(f"w must be a [N, {K}] tensor, got {list(w.shape)}")
         N = w.shape[0]
-        out = (*x.shape[:-1], N)
-        _check_tensor("x", x, x.shape, it, dev)
-        _check_tensor("w", w, (N, K), it, dev)
-        _check_tensor("x_scale", x_scale, x.shape[:-1], f32, dev, True)
-        _check_tensor("w_scale", w_scale, (N,), f32, dev, True)
-        _check_tensor("bias", bias, (N,), f32, dev, True)
-        _check_tensor("residual", residual, out, bf16, dev, True)
-        _check_tensor("z", z, out, bf16, dev, True)
-        _check_tensor("y", y, out, bf16, dev)
-        _check(self._lib.cpdr_linear_fwd(self._h, rows, K, N, _ptr(x), _ptr(w), _ptr(x_scale), _ptr(w_scale),
-                                         _ptr(bias), ACTIVATIONS[activation], _ptr(residual), _ptr(z), _ptr(y),
-                                         _stream(stream)))
+        out, n = (*sh[:-1], N), (N,)
+        if (x_scale is None) != (w_scale is None):
+            raise ValueError("x_scale and w_scale come together")
+        _check(self._lib.cpdr_linear_fwd(self._h, rows, K, N, _addr("x", x, sh, it, dev), _addr("w", w, (N, K), it, dev),
+                                         _opt("x_scale", x_scale, sh[:-1], f32, dev),
+                                         _opt("w_scale", w_scale, n, f32, dev), _opt("bias", bias, n, f32, dev),
+                                         ACTIVATIONS[activation], _opt("residual", residual, out, bf16, dev),
+                                         _opt("z", z, out, bf16, dev), _addr("y", y, out, bf16, dev),
+                                         _raw_stream(stream, dev)))
 
     def linear_bwd_workspace_bytes(self, rows, K, N, activation=None):
         n = ctypes.c_size_t()
@@ -525,26 +529,21 @@ class Context:
         (bf16) and dbias (fp32).  Of a given ``out`` only the entries that it
         holds are computed."""
         rows, K = self._rows(x)
+        bf16, dev, act = torch.bfloat16, self._dev, ACTIVATIONS[activation]
         N = w.shape[0]
-        dev, bf16 = x.device, torch.bfloat16
-        _check_tensor("x", x, x.shape, bf16, dev)
-        _check_tensor("w", w, (N, K), bf16, dev)
-        _check_tensor("dy", dy, (*x.shape[:-1], N), bf16, dev)
-        _check_tensor("z", z, dy.shape, bf16, dev, ACTIVATIONS[activation] == 0)
+        wide = (*x.shape[:-1], N)
+        args = (_addr("x", x, x.shape, bf16, dev), _addr("w", w, (N, K), bf16, dev),
+                _addr("z", z, wide, bf16, dev) if act else None, _addr("dy", dy, wide, bf16, dev), act)
         if out is None:
             out = dict(dx=torch.empty_like(x), dw=torch.empty_like(w),
-                       dbias=torch.empty(N, dtype=torch.float32, device=dev))
-        _check_tensor("dx", out.get("dx"), x.shape, bf16, dev, True)
-        _check_tensor("dw", out.get("dw"), w.shape, bf16, dev, True)
-        _check_tensor("dbias", out.get("dbias"), (N,), torch.float32, dev, True)
+                       dbias=torch.empty(N, dtype=torch.float32, device=x.device))
         if workspace is None:
             workspace = torch.empty(self.linear_bwd_workspace_bytes(rows, K, N, activation), dtype=torch.uint8,
-                                    device=dev)
-        _check(self._lib.cpdr_linear_bwd(self._h, rows, K, N, _ptr(x), _ptr(w), _ptr(z), _ptr(dy),
-                                         ACTIVATIONS[activation], _ptr(out.get("dx")), _ptr(out.get("dw")),
-                                         _ptr(out.get("dbias")), _ptr(workspace),
-                                         ctypes.c_size_t(workspace.numel() * workspace.element_size()),
-                                         _stream(stream)))
+                                    device=x.device)
+        _check(self._lib.cpdr_linear_bwd(self._h, rows, K, N, *args, _opt("dx", out.get("dx"), x.shape, bf16, dev),
+                                         _opt("dw", out.get("dw"), w.shape, bf16, dev),
+                                         _opt("dbias", out.get("dbias"), (N,), torch.float32, dev),
+                                         *_space(workspace, dev), _raw_stream(stream, dev)))
         return out
 
     def check_device_status(self, stream=None):

@@ -379,31 +379,33 @@ constexpr int kNarrowThreads = 32 * 6;
 constexpr int kMaxSplit = 8;
 template <int QN>
 constexpr int kNarrowStage = (128 + QN) * kRBytes;
+// CTAs of an SM, and the stages that this leaves to each beside its sums.
 template <int QN>
-constexpr int kNarrowStages = (200 * 1024) / kNarrowStage<QN> < 12 ? (200 * 1024) / kNarrowStage<QN> : 12;
+constexpr int kNarrowPerSm = QN <= 32 ? 2 : 1;
 template <int QN>
-constexpr size_t kNarrowBytes = (size_t)kNarrowStages<QN> * kNarrowStage<QN> + 512 + 1024;
-static_assert(kNarrowBytes<16> <= 227 * 1024 && kNarrowBytes<128> <= 227 * 1024, "stages fit");
-static_assert(128 * 128 * 4 <= kNarrowStages<128> * kNarrowStage<128> && 128 * 64 * 4 <= kNarrowStages<64> * kNarrowStage<64>,
-              "the partial sums fit the stages' place");
-
+constexpr int kNarrowSums = (QN + kMaxSplit - 1) * 128 * (int)sizeof(float);   // columns rounded up to the split
+template <int QN>
+constexpr int kNarrowStages = (228 * 1024 / kNarrowPerSm<QN> - 3 * 1024 - kNarrowSums<QN>) / kNarrowStage<QN>;
 struct NarrowBars {
-    uint64_t full[12], empty[12], done;
+    uint64_t full[8], empty[8], done;
     Ctl ctl;
     uint32_t tmem;
 };
-static_assert(sizeof(NarrowBars) <= 512, "barriers");
+template <int QN>
+constexpr size_t kNarrowBytes = (size_t)kNarrowStages<QN> * kNarrowStage<QN> + kNarrowSums<QN> + sizeof(NarrowBars) + 1024;
+static_assert(kNarrowStages<16> <= 8 && kNarrowStages<64> <= 8 && kNarrowStages<128> >= 3, "stages and their barriers");
 
 // D here is transposed: lanes are rows of w (q of y), columns rows of x (p of
 // y).  grid: (split, tiles of 128 rows of w, tiles of QN rows of x), cluster (split, 1, 1)
 template <int QN, bool E4M3, bool A_MN>
-__global__ void __launch_bounds__(kNarrowThreads, 1)
+__global__ void __launch_bounds__(kNarrowThreads, kNarrowPerSm<QN>)
 narrow_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx, Args a) {
     constexpr int STAGES = kNarrowStages<QN>, STAGE = kNarrowStage<QN>;
     constexpr int COLS = QN < 32 ? 32 : QN;
     extern __shared__ unsigned char raw[];
     unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    NarrowBars &b = *reinterpret_cast<NarrowBars *>(base + STAGES * STAGE);
+    float *sums = reinterpret_cast<float *>(base + STAGES * STAGE);   // [columns of this CTA][split][128]
+    NarrowBars &b = *reinterpret_cast<NarrowBars *>(base + STAGES * STAGE + kNarrowSums<QN>);
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = gridDim.x, rank = blockIdx.x;
     const int64_t q0 = (int64_t)blockIdx.y * 128, p0 = (int64_t)blockIdx.z * QN;
@@ -424,6 +426,8 @@ narrow_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // waited for before the sums go out: the CTAs of the cluster have all begun
+    if (split > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     const uint32_t tmem = b.tmem;
     bool ok = true;
     float v[QN];
@@ -466,18 +470,26 @@ narrow_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
         for (int i = 0; i < QN; i += 16) tmem_ld16(at + i, *reinterpret_cast<float(*)[16]>(&v[i]));
         tmem_ld_wait();
     }
-    // the stages are free: every load was waited for by the products, and
-    // those by `done` (after a wait that gave up: time to land instead)
+    // after a wait that gave up, copies of this CTA may still be on their way
     if (b.ctl.abort)
         for (int i = 0; i < 1000; i++) __nanosleep(1000);
     const int row = threadIdx.x;   // of the 128 rows of w, threads 0 .. 127
     const int64_t q = q0 + row;
-    float *part = reinterpret_cast<float *>(base);   // [QN][128]
+    const int per = (QN + split - 1) / split;   // columns whose sums a CTA of the cluster takes
     if (split > 1) {
-        __syncthreads();
+        // every partial sum goes to the CTA that adds its column
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         if (w < 4) {
+            int owner = 0, at = 0;
+            uint32_t to = remote(sums + rank * 128 + row, 0);
 #pragma unroll
-            for (int i = 0; i < QN; i++) part[i * 128 + row] = v[i];
+            for (int i = 0; i < QN; i++) {
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + (uint32_t)(at * split * 512)), "f"(v[i]) : "memory");
+                if (++at == per) {
+                    at = 0;
+                    if (++owner < split) to = remote(sums + rank * 128 + row, owner);
+                }
+            }
         }
         cluster_sync();
     }
@@ -495,16 +507,13 @@ narrow_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
             a.y[o] = __float2bfloat16_rn(d);
         };
         if (split > 1) {
-            // this CTA's share of the columns, summed in the order of the CTAs
-            const int i1 = QN * (rank + 1) / split;
-            for (int i = QN * rank / split; i < i1 && p0 + i < a.P; i++) {
+            // this CTA's columns, each summed in the order of the CTAs
+            const int i0 = per * rank, n = min(per, QN - i0);
+#pragma unroll 2
+            for (int i = 0; i < n; i++) {
                 float d = 0.f;
-                for (int z = 0; z < split; z++) {
-                    float t;
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(t) : "r"(remote(&part[i * 128 + row], z)));
-                    d += t;
-                }
-                out(i, d);
+                for (int z = 0; z < split; z++) d += sums[(i * split + z) * 128 + row];
+                out(i0 + i, d);
             }
         } else {
 #pragma unroll
@@ -513,7 +522,6 @@ narrow_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
     }
     tc_fence_before();
     __syncthreads();
-    if (split > 1) cluster_sync();   // no CTA leaves while another may read its sums
     tc_fence_after();
     if (w == 5) tmem_dealloc(tmem, COLS);
 }
@@ -644,21 +652,23 @@ int narrow(const Operand &W, const Operand &X, Args a, int split, cudaStream_t s
 }
 
 // Which kernel runs a product whose rows p are rows of x, by an estimate of
-// its cycles: waves of tiles times what a tile costs.
+// its cycles.
 struct Choice {
     int qn = 0, split = 1;   // qn 0: wide_kernel
 };
 Choice choose(int64_t P, int64_t Q, int blocks, int sms) {
     auto up = [](int64_t x, int64_t d) { return (x + d - 1) / d; };
     Choice best;
-    double cost = (double)up(up(P, kTile) * up(Q, kTile), sms / 2) * (blocks * 520.0 + 4000.0);
+    // tiles one after the other; 512 cycles of the tensor cores per block
+    double cost = (double)up(up(P, kTile) * up(Q, kTile), sms / 2) * (blocks * 520.0 + 1500.0) + 6000.0;
     for (int qn = 16; qn <= 128; qn *= 2) {
         if (qn < 128 && P > qn) continue;
         if (up(Q, 128) > 65535 || up(P, qn) > 65535) continue;
-        const double block = std::max(2.0 * qn, (128 + qn) * kRBytes / 45.0);
-        for (int split = 1; split <= kMaxSplit && split <= blocks; split *= 2) {
-            const double waves = (double)up(up(P, qn) * up(Q, 128) * split, sms);
-            const double c = waves * (up(blocks, split) * block + 4000.0 + (split > 1 ? 1500.0 : 0.0));
+        const int64_t tiles = up(P, qn) * up(Q, 128);
+        const double block = std::max(2.0 * qn, (128 + qn) * kRBytes / 45.0);   // what an SM fetches in a cycle
+        for (int split = 1; split <= kMaxSplit && split <= blocks; split++) {
+            const int64_t per_sm = up(tiles * split, sms);
+            const double c = per_sm * (up(blocks, split) * block) + up(per_sm, qn <= 32 ? 2 : 1) * (4000.0 + (split > 1 ? 1500.0 : 0.0));
             if (c < cost) {
                 cost = c;
                 best.qn = qn;

@@ -326,9 +326,9 @@ cpdr_status cpdr_bwd(const cpdr_ctx *ctx, const void *q, const void *k, const vo
  * channel c and token t of a sequence, with a_t = exp(gate_t),
  *     h_t = a_t h_{t-1} + x_t,    y_t = h_t,
  * from h0 (or zero) at the sequence's start; hT is the state behind its last
- * token (h0, or zero, for an empty sequence).  gate is a natural-log gate of
- * any finite value or -infinity (a_t = 0: the state is dropped); x and h0
- * are finite.  Sequences and token layout are the context's (packed batches,
+ * token (h0, or zero, for an empty sequence).  gate is a natural-log gate, at
+ * most 88; -infinity is one (a_t = 0: the state is dropped).  x and h0 are
+ * finite.  Sequences and token layout are the context's (packed batches,
  * zigzag); its segments play no part.
  * Layout: x, y [B, T, channels] in the context's token order and input dtype;
  * gate [B, T, channels] fp32; h0, hT [N, channels] fp32, either may be NULL
