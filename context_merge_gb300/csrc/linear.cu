@@ -155,11 +155,28 @@ __device__ __forceinline__ void load_stage(uint32_t dst, const CUtensorMap *m, u
     }
 }
 
+// erfc(|z| / sqrt 2) by Abramowitz and Stegun 7.1.26, off by at most 1.5e-7:
+// a fifth of the code of erff, whose two branches made the epilogue longer
+// than the products (32768 x 2048 x 6144: 727 us with erff, 455 without GELU).
+// `e` becomes exp(-z^2 / 2).
+__device__ __forceinline__ float erfc_of(float z, float &e) {
+    const float t = __fdividef(1.f, fmaf(0.3275911f * 0.70710678118654752f, fabsf(z), 1.f));
+    e = __expf(-0.5f * z * z);
+    float p = fmaf(t, 1.061405429f, -1.453152027f);
+    p = fmaf(t, p, 1.421413741f);
+    p = fmaf(t, p, -0.284496736f);
+    p = fmaf(t, p, 0.254829592f);
+    return p * t * e;
+}
 // SiLU z sigmoid(z); the fast divide returns 0 once the denominator passes
-// 2^126, where the exact quotient is below 1e-36.  GELU z Phi(z), by erf.
+// 2^126, where the exact quotient is below 1e-36.  GELU z Phi(z).
 __device__ __forceinline__ float act_of(float z, int act) {
     if (act == 1) return __fdividef(z, 1.f + __expf(-z));
-    if (act == 2) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+    if (act == 2) {
+        float e;
+        const float h = 0.5f * z * erfc_of(z, e);   // z Phi(-|z|)
+        return z > 0.f ? z - h : h;
+    }
     return z;
 }
 __device__ __forceinline__ float act_grad(float z, int act) {
@@ -167,8 +184,9 @@ __device__ __forceinline__ float act_grad(float z, int act) {
         const float s = __fdividef(1.f, 1.f + __expf(-z));
         return s * fmaf(z, 1.f - s, 1.f);
     }
-    const float phi = 0.39894228040143268f * __expf(-0.5f * z * z);
-    return fmaf(z, phi, 0.5f * (1.f + erff(z * 0.70710678118654752f)));
+    float e;
+    const float h = 0.5f * erfc_of(z, e);
+    return fmaf(0.39894228040143268f * z, e, z > 0.f ? 1.f - h : h);
 }
 
 // ------------------------------------------------------------------ wide
@@ -383,17 +401,38 @@ constexpr int kNarrowStage = (128 + QN) * kRBytes;
 template <int QN>
 constexpr int kNarrowPerSm = QN <= 32 ? 2 : 1;
 template <int QN>
-constexpr int kNarrowSums = (QN + kMaxSplit - 1) * 128 * (int)sizeof(float);   // columns rounded up to the split
+constexpr int narrow_sums() {   // groups of 4 columns, rounded up to every split
+    int most = 0;
+    for (int s = 2; s <= kMaxSplit; s++) most = most > (QN / 4 + s - 1) / s * s ? most : (QN / 4 + s - 1) / s * s;
+    return most * 128 * 16;
+}
+template <int QN>
+constexpr int kNarrowSums = narrow_sums<QN>();
 template <int QN>
 constexpr int kNarrowStages = (228 * 1024 / kNarrowPerSm<QN> - 3 * 1024 - kNarrowSums<QN>) / kNarrowStage<QN>;
 struct NarrowBars {
-    uint64_t full[8], empty[8], done;
+    uint64_t full[8], empty[8], done, summed;
     Ctl ctl;
     uint32_t tmem;
 };
 template <int QN>
 constexpr size_t kNarrowBytes = (size_t)kNarrowStages<QN> * kNarrowStage<QN> + kNarrowSums<QN> + sizeof(NarrowBars) + 1024;
 static_assert(kNarrowStages<16> <= 8 && kNarrowStages<64> <= 8 && kNarrowStages<128> >= 3, "stages and their barriers");
+
+// The sum of a group of 4 columns over the CTAs of a cluster, in their order.
+template <int SPLIT>
+__device__ __forceinline__ void add_group(const float4 *s, float (&d)[4]) {
+    float4 u[SPLIT];
+#pragma unroll
+    for (int z = 0; z < SPLIT; z++) u[z] = s[z * 128];
+#pragma unroll
+    for (int z = 0; z < SPLIT; z++) {
+        d[0] += u[z].x;
+        d[1] += u[z].y;
+        d[2] += u[z].z;
+        d[3] += u[z].w;
+    }
+}
 
 // D here is transposed: lanes are rows of w (q of y), columns rows of x (p of
 // y).  grid: (split, tiles of 128 rows of w, tiles of QN rows of x), cluster (split, 1, 1)
@@ -404,25 +443,39 @@ narrow_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
     constexpr int COLS = QN < 32 ? 32 : QN;
     extern __shared__ unsigned char raw[];
     unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    float *sums = reinterpret_cast<float *>(base + STAGES * STAGE);   // [columns of this CTA][split][128]
+    float4 *sums = reinterpret_cast<float4 *>(base + STAGES * STAGE);   // [this CTA's groups of 4 columns][split][128 rows]
     NarrowBars &b = *reinterpret_cast<NarrowBars *>(base + STAGES * STAGE + kNarrowSums<QN>);
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = gridDim.x, rank = blockIdx.x;
     const int64_t q0 = (int64_t)blockIdx.y * 128, p0 = (int64_t)blockIdx.z * QN;
-    const int k0 = (int)((int64_t)a.blocks * rank / split), k1 = (int)((int64_t)a.blocks * (rank + 1) / split);
-    if (threadIdx.x == 0) {
-        b.ctl.abort = 0;
-        for (int s = 0; s < STAGES; s++) {
-            mbar_init(&b.full[s], 1);
-            mbar_init(&b.empty[s], 1);
+    const int k0 = (int)((int64_t)a.blocks * rank / split), n = (int)((int64_t)a.blocks * (rank + 1) / split) - k0;
+    auto load = [&](int it) {
+        const int s = it % STAGES;
+        mbar_arrive_expect_tx(&b.full[s], STAGE);
+        const uint32_t dst = smem_u32(base + s * STAGE), bar = smem_u32(&b.full[s]);
+        load_stage<1, A_MN, E4M3>(dst, &mw, bar, (int)q0, k0 + it);
+        load_stage<1, false, E4M3>(dst + 128 * kRBytes, &mx, bar, (int)p0, k0 + it);
+    };
+    if (w == 4) {
+        // the first loads do not wait for the rest to be set up
+        if (lane == 0) {
+            tma_prefetch_desc(&mw);
+            tma_prefetch_desc(&mx);
+            b.ctl.abort = 0;
+            for (int s = 0; s < STAGES; s++) {
+                mbar_init(&b.full[s], 1);
+                mbar_init(&b.empty[s], 1);
+            }
+            mbar_init(&b.done, 1);
+            mbar_init(&b.summed, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            for (int it = 0; it < min(n, STAGES); it++) load(it);
         }
-        mbar_init(&b.done, 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    if (w == 5) {
+    } else if (w == 5) {
         tmem_alloc(&b.tmem, COLS);
         tmem_relinquish();
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -433,14 +486,9 @@ narrow_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
     float v[QN];
     if (w == 4) {
         if (lane == 0) {
-            int it = 0;
-            for (int k = k0; k < k1; k++, it++) {
-                const int s = it % STAGES;
-                if (!mbar_wait(&b.empty[s], (uint32_t)(it / STAGES + 1) & 1u, &b.ctl, a.status, 170)) break;
-                mbar_arrive_expect_tx(&b.full[s], STAGE);
-                const uint32_t dst = smem_u32(base + s * STAGE), bar = smem_u32(&b.full[s]);
-                load_stage<1, A_MN, E4M3>(dst, &mw, bar, (int)q0, k);
-                load_stage<1, false, E4M3>(dst + 128 * kRBytes, &mx, bar, (int)p0, k);
+            for (int it = STAGES; it < n; it++) {
+                if (!mbar_wait(&b.empty[it % STAGES], (uint32_t)(it / STAGES + 1) & 1u, &b.ctl, a.status, 170)) break;
+                load(it);
             }
         }
         __syncwarp();
@@ -448,8 +496,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
         if (lane == 0) {
             constexpr uint32_t id = idesc_of<E4M3, A_MN, false>(128, QN);
             const uint64_t ad = stage_desc<A_MN>(smem_u32(base)), bd = stage_desc<false>(smem_u32(base + 128 * kRBytes));
-            int it = 0;
-            for (int k = k0; k < k1; k++, it++) {
+            for (int it = 0; it < n; it++) {
                 const int s = it % STAGES;
                 if (!mbar_wait(&b.full[s], (uint32_t)(it / STAGES) & 1u, &b.ctl, a.status, 171)) break;
                 tc_fence_after();
@@ -475,49 +522,78 @@ narrow_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
         for (int i = 0; i < 1000; i++) __nanosleep(1000);
     const int row = threadIdx.x;   // of the 128 rows of w, threads 0 .. 127
     const int64_t q = q0 + row;
-    const int per = (QN + split - 1) / split;   // columns whose sums a CTA of the cluster takes
+    // groups of 4 columns whose sums a CTA of the cluster takes
+    const int per = (QN / 4 + split - 1) / split, g0 = per * rank, groups = min(per, QN / 4 - g0);
+    const bool mine = w < 4 && q < a.Q && ok;
+    const float bias = mine && a.e.bias ? a.e.bias[q] : 0.f, ws = mine && a.e.ws ? a.e.ws[q] : 1.f;
     if (split > 1) {
-        // every partial sum goes to the CTA that adds its column
+        // every partial sum goes to the CTA that adds its group, which counts
+        // the bytes; no CTA leaves before all of its own have come
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         if (w < 4) {
+            if (threadIdx.x == 0 && groups > 0) mbar_arrive_expect_tx(&b.summed, (uint32_t)(groups * split * 2048));
             int owner = 0, at = 0;
-            uint32_t to = remote(sums + rank * 128 + row, 0);
+            uint32_t to = remote(sums + rank * 128 + row, 0), bar = remote(&b.summed, 0);
 #pragma unroll
-            for (int i = 0; i < QN; i++) {
-                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + (uint32_t)(at * split * 512)), "f"(v[i]) : "memory");
+            for (int i = 0; i < QN; i += 4) {
+                asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                                 to + (uint32_t)(at * split * 2048)),
+                             "f"(v[i]), "f"(v[i + 1]), "f"(v[i + 2]), "f"(v[i + 3]), "r"(bar)
+                             : "memory");
                 if (++at == per) {
                     at = 0;
-                    if (++owner < split) to = remote(sums + rank * 128 + row, owner);
+                    if (++owner < split) {
+                        to = remote(sums + rank * 128 + row, owner);
+                        bar = remote(&b.summed, owner);
+                    }
                 }
             }
+            if (groups > 0) ok = warp_wait_all(&b.summed, 0, &b.ctl, a.status, 173) && ok;
         }
-        cluster_sync();
     }
-    if (w < 4 && q < a.Q && ok) {
-        const float bias = a.e.bias ? a.e.bias[q] : 0.f, ws = a.e.ws ? a.e.ws[q] : 1.f;
-        auto out = [&](int i, float d) {
+    if (mine && ok) {
+        // four rows of x from column i on
+        auto out = [&](int i, float (&d)[4]) {
             const int64_t p = p0 + i;
-            if (p >= a.P) return;
-            if (a.e.ws) d *= a.e.xs[p] * ws;
-            if (a.e.bias) d += bias;
+            const int n = (int)min((int64_t)4, a.P - p);
             const int64_t o = p * a.Q + q;
-            if (a.e.has_z) a.z[o] = __float2bfloat16_rn(d);
-            d = act_of(d, a.e.act);
-            if (a.e.residual) d += __bfloat162float(a.e.residual[o]);
-            a.y[o] = __float2bfloat16_rn(d);
+            float r[4] = {};
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                if (j >= n) break;
+                if (a.e.residual) r[j] = __bfloat162float(a.e.residual[o + j * a.Q]);
+                if (a.e.ws) d[j] *= a.e.xs[p + j] * ws;
+                d[j] += bias;
+                if (a.e.has_z) a.z[o + j * a.Q] = __float2bfloat16_rn(d[j]);
+            }
+            if (a.e.act) {
+#pragma unroll
+                for (int j = 0; j < 4; j++) d[j] = act_of(d[j], a.e.act);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                if (j < n) a.y[o + j * a.Q] = __float2bfloat16_rn(d[j] + r[j]);
         };
         if (split > 1) {
-            // this CTA's columns, each summed in the order of the CTAs
-            const int i0 = per * rank, n = min(per, QN - i0);
-#pragma unroll 2
-            for (int i = 0; i < n; i++) {
-                float d = 0.f;
-                for (int z = 0; z < split; z++) d += sums[(i * split + z) * 128 + row];
-                out(i0 + i, d);
+            // this CTA's groups, each summed in the order of the CTAs
+            for (int i = 0; i < groups && p0 + 4 * (g0 + i) < a.P; i++) {
+                float d[4] = {};
+                const float4 *s = sums + i * split * 128 + row;
+                switch (split) {
+                    case 2: add_group<2>(s, d); break;
+                    case 3: add_group<3>(s, d); break;
+                    case 4: add_group<4>(s, d); break;
+                    case 5: add_group<5>(s, d); break;
+                    case 6: add_group<6>(s, d); break;
+                    case 7: add_group<7>(s, d); break;
+                    default: add_group<8>(s, d); break;
+                }
+                out(4 * (g0 + i), d);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < QN; i++) out(i, v[i]);
+            for (int i = 0; i < QN; i += 4)
+                if (p0 + i < a.P) out(i, *reinterpret_cast<float(*)[4]>(&v[i]));
         }
     }
     tc_fence_before();
@@ -659,16 +735,21 @@ struct Choice {
 Choice choose(int64_t P, int64_t Q, int blocks, int sms) {
     auto up = [](int64_t x, int64_t d) { return (x + d - 1) / d; };
     Choice best;
-    // tiles one after the other; 512 cycles of the tensor cores per block
-    double cost = (double)up(up(P, kTile) * up(Q, kTile), sms / 2) * (blocks * 520.0 + 1500.0) + 6000.0;
+    // tiles one after the other; 700 cycles to fetch a block and multiply
+    double cost = (double)up(up(P, kTile) * up(Q, kTile), sms / 2) * (blocks * 700.0 + 1500.0) + 9000.0;
     for (int qn = 16; qn <= 128; qn *= 2) {
         if (qn < 128 && P > qn) continue;
         if (up(Q, 128) > 65535 || up(P, qn) > 65535) continue;
         const int64_t tiles = up(P, qn) * up(Q, 128);
-        const double block = std::max(2.0 * qn, (128 + qn) * kRBytes / 45.0);   // what an SM fetches in a cycle
+        const int fit = qn <= 32 ? 2 : 1;
+        const double block = std::max(2.0 * qn, (128 + qn) * kRBytes / 30.0);   // what an SM fetches in a cycle
         for (int split = 1; split <= kMaxSplit && split <= blocks; split++) {
-            const int64_t per_sm = up(tiles * split, sms);
-            const double c = per_sm * (up(blocks, split) * block) + up(per_sm, qn <= 32 ? 2 : 1) * (4000.0 + (split > 1 ? 1500.0 : 0.0));
+            // a cluster of more than two finds no place on some of the last SMs
+            const int64_t room = (int64_t)sms * fit * (split > 2 ? 15 : 16) / 16;
+            const int64_t waves = up(tiles * split, room);
+            const double together = waves > 1 ? fit : (double)up(tiles * split, sms);
+            // what a partial sum costs to send and to add, 50 cycles a column
+            const double c = waves * (up(blocks, split) * block * together + 7000.0 + (split > 1 ? 1500.0 + 50.0 * qn : 15.0 * qn));
             if (c < cost) {
                 cost = c;
                 best.qn = qn;
