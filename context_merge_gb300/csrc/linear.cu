@@ -30,7 +30,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <type_traits>
 
 #include "cpdr_internal.hpp"
 #include "tc_common.cuh"
@@ -69,6 +68,14 @@ __device__ __forceinline__ uint32_t ctarank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// True in one thread of the warp, which the compiler then knows to be one: by
+// "lane == 0" it wraps every product and copy in a loop over the active
+// threads, 152 cycles a product where the tensor cores need 128.
+__device__ __forceinline__ bool elected() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
 // The shared-memory address of the same place in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t remote(const void *p, uint32_t rank) {
     uint32_t r;
@@ -101,6 +108,7 @@ __device__ __forceinline__ void tma_store(const CUtensorMap *m, uint32_t src, in
                  : "memory");
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
+// The stores of this thread have read their tiles.
 __device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
 template <int GROUP, bool E4M3>
@@ -155,37 +163,48 @@ __device__ __forceinline__ void load_stage(uint32_t dst, const CUtensorMap *m, u
     }
 }
 
-// erfc(|z| / sqrt 2) by Abramowitz and Stegun 7.1.26, off by at most 1.5e-7:
-// a fifth of the code of erff, whose two branches made the epilogue longer
-// than the products (32768 x 2048 x 6144: 727 us with erff, 455 without GELU).
-// `e` becomes exp(-z^2 / 2).
-__device__ __forceinline__ float erfc_of(float z, float &e) {
-    const float t = __fdividef(1.f, fmaf(0.3275911f * 0.70710678118654752f, fabsf(z), 1.f));
-    e = __expf(-0.5f * z * z);
-    float p = fmaf(t, 1.061405429f, -1.453152027f);
-    p = fmaf(t, p, 1.421413741f);
-    p = fmaf(t, p, -0.284496736f);
-    p = fmaf(t, p, 0.254829592f);
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float kLog2E = 1.44269504088896341f;
+
+// erfc(a / sqrt 2) / 2 for 0 <= a by Abramowitz and Stegun 7.1.26 (erfc off by
+// at most 1.5e-7): a third of the code of erff, whose two branches made the
+// epilogue longer than the products.  `e` becomes exp(-a^2 / 2).
+__device__ __forceinline__ float upper_tail(float a, float &e) {
+    const float t = rcp_fast(fmaf(0.3275911f * 0.70710678118654752f, a, 1.f));
+    e = exp2_fast(-0.5f * kLog2E * a * a);
+    float p = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
+    p = fmaf(t, p, 0.5f * 1.421413741f);
+    p = fmaf(t, p, 0.5f * -0.284496736f);
+    p = fmaf(t, p, 0.5f * 0.254829592f);
     return p * t * e;
 }
-// SiLU z sigmoid(z); the fast divide returns 0 once the denominator passes
-// 2^126, where the exact quotient is below 1e-36.  GELU z Phi(z).
-__device__ __forceinline__ float act_of(float z, int act) {
-    if (act == 1) return __fdividef(z, 1.f + __expf(-z));
-    if (act == 2) {
-        float e;
-        const float h = 0.5f * z * erfc_of(z, e);   // z Phi(-|z|)
-        return z > 0.f ? z - h : h;
-    }
-    return z;
+// SiLU z sigmoid(z); the quotient is 0 once its denominator passes 2^126, where
+// the exact one is below 1e-36.
+__device__ __forceinline__ float silu(float z) { return z * rcp_fast(1.f + exp2_fast(-kLog2E * z)); }
+// GELU z Phi(z) = max(z, 0) - |z| Phi(-|z|); past 40 the second term is zero.
+__device__ __forceinline__ float gelu(float z) {
+    float e, m;
+    const float a = fminf(fabsf(z), 40.f);
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(z), "f"(0.f));
+    return fmaf(-a, upper_tail(a, e), m);
 }
-__device__ __forceinline__ float act_grad(float z, int act) {
-    if (act == 1) {
-        const float s = __fdividef(1.f, 1.f + __expf(-z));
+template <int ACT>
+__device__ __forceinline__ float act_grad(float z) {
+    if (ACT == 1) {
+        const float s = rcp_fast(1.f + exp2_fast(-kLog2E * z));
         return s * fmaf(z, 1.f - s, 1.f);
     }
     float e;
-    const float h = 0.5f * erfc_of(z, e);
+    const float h = upper_tail(fabsf(z), e);
     return fmaf(0.39894228040143268f * z, e, z > 0.f ? 1.f - h : h);
 }
 
@@ -195,6 +214,7 @@ constexpr int kWideStages = 6;
 constexpr int kHalfStage = 128 * kRBytes;
 constexpr int kWideStage = 2 * kHalfStage;
 constexpr int kEpiWarps = 8;
+constexpr int kEpiCols = 256 / (kEpiWarps / 4);   // columns of a warp
 constexpr int kStaging = 32 * 128;       // a warp's 32 rows of 64 bf16
 constexpr int kWideThreads = 32 * (kEpiWarps + 2);
 constexpr size_t kWideBytes = (size_t)kWideStages * kWideStage + kEpiWarps * kStaging + 256 + 1024;
@@ -208,7 +228,9 @@ struct WideBars {
 static_assert(sizeof(WideBars) <= 256, "barriers");
 
 // Tiles in groups of 8 rows of tiles, column by column inside a group, so
-// that the tiles that run together share their operands in the L2.
+// that the tiles that run together share their operands in the L2.  (One B
+// fetched for two pairs by multicast, in clusters of 4: 0.92 to 1.09 of these
+// times, and 8 of the 152 SMs find no cluster: not worth a second kernel.)
 __device__ __forceinline__ void tile_at(const Args &a, int i, int &tp, int &tq) {
     const int per = 8 * a.tiles_q, g = i / per, r = i - g * per;
     const int rows = min(8, a.tiles_p - 8 * g);
@@ -239,11 +261,17 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (w == 8) {
+    if (w == kEpiWarps) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&b.tmem)), "r"(512)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
+    if (w == kEpiWarps + 1 && lane == 0) {
+        tma_prefetch_desc(&ma);
+        tma_prefetch_desc(&mb);
+        tma_prefetch_desc(&my);
+    }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     cluster_sync();
@@ -252,10 +280,8 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
 
     if (w == kEpiWarps) {
         // -------------------------------------------------------- loads
-        if (lane == 0) {
-            tma_prefetch_desc(&ma);
-            tma_prefetch_desc(&mb);
-            uint32_t full0 = remote(&b.full[0], 0);
+        if (elected()) {
+            const uint32_t full0 = remote(&b.full[0], 0);
             int it = 0;
             for (int t = pair; t < tiles && !b.ctl.abort; t += pairs) {
                 int tp, tq;
@@ -273,7 +299,7 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
         }
     } else if (w == kEpiWarps + 1) {
         // -------------------------------------------------------- products
-        if (rank == 0 && lane == 0) {
+        if (rank == 0 && elected()) {
             constexpr uint32_t id = idesc_of<E4M3, A_MN, B_MN>(256, 256);
             const uint64_t ad = stage_desc<A_MN>(smem_u32(base)), bd = stage_desc<B_MN>(smem_u32(base + kHalfStage));
             int it = 0, n = 0;
@@ -284,7 +310,6 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
                 for (int k = 0; k < a.blocks; k++, it++) {
                     const int s = it % kWideStages;
                     if (!mbar_wait(&b.full[s], (uint32_t)(it / kWideStages) & 1u, &b.ctl, a.status, 162)) break;
-                    tc_fence_after();
                     const uint64_t so = (uint64_t)(s * kWideStage) >> 4;
 #pragma unroll
                     for (int j = 0; j < 4; j++)
@@ -297,8 +322,11 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
         }
     } else {
         // -------------------------------------------------------- epilogue
-        // warp w: TMEM lanes (rows) 32 (w % 4) .. + 31, columns 128 (w / 4) .. + 127, 64 at a time
-        const int quad = w & 3, half = w >> 2;
+        // warp w: TMEM lanes (rows) 32 (w % 4) .. + 31, kEpiCols columns, 64 at
+        // a time.  The first piece's residual is on its way before the products
+        // are done, a later one's while the piece before it is worked on.
+        // Where z is wanted too, a first pass over the piece writes it.
+        const int quad = w & 3, c0 = (w >> 2) * kEpiCols;
         unsigned char *mine = staging + w * kStaging;
         const uint32_t empty0 = remote(&b.acc_empty[0], 0);
         int n = 0;
@@ -309,74 +337,98 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
             const int64_t p0 = (int64_t)tp * kTile + rank * 128 + quad * 32, p = p0 + lane;
             const bool row = p < a.P;
             const float xs = a.e.xs && row ? a.e.xs[p] : 1.f;
+            uint4 res[8];
+            auto fetch = [&](int64_t q0) {
+                const __nv_bfloat16 *src = a.e.residual + p * a.Q + q0;
+#pragma unroll
+                for (int g = 0; g < 8; g++) {
+                    res[g] = make_uint4(0, 0, 0, 0);
+                    if (row && q0 + 8 * g < a.Q) res[g] = vio::load16(src + 8 * g);
+                }
+            };
+            if (a.e.residual) fetch((int64_t)tq * kTile + c0);
             if (!warp_wait_all(&b.acc_full[acc], (uint32_t)(n >> 1) & 1u, &b.ctl, a.status, 163)) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int ch = 0; ch < 2; ch++) {
-                const int col = half * 128 + ch * 64;
-                const int64_t q0 = (int64_t)tq * kTile + col;
-                float v[2][32];
-                const uint32_t at = tmem + acc * 256 + col + ((uint32_t)(32 * quad) << 16);
-                tmem_ld32(at, v[0]);
-                tmem_ld32(at + 32, v[1]);
-                tmem_ld_wait();
-                if (ch == 1) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive_remote(empty0 + 8u * acc);
-                }
-                if (p0 >= a.P || q0 >= a.Q) continue;
-#pragma unroll
-                for (int g = 0; g < 8; g++) {
-                    float *u = &v[g >> 2][(g & 3) * 8];
-                    const int64_t q = q0 + 8 * g;
-                    const bool in = q < a.Q;   // Q % 8 == 0
-                    if (a.e.ws) {
-                        float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f), s1 = s0;
-                        if (in) {
-                            s0 = *reinterpret_cast<const float4 *>(a.e.ws + q);
-                            s1 = *reinterpret_cast<const float4 *>(a.e.ws + q + 4);
-                        }
-                        u[0] *= xs * s0.x; u[1] *= xs * s0.y; u[2] *= xs * s0.z; u[3] *= xs * s0.w;
-                        u[4] *= xs * s1.x; u[5] *= xs * s1.y; u[6] *= xs * s1.z; u[7] *= xs * s1.w;
-                    }
-                    if (a.e.bias && in) {
-                        const float4 s0 = *reinterpret_cast<const float4 *>(a.e.bias + q);
-                        const float4 s1 = *reinterpret_cast<const float4 *>(a.e.bias + q + 4);
-                        u[0] += s0.x; u[1] += s0.y; u[2] += s0.z; u[3] += s0.w;
-                        u[4] += s1.x; u[5] += s1.y; u[6] += s1.z; u[7] += s1.w;
-                    }
-                }
-                auto put = [&](const CUtensorMap *m) {
+            for (int c = c0; c < c0 + kEpiCols; c += 64) {
+                const int64_t q0 = (int64_t)tq * kTile + c;
+                const bool any = p0 < a.P && q0 < a.Q;
+#pragma unroll 1
+                for (int last = a.e.has_z ? 0 : 1; last < 2; last++) {
                     if (lane == 0) tma_store_wait();   // the staging tile has been read
                     __syncwarp();
 #pragma unroll
-                    for (int g = 0; g < 8; g++) {
-                        const float *u = &v[g >> 2][(g & 3) * 8];
-                        *reinterpret_cast<uint4 *>(mine + sw128(lane, g)) =
-                            make_uint4(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]), pack_bf16(u[4], u[5]), pack_bf16(u[6], u[7]));
+                    for (int ch = 0; ch < 2; ch++) {
+                        float v[32];
+                        tmem_ld32(tmem + acc * 256 + c + ch * 32 + ((uint32_t)(32 * quad) << 16), v);
+                        float4 s[8];
+                        if (a.e.ws) {
+#pragma unroll
+                            for (int g = 0; g < 8; g++) {
+                                const int64_t q = q0 + ch * 32 + 4 * g;   // Q % 8 == 0
+                                s[g] = q < a.Q ? *reinterpret_cast<const float4 *>(a.e.ws + q) : make_float4(0.f, 0.f, 0.f, 0.f);
+                            }
+                        }
+                        tmem_ld_wait();
+                        if (last && ch == 1 && c + 64 == c0 + kEpiCols) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) arrive_remote(empty0 + 8u * acc);
+                        }
+                        if (!any) continue;
+                        if (a.e.ws) {
+#pragma unroll
+                            for (int g = 0; g < 8; g++) {
+                                v[4 * g] *= xs * s[g].x;
+                                v[4 * g + 1] *= xs * s[g].y;
+                                v[4 * g + 2] *= xs * s[g].z;
+                                v[4 * g + 3] *= xs * s[g].w;
+                            }
+                        }
+                        if (a.e.bias) {
+#pragma unroll
+                            for (int g = 0; g < 8; g++) {
+                                const int64_t q = q0 + ch * 32 + 4 * g;
+                                s[g] = q < a.Q ? *reinterpret_cast<const float4 *>(a.e.bias + q) : make_float4(0.f, 0.f, 0.f, 0.f);
+                            }
+#pragma unroll
+                            for (int g = 0; g < 8; g++) {
+                                v[4 * g] += s[g].x;
+                                v[4 * g + 1] += s[g].y;
+                                v[4 * g + 2] += s[g].z;
+                                v[4 * g + 3] += s[g].w;
+                            }
+                        }
+                        if (last) {
+                            if (a.e.act == 1) {
+#pragma unroll
+                                for (int i = 0; i < 32; i++) v[i] = silu(v[i]);
+                            } else if (a.e.act == 2) {
+#pragma unroll
+                                for (int i = 0; i < 32; i++) v[i] = gelu(v[i]);
+                            }
+                            if (a.e.residual) {
+#pragma unroll
+                                for (int g = 0; g < 4; g++) {
+                                    float r[8];
+                                    vio::widen16(res[ch * 4 + g], r);
+#pragma unroll
+                                    for (int i = 0; i < 8; i++) v[g * 8 + i] += r[i];
+                                }
+                                if (ch == 1 && c + 64 < c0 + kEpiCols) fetch(q0 + 64);
+                            }
+                        }
+#pragma unroll
+                        for (int g = 0; g < 4; g++) {
+                            const float *u = &v[g * 8];
+                            *reinterpret_cast<uint4 *>(mine + sw128(lane, ch * 4 + g)) = make_uint4(
+                                pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]), pack_bf16(u[4], u[5]), pack_bf16(u[6], u[7]));
+                        }
                     }
                     fence_async_smem();
                     __syncwarp();
-                    if (lane == 0) tma_store(m, smem_u32(mine), (int)q0, (int)p0);
-                };
-                if (a.e.has_z) put(&mz);
-                if (a.e.act) {
-#pragma unroll
-                    for (int i = 0; i < 64; i++) v[i >> 5][i & 31] = act_of(v[i >> 5][i & 31], a.e.act);
+                    if (lane == 0 && any) tma_store(last ? &my : &mz, smem_u32(mine), (int)q0, (int)p0);
                 }
-                if (a.e.residual && row) {
-                    const __nv_bfloat16 *res = a.e.residual + p * a.Q + q0;
-#pragma unroll
-                    for (int g = 0; g < 8; g++) {
-                        if (q0 + 8 * g >= a.Q) break;
-                        float r[8];
-                        vio::widen16(vio::load16(res + 8 * g), r);
-#pragma unroll
-                        for (int i = 0; i < 8; i++) v[g >> 2][(g & 3) * 8 + i] += r[i];
-                    }
-                }
-                put(&my);
             }
         }
         if (lane == 0) tma_store_wait();
@@ -389,7 +441,7 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
     __syncthreads();
     cluster_sync();
     tc_fence_after();
-    if (w == 8) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    if (w == kEpiWarps) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
 // ------------------------------------------------------------------ narrow
@@ -445,7 +497,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
     unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     float4 *sums = reinterpret_cast<float4 *>(base + STAGES * STAGE);   // [this CTA's groups of 4 columns][split][128 rows]
     NarrowBars &b = *reinterpret_cast<NarrowBars *>(base + STAGES * STAGE + kNarrowSums<QN>);
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int w = threadIdx.x >> 5;
     const int split = gridDim.x, rank = blockIdx.x;
     const int64_t q0 = (int64_t)blockIdx.y * 128, p0 = (int64_t)blockIdx.z * QN;
     const int k0 = (int)((int64_t)a.blocks * rank / split), n = (int)((int64_t)a.blocks * (rank + 1) / split) - k0;
@@ -458,7 +510,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
     };
     if (w == 4) {
         // the first loads do not wait for the rest to be set up
-        if (lane == 0) {
+        if (elected()) {
             tma_prefetch_desc(&mw);
             tma_prefetch_desc(&mx);
             b.ctl.abort = 0;
@@ -485,7 +537,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
     bool ok = true;
     float v[QN];
     if (w == 4) {
-        if (lane == 0) {
+        if (elected()) {
             for (int it = STAGES; it < n; it++) {
                 if (!mbar_wait(&b.empty[it % STAGES], (uint32_t)(it / STAGES + 1) & 1u, &b.ctl, a.status, 170)) break;
                 load(it);
@@ -493,13 +545,12 @@ narrow_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
         }
         __syncwarp();
     } else if (w == 5) {
-        if (lane == 0) {
+        if (elected()) {
             constexpr uint32_t id = idesc_of<E4M3, A_MN, false>(128, QN);
             const uint64_t ad = stage_desc<A_MN>(smem_u32(base)), bd = stage_desc<false>(smem_u32(base + 128 * kRBytes));
             for (int it = 0; it < n; it++) {
                 const int s = it % STAGES;
                 if (!mbar_wait(&b.full[s], (uint32_t)(it / STAGES) & 1u, &b.ctl, a.status, 171)) break;
-                tc_fence_after();
                 const uint64_t so = (uint64_t)(s * STAGE) >> 4;
 #pragma unroll
                 for (int j = 0; j < 4; j++)
@@ -568,7 +619,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
             }
             if (a.e.act) {
 #pragma unroll
-                for (int j = 0; j < 4; j++) d[j] = act_of(d[j], a.e.act);
+                for (int j = 0; j < 4; j++) d[j] = a.e.act == 1 ? silu(d[j]) : gelu(d[j]);
             }
 #pragma unroll
             for (int j = 0; j < 4; j++)
@@ -605,29 +656,43 @@ narrow_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
 // ------------------------------------------------------------------ dz
 // dz = dy act'(z), rounded once, and its column sums over blocks of rows
 // (from the unrounded values).  A block is 256 columns by `per` rows, a
-// thread 8 columns of every 8th row.
+// thread 8 columns of every 8th row, four rows' loads at a time.
+template <int ACT>
 __global__ void __launch_bounds__(256)
-dz_kernel(const __nv_bfloat16 *__restrict__ dy, const __nv_bfloat16 *__restrict__ z, int act, int64_t rows, int width,
-          int per, __nv_bfloat16 *__restrict__ dz, float *__restrict__ part) {
+dz_kernel(const __nv_bfloat16 *__restrict__ dy, const __nv_bfloat16 *__restrict__ z, int64_t rows, int width, int per,
+          __nv_bfloat16 *__restrict__ dz, float *__restrict__ part) {
+    constexpr int AHEAD = 4;
     __shared__ float sh[8][256];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int col = blockIdx.y * 256 + tx * 8;
     const int64_t r0 = (int64_t)blockIdx.x * per, r1 = min(rows, r0 + per);
     float sum[8] = {};
     if (col < width) {
-#pragma unroll 4
-        for (int64_t r = r0 + ty; r < r1; r += 8) {
-            float d[8];
-            vio::widen16(vio::load16(dy + r * width + col), d);
-            if (act) {
-                float u[8];
-                vio::widen16(vio::load16(z + r * width + col), u);
+        for (int64_t r = r0 + ty; r < r1; r += 8 * AHEAD) {
+            uint4 dr[AHEAD], zr[AHEAD];
 #pragma unroll
-                for (int i = 0; i < 8; i++) d[i] *= act_grad(u[i], act);
-                vio::store16(dz + r * width + col, d);
+            for (int j = 0; j < AHEAD; j++) {
+                dr[j] = zr[j] = make_uint4(0, 0, 0, 0);
+                if (r + 8 * j < r1) {
+                    dr[j] = vio::load16(dy + (r + 8 * j) * width + col);
+                    if (ACT) zr[j] = vio::load16(z + (r + 8 * j) * width + col);
+                }
             }
 #pragma unroll
-            for (int i = 0; i < 8; i++) sum[i] += d[i];
+            for (int j = 0; j < AHEAD; j++) {
+                if (r + 8 * j >= r1) break;
+                float d[8];
+                vio::widen16(dr[j], d);
+                if (ACT) {
+                    float u[8];
+                    vio::widen16(zr[j], u);
+#pragma unroll
+                    for (int i = 0; i < 8; i++) d[i] *= act_grad<ACT>(u[i]);
+                    vio::store16(dz + (r + 8 * j) * width + col, d);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; i++) sum[i] += d[i];
+            }
         }
     }
     if (!part) return;
@@ -660,7 +725,7 @@ EncodeTiledFn encoder() {
     return fn;
 }
 
-// [rows, cols] row-major, box {bx, by}, 128-byte swizzle; what lies outside reads as zero.
+// [rows, cols] row-major, box {bx, by}; what lies outside reads as zero and is not written.
 bool encode(CUtensorMap *m, const void *p, bool e4m3, int64_t rows, int64_t cols, int bx, int by) {
     EncodeTiledFn fn = encoder();
     if (!fn) return false;
@@ -685,6 +750,7 @@ bool encode(CUtensorMap *m, const Operand &o, bool e4m3, int tile_rows) {
     return o.mn ? encode(m, o.p, e4m3, o.red, o.rows, 64, 64) : encode(m, o.p, e4m3, o.rows, o.red, e4m3 ? 128 : 64, tile_rows);
 }
 
+
 template <typename K>
 int launch_cluster(K kernel, dim3 grid, int threads, int cluster, size_t bytes, cudaStream_t st, void **args) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
@@ -703,14 +769,16 @@ int launch_cluster(K kernel, dim3 grid, int threads, int cluster, size_t bytes, 
     return (int)cudaLaunchKernelExC(&cfg, (const void *)kernel, args);
 }
 
+int64_t up(int64_t x, int64_t d) { return (x + d - 1) / d; }
+
 template <bool E4M3, bool A_MN, bool B_MN>
 int wide(const Operand &A, const Operand &B, Args a, void *y, void *z, int sms, cudaStream_t st) {
     CUtensorMap ma, mb, my, mz;
     if (!encode(&ma, A, E4M3, 128) || !encode(&mb, B, E4M3, 128) || !encode(&my, y, false, a.P, a.Q, 64, 32) ||
         !encode(&mz, z ? z : y, false, a.P, a.Q, 64, 32))
         return (int)cudaErrorInvalidValue;
-    a.tiles_p = (int)((a.P + kTile - 1) / kTile);
-    a.tiles_q = (int)((a.Q + kTile - 1) / kTile);
+    a.tiles_p = (int)up(a.P, kTile);
+    a.tiles_q = (int)up(a.Q, kTile);
     const int64_t tiles = (int64_t)a.tiles_p * a.tiles_q;
     if (tiles > (int64_t)0x3fffffff) return (int)cudaErrorInvalidValue;
     const int pairs = (int)std::min<int64_t>(tiles, sms / 2);
@@ -733,10 +801,9 @@ struct Choice {
     int qn = 0, split = 1;   // qn 0: wide_kernel
 };
 Choice choose(int64_t P, int64_t Q, int blocks, int sms) {
-    auto up = [](int64_t x, int64_t d) { return (x + d - 1) / d; };
     Choice best;
-    // tiles one after the other; 700 cycles to fetch a block and multiply
-    double cost = (double)up(up(P, kTile) * up(Q, kTile), sms / 2) * (blocks * 700.0 + 1500.0) + 9000.0;
+    // tiles one after the other; 590 cycles for a block (512 are the products')
+    double cost = (double)up(up(P, kTile) * up(Q, kTile), sms / 2) * (blocks * 590.0 + 1500.0) + 9000.0;
     for (int qn = 16; qn <= 128; qn *= 2) {
         if (qn < 128 && P > qn) continue;
         if (up(Q, 128) > 65535 || up(P, qn) > 65535) continue;
@@ -813,8 +880,9 @@ int launch_linear_bwd(const cpdr_ctx *c, int64_t rows, int K, int N, const void 
     if (act || dbias) {
         const int per = dz_rows_per_block(rows, N, sms);
         const int64_t parts = (rows + per - 1) / per;
-        dz_kernel<<<dim3((unsigned)parts, (unsigned)((N + 255) / 256)), 256, 0, st>>>(
-            (const __nv_bfloat16 *)dy, (const __nv_bfloat16 *)z, act, rows, N, per, (__nv_bfloat16 *)dz, dbias ? part : nullptr);
+        auto kernel = act == 0 ? dz_kernel<0> : act == 1 ? dz_kernel<1> : dz_kernel<2>;
+        kernel<<<dim3((unsigned)parts, (unsigned)((N + 255) / 256)), 256, 0, st>>>(
+            (const __nv_bfloat16 *)dy, (const __nv_bfloat16 *)z, rows, N, per, (__nv_bfloat16 *)dz, dbias ? part : nullptr);
         rc = (int)cudaGetLastError();
         if (rc) return rc;
         if (dbias) rc = launch_column_sums(part, (int)parts, N, dbias, stream);
