@@ -45,7 +45,7 @@ constexpr int kRBytes = 128;   // bytes of r in a stage: 64 bf16 or 128 e4m3
 struct Epilogue {
     const float *bias;       // [q] or NULL
     const float *xs, *ws;    // scales of e4m3 rows, or NULL
-    const __nv_bfloat16 *residual;   // [p, q] or NULL
+    const __nv_bfloat16 *residual;   // [p, q] or NULL (wide_kernel has it as a tensor map)
     int act;                 // 0 none, 1 SiLU, 2 GELU
     int has_z;               // the value before the activation is an output too
 };
@@ -68,7 +68,7 @@ __device__ __forceinline__ uint32_t ctarank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// True in one thread of the warp, which the compiler then knows to be one: by
+// True in one thread of the warp, always the same, which the compiler then knows to be one: by
 // "lane == 0" it wraps every product and copy in a loop over the active
 // threads, 152 cycles a product where the tensor cores need 128.
 __device__ __forceinline__ bool elected() {
@@ -197,6 +197,23 @@ __device__ __forceinline__ float gelu(float z) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(z), "f"(0.f));
     return fmaf(-a, upper_tail(a, e), m);
 }
+// The same for two values.
+__device__ __forceinline__ float2 gelu2(float2 z) {
+    using namespace vio;
+    const float2 a = make_float2(fminf(fabsf(z.x), 40.f), fminf(fabsf(z.y), 40.f));
+    const float2 d = fma2(a, both(0.3275911f * 0.70710678118654752f), both(1.f));
+    const float2 t = make_float2(rcp_fast(d.x), rcp_fast(d.y));
+    const float2 x = mul2(mul2(a, both(-0.5f * kLog2E)), a);
+    const float2 e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+    float2 p = fma2(t, both(0.5f * 1.061405429f), both(0.5f * -1.453152027f));
+    p = fma2(t, p, both(0.5f * 1.421413741f));
+    p = fma2(t, p, both(0.5f * -0.284496736f));
+    p = fma2(t, p, both(0.5f * 0.254829592f));
+    float2 m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m.x) : "f"(z.x), "f"(0.f));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m.y) : "f"(z.y), "f"(0.f));
+    return fma2(mul2(mul2(p, t), e), mul2(a, both(-1.f)), m);
+}
 template <int ACT>
 __device__ __forceinline__ float act_grad(float z) {
     if (ACT == 1) {
@@ -210,18 +227,27 @@ __device__ __forceinline__ float act_grad(float z) {
 
 // ------------------------------------------------------------------ wide
 constexpr int kTile = 256;               // rows and columns of a pair's tile
-constexpr int kWideStages = 6;
+// With a residual, a staging tile for each piece of a warp's columns (the
+// residual waits there) and a stage less; without, one tile and six stages
+// (32768 x 2048 x 6144: 417 us, with five stages 434).
+template <bool RES>
+constexpr int kWideStages = RES ? 5 : 6;
 constexpr int kHalfStage = 128 * kRBytes;
 constexpr int kWideStage = 2 * kHalfStage;
 constexpr int kEpiWarps = 8;
-constexpr int kEpiCols = 256 / (kEpiWarps / 4);   // columns of a warp
-constexpr int kStaging = 32 * 128;       // a warp's 32 rows of 64 bf16
+constexpr int kEpiCols = 256 / (kEpiWarps / 4);   // columns of a warp: two pieces of 64
+static_assert(kEpiCols == 128, "two pieces");
+constexpr int kPiece = 32 * 128;         // 32 rows of 64 bf16
+template <bool RES>
+constexpr int kStaging = RES ? 2 * kPiece : kPiece;   // a warp's
 constexpr int kWideThreads = 32 * (kEpiWarps + 2);
-constexpr size_t kWideBytes = (size_t)kWideStages * kWideStage + kEpiWarps * kStaging + 256 + 1024;
-static_assert(kWideBytes <= 227 * 1024, "a CTA's stages and staging fit its shared memory");
+template <bool RES>
+constexpr size_t kWideBytes = (size_t)kWideStages<RES> * kWideStage + kEpiWarps * kStaging<RES> + 256 + 1024;
+static_assert(kWideBytes<true> <= 227 * 1024 && kWideBytes<false> <= 227 * 1024,
+              "a CTA's stages and staging fit its shared memory");
 
 struct WideBars {
-    uint64_t full[kWideStages], empty[kWideStages], acc_full[2], acc_empty[2];
+    uint64_t full[6], empty[6], acc_full[2], acc_empty[2], residual[kEpiWarps];
     Ctl ctl;
     uint32_t tmem;
 };
@@ -238,20 +264,22 @@ __device__ __forceinline__ void tile_at(const Args &a, int i, int &tp, int &tq) 
     tp = 8 * g + (r - tq * rows);
 }
 
-template <bool E4M3, bool A_MN, bool B_MN>
+template <bool E4M3, bool A_MN, bool B_MN, bool RES>
 __global__ void __launch_bounds__(kWideThreads, 1)
 wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
-            const __grid_constant__ CUtensorMap my, const __grid_constant__ CUtensorMap mz, Args a) {
+            const __grid_constant__ CUtensorMap my, const __grid_constant__ CUtensorMap mz,
+            const __grid_constant__ CUtensorMap mr, Args a) {
+    constexpr int STAGES = kWideStages<RES>;
     extern __shared__ unsigned char raw[];
     unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    unsigned char *staging = base + kWideStages * kWideStage;
-    WideBars &b = *reinterpret_cast<WideBars *>(staging + kEpiWarps * kStaging);
+    unsigned char *staging = base + STAGES * kWideStage;
+    WideBars &b = *reinterpret_cast<WideBars *>(staging + kEpiWarps * kStaging<RES>);
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = ctarank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, tiles = a.tiles_p * a.tiles_q;
     if (threadIdx.x == 0) {
         b.ctl.abort = 0;
-        for (int s = 0; s < kWideStages; s++) {
+        for (int s = 0; s < STAGES; s++) {
             mbar_init(&b.full[s], 1);
             mbar_init(&b.empty[s], 1);
         }
@@ -259,6 +287,7 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
             mbar_init(&b.acc_full[s], 1);
             mbar_init(&b.acc_empty[s], 2 * kEpiWarps);
         }
+        for (int s = 0; s < kEpiWarps; s++) mbar_init(&b.residual[s], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (w == kEpiWarps) {
@@ -288,8 +317,8 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
                 tile_at(a, t, tp, tq);
                 const int p0 = tp * kTile + (int)rank * 128, q0 = tq * kTile + (int)rank * 128;
                 for (int k = 0; k < a.blocks; k++, it++) {
-                    const int s = it % kWideStages;
-                    if (!mbar_wait(&b.empty[s], (uint32_t)(it / kWideStages + 1) & 1u, &b.ctl, a.status, 160)) break;
+                    const int s = it % STAGES;
+                    if (!mbar_wait(&b.empty[s], (uint32_t)(it / STAGES + 1) & 1u, &b.ctl, a.status, 160)) break;
                     if (rank == 0) mbar_arrive_expect_tx(&b.full[s], 2 * kWideStage);
                     const uint32_t dst = smem_u32(base + s * kWideStage), bar = full0 + 8u * s;
                     load_stage<2, A_MN, E4M3>(dst, &ma, bar, p0, k);
@@ -308,8 +337,8 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
                 if (!mbar_wait(&b.acc_empty[acc], (uint32_t)((n >> 1) + 1) & 1u, &b.ctl, a.status, 161)) break;
                 tc_fence_after();
                 for (int k = 0; k < a.blocks; k++, it++) {
-                    const int s = it % kWideStages;
-                    if (!mbar_wait(&b.full[s], (uint32_t)(it / kWideStages) & 1u, &b.ctl, a.status, 162)) break;
+                    const int s = it % STAGES;
+                    if (!mbar_wait(&b.full[s], (uint32_t)(it / STAGES) & 1u, &b.ctl, a.status, 162)) break;
                     const uint64_t so = (uint64_t)(s * kWideStage) >> 4;
 #pragma unroll
                     for (int j = 0; j < 4; j++)
@@ -322,116 +351,119 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
         }
     } else {
         // -------------------------------------------------------- epilogue
-        // warp w: TMEM lanes (rows) 32 (w % 4) .. + 31, kEpiCols columns, 64 at
-        // a time.  The first piece's residual is on its way before the products
-        // are done, a later one's while the piece before it is worked on.
-        // Where z is wanted too, a first pass over the piece writes it.
+        // warp w: TMEM lanes (rows) 32 (w % 4) .. + 31, columns 128 (w / 4) ..
+        // + 127, in two pieces of 64.  The residual's pieces come into the
+        // staging tiles by TMA while the products run (a lane owns a row, and 32
+        // rows are 32 lines to a load instruction: fetched by loads they took
+        // 3000 cycles of a tile), and y takes their place.
+        // Where z is wanted too, a second pass over the piece writes it.
         const int quad = w & 3, c0 = (w >> 2) * kEpiCols;
-        unsigned char *mine = staging + w * kStaging;
+        unsigned char *mine = staging + w * kStaging<RES>;
         const uint32_t empty0 = remote(&b.acc_empty[0], 0);
-        int n = 0;
+        int n = 0, fetched = 0;
         for (int t = pair; t < tiles; t += pairs, n++) {
             const int acc = n & 1;
             int tp, tq;
             tile_at(a, t, tp, tq);
             const int64_t p0 = (int64_t)tp * kTile + rank * 128 + quad * 32, p = p0 + lane;
-            const bool row = p < a.P;
-            const float xs = a.e.xs && row ? a.e.xs[p] : 1.f;
-            uint4 res[8];
-            auto fetch = [&](int64_t q0) {
-                const __nv_bfloat16 *src = a.e.residual + p * a.Q + q0;
+            const int64_t q0 = (int64_t)tq * kTile + c0;
+            const float xs = a.e.xs && p < a.P ? a.e.xs[p] : 1.f;
+            const int pieces = p0 < a.P ? (q0 + 64 < a.Q ? 2 : q0 < a.Q ? 1 : 0) : 0;   // that hold any of D
+            if (RES && pieces && elected()) {
+                tma_store_wait();   // the staging tiles have been read
+                const uint32_t bar = smem_u32(&b.residual[w]);
+                mbar_arrive_expect_tx(&b.residual[w], pieces * kPiece);
+                for (int i = 0; i < pieces; i++)
+                    tma_load<1>(smem_u32(mine + i * kPiece), &mr, bar, (int)q0 + 64 * i, (int)p0);
+            }
+            __syncwarp();
+            // scales and bias of 32 columns, the next ones' on their way while these are used
+            float4 sc[8], bi[8];
+            auto columns = [&](int64_t q) {
 #pragma unroll
                 for (int g = 0; g < 8; g++) {
-                    res[g] = make_uint4(0, 0, 0, 0);
-                    if (row && q0 + 8 * g < a.Q) res[g] = vio::load16(src + 8 * g);
+                    const bool in = q + 4 * g < a.Q;   // Q % 8 == 0
+                    sc[g] = bi[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (a.e.ws && in) sc[g] = *reinterpret_cast<const float4 *>(a.e.ws + q + 4 * g);
+                    if (a.e.bias && in) bi[g] = *reinterpret_cast<const float4 *>(a.e.bias + q + 4 * g);
                 }
             };
-            if (a.e.residual) fetch((int64_t)tq * kTile + c0);
+            columns(q0);
             if (!warp_wait_all(&b.acc_full[acc], (uint32_t)(n >> 1) & 1u, &b.ctl, a.status, 163)) break;
             tc_fence_after();
+            if (RES && pieces && !warp_wait_all(&b.residual[w], (uint32_t)(fetched++) & 1u, &b.ctl, a.status, 164)) break;
 #pragma unroll 1
-            for (int c = c0; c < c0 + kEpiCols; c += 64) {
-                const int64_t q0 = (int64_t)tq * kTile + c;
-                const bool any = p0 < a.P && q0 < a.Q;
+            for (int i = 0; i < 2; i++) {
+                unsigned char *tile = RES ? mine + i * kPiece : mine;
 #pragma unroll 1
-                for (int last = a.e.has_z ? 0 : 1; last < 2; last++) {
-                    if (lane == 0) tma_store_wait();   // the staging tile has been read
-                    __syncwarp();
+                for (int pass = 0; pass <= a.e.has_z; pass++) {
+                    if (!RES || pass) {
+                        if (elected()) tma_store_wait();   // the staging tile has been read
+                        __syncwarp();
+                    }
+                    if (pass) columns(q0 + 64 * i);
 #pragma unroll
                     for (int ch = 0; ch < 2; ch++) {
                         float v[32];
-                        tmem_ld32(tmem + acc * 256 + c + ch * 32 + ((uint32_t)(32 * quad) << 16), v);
-                        float4 s[8];
-                        if (a.e.ws) {
-#pragma unroll
-                            for (int g = 0; g < 8; g++) {
-                                const int64_t q = q0 + ch * 32 + 4 * g;   // Q % 8 == 0
-                                s[g] = q < a.Q ? *reinterpret_cast<const float4 *>(a.e.ws + q) : make_float4(0.f, 0.f, 0.f, 0.f);
-                            }
-                        }
+                        tmem_ld32(tmem + acc * 256 + c0 + 64 * i + 32 * ch + ((uint32_t)(32 * quad) << 16), v);
                         tmem_ld_wait();
-                        if (last && ch == 1 && c + 64 == c0 + kEpiCols) {
+                        if (i == 1 && ch == 1 && pass == a.e.has_z) {
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0) arrive_remote(empty0 + 8u * acc);
                         }
-                        if (!any) continue;
+                        if (i >= pieces) continue;
                         if (a.e.ws) {
 #pragma unroll
                             for (int g = 0; g < 8; g++) {
-                                v[4 * g] *= xs * s[g].x;
-                                v[4 * g + 1] *= xs * s[g].y;
-                                v[4 * g + 2] *= xs * s[g].z;
-                                v[4 * g + 3] *= xs * s[g].w;
+                                v[4 * g] *= xs * sc[g].x;
+                                v[4 * g + 1] *= xs * sc[g].y;
+                                v[4 * g + 2] *= xs * sc[g].z;
+                                v[4 * g + 3] *= xs * sc[g].w;
                             }
                         }
-                        if (a.e.bias) {
 #pragma unroll
-                            for (int g = 0; g < 8; g++) {
-                                const int64_t q = q0 + ch * 32 + 4 * g;
-                                s[g] = q < a.Q ? *reinterpret_cast<const float4 *>(a.e.bias + q) : make_float4(0.f, 0.f, 0.f, 0.f);
-                            }
-#pragma unroll
-                            for (int g = 0; g < 8; g++) {
-                                v[4 * g] += s[g].x;
-                                v[4 * g + 1] += s[g].y;
-                                v[4 * g + 2] += s[g].z;
-                                v[4 * g + 3] += s[g].w;
-                            }
+                        for (int g = 0; g < 8; g++) {
+                            v[4 * g] += bi[g].x;
+                            v[4 * g + 1] += bi[g].y;
+                            v[4 * g + 2] += bi[g].z;
+                            v[4 * g + 3] += bi[g].w;
                         }
-                        if (last) {
+                        columns(q0 + 64 * i + 32 * ch + 32);
+                        if (pass == 0) {
                             if (a.e.act == 1) {
 #pragma unroll
-                                for (int i = 0; i < 32; i++) v[i] = silu(v[i]);
+                                for (int j = 0; j < 32; j++) v[j] = silu(v[j]);
                             } else if (a.e.act == 2) {
 #pragma unroll
-                                for (int i = 0; i < 32; i++) v[i] = gelu(v[i]);
-                            }
-                            if (a.e.residual) {
-#pragma unroll
-                                for (int g = 0; g < 4; g++) {
-                                    float r[8];
-                                    vio::widen16(res[ch * 4 + g], r);
-#pragma unroll
-                                    for (int i = 0; i < 8; i++) v[g * 8 + i] += r[i];
+                                for (int j = 0; j < 32; j += 2) {
+                                    const float2 u = gelu2(make_float2(v[j], v[j + 1]));
+                                    v[j] = u.x;
+                                    v[j + 1] = u.y;
                                 }
-                                if (ch == 1 && c + 64 < c0 + kEpiCols) fetch(q0 + 64);
                             }
                         }
 #pragma unroll
                         for (int g = 0; g < 4; g++) {
-                            const float *u = &v[g * 8];
-                            *reinterpret_cast<uint4 *>(mine + sw128(lane, ch * 4 + g)) = make_uint4(
-                                pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]), pack_bf16(u[4], u[5]), pack_bf16(u[6], u[7]));
+                            float *u = &v[g * 8];
+                            uint4 *at = reinterpret_cast<uint4 *>(tile + sw128(lane, ch * 4 + g));
+                            if (RES && pass == 0) {
+                                float r[8];
+                                vio::widen16(*at, r);
+#pragma unroll
+                                for (int j = 0; j < 8; j++) u[j] += r[j];
+                            }
+                            *at = make_uint4(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]), pack_bf16(u[4], u[5]),
+                                             pack_bf16(u[6], u[7]));
                         }
                     }
                     fence_async_smem();
                     __syncwarp();
-                    if (lane == 0 && any) tma_store(last ? &my : &mz, smem_u32(mine), (int)q0, (int)p0);
+                    if (i < pieces && elected()) tma_store(pass ? &mz : &my, smem_u32(tile), (int)q0 + 64 * i, (int)p0);
                 }
             }
         }
-        if (lane == 0) tma_store_wait();
+        if (elected()) tma_store_wait();
     }
     __syncwarp();
     // After a wait that gave up, copies of this CTA may still be on their way.
@@ -603,27 +635,32 @@ narrow_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
         }
     }
     if (mine && ok) {
-        // four rows of x from column i on
-        auto out = [&](int i, float (&d)[4]) {
-            const int64_t p = p0 + i;
-            const int n = (int)min((int64_t)4, a.P - p);
-            const int64_t o = p * a.Q + q;
-            float r[4] = {};
+        // columns (rows of x) i .. i + M - 1: what the epilogue reads of them is
+        // loaded for all at once
+        auto out = [&](int i, auto &d) {
+            constexpr int M = sizeof(d) / sizeof(float);
+            const int64_t p = p0 + i, o = p * a.Q + q;
+            const int n = (int)min((int64_t)M, a.P - p);
+            __nv_bfloat16 r[M];
+            float xs[M];
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                if (j >= n) break;
-                if (a.e.residual) r[j] = __bfloat162float(a.e.residual[o + j * a.Q]);
-                if (a.e.ws) d[j] *= a.e.xs[p + j] * ws;
+            for (int j = 0; j < M; j++) {
+                r[j] = a.e.residual && j < n ? a.e.residual[o + j * a.Q] : __nv_bfloat16(0.f);
+                xs[j] = a.e.ws && j < n ? a.e.xs[p + j] * ws : 1.f;
+            }
+#pragma unroll
+            for (int j = 0; j < M; j++) {
+                if (a.e.ws) d[j] *= xs[j];
                 d[j] += bias;
-                if (a.e.has_z) a.z[o + j * a.Q] = __float2bfloat16_rn(d[j]);
+                if (a.e.has_z && j < n) a.z[o + j * a.Q] = __float2bfloat16_rn(d[j]);
             }
             if (a.e.act) {
 #pragma unroll
-                for (int j = 0; j < 4; j++) d[j] = a.e.act == 1 ? silu(d[j]) : gelu(d[j]);
+                for (int j = 0; j < M; j++) d[j] = a.e.act == 1 ? silu(d[j]) : gelu(d[j]);
             }
 #pragma unroll
-            for (int j = 0; j < 4; j++)
-                if (j < n) a.y[o + j * a.Q] = __float2bfloat16_rn(d[j] + r[j]);
+            for (int j = 0; j < M; j++)
+                if (j < n) a.y[o + j * a.Q] = __float2bfloat16_rn(d[j] + __bfloat162float(r[j]));
         };
         if (split > 1) {
             // this CTA's groups, each summed in the order of the CTAs
@@ -643,8 +680,8 @@ narrow_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < QN; i += 4)
-                if (p0 + i < a.P) out(i, *reinterpret_cast<float(*)[4]>(&v[i]));
+            for (int i = 0; i < QN; i += 16)
+                if (p0 + i < a.P) out(i, *reinterpret_cast<float(*)[16]>(&v[i]));
         }
     }
     tc_fence_before();
@@ -771,19 +808,20 @@ int launch_cluster(K kernel, dim3 grid, int threads, int cluster, size_t bytes, 
 
 int64_t up(int64_t x, int64_t d) { return (x + d - 1) / d; }
 
-template <bool E4M3, bool A_MN, bool B_MN>
+template <bool E4M3, bool A_MN, bool B_MN, bool RES = false>
 int wide(const Operand &A, const Operand &B, Args a, void *y, void *z, int sms, cudaStream_t st) {
-    CUtensorMap ma, mb, my, mz;
+    CUtensorMap ma, mb, my, mz, mr;
     if (!encode(&ma, A, E4M3, 128) || !encode(&mb, B, E4M3, 128) || !encode(&my, y, false, a.P, a.Q, 64, 32) ||
-        !encode(&mz, z ? z : y, false, a.P, a.Q, 64, 32))
+        !encode(&mz, z ? z : y, false, a.P, a.Q, 64, 32) ||
+        !encode(&mr, a.e.residual ? a.e.residual : y, false, a.P, a.Q, 64, 32))
         return (int)cudaErrorInvalidValue;
     a.tiles_p = (int)up(a.P, kTile);
     a.tiles_q = (int)up(a.Q, kTile);
     const int64_t tiles = (int64_t)a.tiles_p * a.tiles_q;
     if (tiles > (int64_t)0x3fffffff) return (int)cudaErrorInvalidValue;
     const int pairs = (int)std::min<int64_t>(tiles, sms / 2);
-    void *args[] = {&ma, &mb, &my, &mz, &a};
-    return launch_cluster(wide_kernel<E4M3, A_MN, B_MN>, dim3(2 * pairs), kWideThreads, 2, kWideBytes, st, args);
+    void *args[] = {&ma, &mb, &my, &mz, &mr, &a};
+    return launch_cluster(wide_kernel<E4M3, A_MN, B_MN, RES>, dim3(2 * pairs), kWideThreads, 2, kWideBytes<RES>, st, args);
 }
 
 template <int QN, bool E4M3, bool A_MN>
@@ -796,16 +834,18 @@ int narrow(const Operand &W, const Operand &X, Args a, int split, cudaStream_t s
 }
 
 // Which kernel runs a product whose rows p are rows of x, by an estimate of
-// its cycles.
+// its cycles from measured parts (16 x 2048 x 6144: 9.7 us narrow, 17 wide;
+// 256 x 2048 x 6144: 38 us narrow, 18 wide).
 struct Choice {
     int qn = 0, split = 1;   // qn 0: wide_kernel
 };
 Choice choose(int64_t P, int64_t Q, int blocks, int sms) {
     Choice best;
-    // tiles one after the other; 590 cycles for a block (512 are the products')
-    double cost = (double)up(up(P, kTile) * up(Q, kTile), sms / 2) * (blocks * 590.0 + 1500.0) + 9000.0;
+    // tiles one after the other: 590 cycles for a block (512 are the products'),
+    // 7000 for an epilogue that goes on meanwhile; the first load and the last
+    // epilogue alone
+    double cost = (double)up(up(P, kTile) * up(Q, kTile), sms / 2) * std::max(blocks * 590.0, 7000.0) + 11500.0;
     for (int qn = 16; qn <= 128; qn *= 2) {
-        if (qn < 128 && P > qn) continue;
         if (up(Q, 128) > 65535 || up(P, qn) > 65535) continue;
         const int64_t tiles = up(P, qn) * up(Q, 128);
         const int fit = qn <= 32 ? 2 : 1;
@@ -815,15 +855,15 @@ Choice choose(int64_t P, int64_t Q, int blocks, int sms) {
             const int64_t room = (int64_t)sms * fit * (split > 2 ? 15 : 16) / 16;
             const int64_t waves = up(tiles * split, room);
             const double together = waves > 1 ? fit : (double)up(tiles * split, sms);
-            // what a partial sum costs to send and to add, 50 cycles a column
-            const double c = waves * (up(blocks, split) * block * together + 7000.0 + (split > 1 ? 1500.0 + 50.0 * qn : 15.0 * qn));
+            // a column's epilogue, or its partial sums to send and to add
+            const double columns = split > 1 ? 1500.0 + 50.0 * qn : 150.0 * qn;
+            const double c = waves * (up(blocks, split) * block * together + 7000.0 + columns);
             if (c < cost) {
                 cost = c;
                 best.qn = qn;
                 best.split = split;
             }
         }
-        if (P <= qn) break;
     }
     return best;
 }
@@ -839,8 +879,12 @@ int product(const Operand &X, const Operand &W, Args a, void *y, void *z, int sm
         case 32: return narrow<32, E4M3, W_MN>(W, X, a, c.split, st);
         case 64: return narrow<64, E4M3, W_MN>(W, X, a, c.split, st);
         case 128: return narrow<128, E4M3, W_MN>(W, X, a, c.split, st);
-        default: return wide<E4M3, false, W_MN>(X, W, a, y, z, sms, st);
+        default: break;
     }
+    if constexpr (!W_MN) {
+        if (a.e.residual) return wide<E4M3, false, false, true>(X, W, a, y, z, sms, st);
+    }
+    return wide<E4M3, false, W_MN>(X, W, a, y, z, sms, st);
 }
 
 // Row blocks of dz_kernel: enough for eight blocks per SM, of 64 rows or more.

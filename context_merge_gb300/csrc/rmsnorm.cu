@@ -9,7 +9,7 @@
 //     dw_i = sum over rows of dy_i s_i rstd.
 //
 // Bound by HBM: every tensor is read and written once.  A row lives in the
-// registers of one group of threads (16 to 1024 of them, one to four 16-byte
+// registers of one group of threads (1 to 1024 of them, one to four 16-byte
 // vectors each), which needs one reduction for everything: the e4m3 row's
 // largest |s w| comes with the sum of squares, since rounding is monotonic
 // and rstd is one number per row, so max|y| is max|s w| times rstd exactly.
@@ -48,7 +48,7 @@ __device__ __forceinline__ float2 row_reduce(float s, float m, float2 *sh, int p
         const float t = __shfl_xor_sync(0xffffffffu, m, o);
         m = MAX ? max_nan(m, t) : m + t;
     }
-    if (TPR > 32) {
+    if constexpr (TPR > 32) {
         constexpr int W = TPR / 32;
         float2 *mine = sh + par * 32;
         const int w = threadIdx.x >> 5;
@@ -319,11 +319,15 @@ int bwd(const BwdParams &p, int grid, float *dw, cudaStream_t st) {
     return launch_column_sums(p.part, grid, p.width, dw, st);
 }
 
-// Threads per row: two 16-byte vectors each where that gives a group of 16 to
-// 1024 threads, one for the narrowest rows, four for the widest fp32 rows.
+// Threads per row: one 16-byte vector each for rows of up to 32 vectors, two
+// for wider ones, four for the widest fp32 rows.
 template <typename T, typename F>
 int by_width(int width, F f) {
     const int vecs = (width + kVecOf<T> - 1) / kVecOf<T>;
+    if (vecs <= 1) return f(std::integral_constant<int, 1>(), std::integral_constant<int, 1>());
+    if (vecs <= 2) return f(std::integral_constant<int, 2>(), std::integral_constant<int, 1>());
+    if (vecs <= 4) return f(std::integral_constant<int, 4>(), std::integral_constant<int, 1>());
+    if (vecs <= 8) return f(std::integral_constant<int, 8>(), std::integral_constant<int, 1>());
     if (vecs <= 16) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 1>());
     if (vecs <= 32) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 1>());
     if (vecs <= 64) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 2>());

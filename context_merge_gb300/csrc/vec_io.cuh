@@ -9,6 +9,27 @@
 namespace cpdr {
 namespace vio {
 
+// Two values in one instruction (round to nearest, as the scalar forms).
+__device__ __forceinline__ uint64_t pair(float2 v) { return *reinterpret_cast<uint64_t *>(&v); }
+__device__ __forceinline__ float2 unpair(uint64_t r) { return *reinterpret_cast<float2 *>(&r); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)), "l"(pair(c)));
+    return unpair(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)));
+    return unpair(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)));
+    return unpair(r);
+}
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 // Two neighbouring channels as loaded.
 template <typename T>
 struct Raw2;

@@ -56,7 +56,7 @@ def close_e4m3(y8, scale, ref):
     assert (np.abs(got - ref) <= tol).all()
 
 
-WIDTHS = [8, 24, 64, 128, 136, 256, 264, 512, 520, 1024, 1032, 2048, 2056, 4096, 4104, 8192, 8200, 16384]
+WIDTHS = [8, 16, 24, 32, 56, 64, 128, 136, 256, 264, 512, 520, 1024, 1032, 2048, 2056, 4096, 4104, 8192, 8200, 16384]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
