@@ -8,6 +8,7 @@ is missing -- there is no fallback of any kind.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -156,6 +157,13 @@ def _space(t, dev):
     if not t.is_contiguous() or t.get_device() != dev:
         raise ValueError(f"workspace must be a contiguous tensor on the context's device {dev}")
     return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _owned_by(stream):
+    """Tensors made inside belong to ``stream`` (None: torch's current one):
+    what a call makes and uses on a stream must not come from another one's
+    memory."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _raw_stream(stream, dev):
@@ -426,8 +434,9 @@ class Context:
                 _addr("carry", carry, self.glr_carry_shape(C), f32, dev), _addr("dy", dy, tok, dt, dev),
                 _opt("dhT", dhT, st, f32, dev))
         if out is None:
-            out = dict(dx=torch.empty_like(x), dg=torch.empty_like(g),
-                       dh0=torch.empty(st, dtype=f32, device=x.device))
+            with _owned_by(stream):
+                out = dict(dx=torch.empty_like(x), dg=torch.empty_like(g),
+                           dh0=torch.empty(st, dtype=f32, device=x.device))
         _check(self._lib.cpdr_glr_bwd(self._h, *args, C, _addr("dx", out["dx"], tok, dt, dev),
                                       _addr("dg", out["dg"], tok, f32, dev), _opt("dh0", out.get("dh0"), st, f32, dev),
                                       _raw_stream(stream, dev)))
@@ -486,10 +495,12 @@ class Context:
         f32, dt, dev, sh = torch.float32, self.torch_dtype, self._dev, s.shape
         args = (_addr("s", s, sh, dt, dev), _addr("weight", weight, sh[-1:], f32, dev), eps,
                 _addr("dy", dy, sh, dt, dev), _opt("dsum", dsum, sh, dt, dev))
-        if out is None:
-            out = dict(ds=torch.empty_like(s), dweight=torch.empty_like(weight))
-        if workspace is None:
-            workspace = torch.empty(self.rmsnorm_bwd_workspace_bytes(rows, width), dtype=torch.uint8, device=s.device)
+        with _owned_by(stream):
+            if out is None:
+                out = dict(ds=torch.empty_like(s), dweight=torch.empty_like(weight))
+            if workspace is None:
+                workspace = torch.empty(self.rmsnorm_bwd_workspace_bytes(rows, width), dtype=torch.uint8,
+                                        device=s.device)
         _check(self._lib.cpdr_rmsnorm_bwd(self._h, rows, width, *args, _addr("ds", out["ds"], sh, dt, dev),
                                           _addr("dweight", out["dweight"], sh[-1:], f32, dev), *_space(workspace, dev),
                                           _raw_stream(stream, dev)))
@@ -534,12 +545,13 @@ class Context:
         wide = (*x.shape[:-1], N)
         args = (_addr("x", x, x.shape, bf16, dev), _addr("w", w, (N, K), bf16, dev),
                 _addr("z", z, wide, bf16, dev) if act else None, _addr("dy", dy, wide, bf16, dev), act)
-        if out is None:
-            out = dict(dx=torch.empty_like(x), dw=torch.empty_like(w),
-                       dbias=torch.empty(N, dtype=torch.float32, device=x.device))
-        if workspace is None:
-            workspace = torch.empty(self.linear_bwd_workspace_bytes(rows, K, N, activation), dtype=torch.uint8,
-                                    device=x.device)
+        with _owned_by(stream):
+            if out is None:
+                out = dict(dx=torch.empty_like(x), dw=torch.empty_like(w),
+                           dbias=torch.empty(N, dtype=torch.float32, device=x.device))
+            if workspace is None:
+                workspace = torch.empty(self.linear_bwd_workspace_bytes(rows, K, N, activation), dtype=torch.uint8,
+                                        device=x.device)
         _check(self._lib.cpdr_linear_bwd(self._h, rows, K, N, *args, _opt("dx", out.get("dx"), x.shape, bf16, dev),
                                          _opt("dw", out.get("dw"), w.shape, bf16, dev),
                                          _opt("dbias", out.get("dbias"), (N,), torch.float32, dev),

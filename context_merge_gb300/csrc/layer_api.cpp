@@ -86,7 +86,7 @@ cpdr_status check_linear(const char *what, const cpdr_ctx *c, int64_t rows, int3
     if (K < 1 || K % mult != 0)
         return fail_with(CPDR_ERR_INVALID, std::string(what) + ": K must be a positive multiple of " + std::to_string(mult));
     if (N < 1 || N % 8 != 0) return fail_with(CPDR_ERR_INVALID, std::string(what) + ": N must be a positive multiple of 8");
-    if (K > (1 << 24) || N > (1 << 24)) return fail_with(CPDR_ERR_UNSUPPORTED, std::string(what) + ": K and N are at most 2^24");
+    if (K > (1 << 23) || N > (1 << 23)) return fail_with(CPDR_ERR_UNSUPPORTED, std::string(what) + ": K and N are at most 2^23");
     if (act < 0 || act > 2)
         return fail_with(CPDR_ERR_INVALID, std::string(what) + ": activation must be 0 (none), 1 (SiLU) or 2 (GELU)");
     return CPDR_OK;

@@ -332,7 +332,7 @@ cpdr_status cpdr_bwd(const cpdr_ctx *ctx, const void *q, const void *k, const vo
  * zigzag); its segments play no part.
  * Layout: x, y [B, T, channels] in the context's token order and input dtype;
  * gate [B, T, channels] fp32; h0, hT [N, channels] fp32, either may be NULL
- * (hT may be h0 itself); channels % 8 == 0.
+ * (hT may be h0 itself); channels % 8 == 0, at most 2^24.
  * carry (NULL, or cpdr_glr_carry_bytes() bytes): what cpdr_glr_bwd needs of
  * the forward, fp32 [groups, channels]: the state before every 16th token of
  * each sequence (its tokens 0, 16, 32, ...), sequence after sequence.
@@ -411,7 +411,7 @@ cpdr_status cpdr_rmsnorm_bwd(const cpdr_ctx *ctx, int64_t rows, int32_t width, c
  * e4m3, standing for x[i, k] x_scale[i] and w[n, k] w_scale[n] (what
  * cpdr_rmsnorm_fwd leaves in y8 and scale is such an x).  The products are
  * accumulated in fp32; y and z are rounded once.
- * rows >= 0; K % 8 == 0 (e4m3: K % 16 == 0); N % 8 == 0.
+ * rows >= 0; K % 8 == 0 (e4m3: K % 16 == 0); N % 8 == 0; both at most 2^23.
  * Errors: CPDR_ERR_UNSUPPORTED (an fp32 context), CPDR_ERR_INVALID,
  * CPDR_ERR_CUDA.
  */

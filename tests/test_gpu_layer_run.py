@@ -275,3 +275,63 @@ def test_two_graphs_that_share_a_workspace_run_one_after_the_other():
     for a, b in zip(ref, outs):
         for k in a:
             assert torch.equal(a[k], b[k]), k
+
+
+def test_what_a_call_makes_belongs_to_the_stream_it_runs_on():
+    """Backwards on a stream of their own, whose workspaces and outputs are made by the call, while the
+    current stream keeps taking and filling memory."""
+    ctx = cpdr.Context(1, 1, 1, 64, 1, dtype="bf16")
+    gen = torch.Generator(device="cuda").manual_seed(11)
+
+    def rb(*s):
+        return torch.randn(s, generator=gen, device="cuda").bfloat16()
+
+    x, wt, dy, z = rb(3000, 264), rb(520, 264), rb(3000, 520), rb(3000, 520)
+    w = torch.ones(520, device="cuda")
+    lin = ctx.linear_bwd(x, wt, dy, z=z, activation="silu")
+    norm = ctx.rmsnorm_bwd(z, w, dy)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = []
+    for _ in range(8):
+        got.append((ctx.linear_bwd(x, wt, dy, z=z, activation="silu", stream=side),
+                    ctx.rmsnorm_bwd(z, w, dy, stream=side)))
+        for _ in range(4):
+            torch.full((3000 * 520 * 2 + 4096,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert all(torch.equal(a[k], lin[k]) for k in lin) and all(torch.equal(b[k], norm[k]) for k in norm)
+
+
+def test_calls_on_two_streams_at_once():
+    """The same context on two streams whose work overlaps: nothing is shared but the status word."""
+    ctx = cpdr.Context(1, 2000, 1, 64, 1, dtype="bf16")
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    sets = []
+    for _ in range(2):
+        x = torch.randn((1, 2000, 264), generator=gen, device="cuda").bfloat16()
+        g = -torch.rand((1, 2000, 264), generator=gen, device="cuda")
+        w = torch.randn((264, 264), generator=gen, device="cuda").bfloat16()
+        sets.append((x, g, w))
+
+    def go(x, g, w):
+        u, h, few = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x[:, :7])
+        ctx.linear_fwd(x, w, u, activation="gelu")
+        ctx.glr_fwd(u, g, h)
+        ctx.linear_fwd(x[:, :7].contiguous(), w, few)
+        ctx.rmsnorm_fwd(h, torch.ones(264, device="cuda"), y=h)
+        return u, h, few
+
+    ref = [go(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    outs = [[], []]
+    for _ in range(5):
+        for i, (st, s) in enumerate(zip(streams, sets)):
+            with torch.cuda.stream(st):
+                outs[i].append(go(*s))
+    torch.cuda.synchronize()
+    ctx.check_device_status()
+    for r, many in zip(ref, outs):
+        for one in many:
+            assert all(torch.equal(a, b) for a, b in zip(r, one))
