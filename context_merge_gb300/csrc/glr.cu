@@ -10,14 +10,17 @@
 // chip once.  A channel's tokens depend on one another only through affine
 // maps h -> A h + B, which compose: (A1, B1) then (A2, B2) is
 // (A2 A1, A2 B1 + B2).  One warp takes 64 channels (2 per lane: rows of 128
-// bytes of bf16) by kGroup = 16 tokens in registers, a CTA 8 such groups one
-// behind the other, a cluster of up to 8 CTAs 8 times as many; each step of
-// the cluster composes the groups' maps (shared memory inside the CTA,
-// distributed shared memory between CTAs), and every group then runs its
-// tokens from its own start.  So nothing is read twice and no CTA waits on
-// another cluster; all sums run in a fixed order, and the result does not
-// depend on timing.  The sequential part, one exchange per cluster step, is
-// hidden by the other CTAs of the SM.
+// bytes of bf16) by 16 tokens, a CTA 4 (backward 8) such groups one behind the
+// other, a cluster of up to 8 CTAs 8 times as many; each step of the cluster
+// composes the groups' maps (shared memory inside the CTA, distributed shared
+// memory between CTAs), and every group then runs its tokens from its own
+// start.  So nothing is read twice and no CTA waits on another cluster; all
+// sums run in a fixed order, and the result does not depend on timing.  A
+// step's exchange goes on while the step before it is written.
+//
+// Measured (of 6782 GB/s): forward 262144 x 2048 bf16, one sequence, 677 us,
+// 0.96; packed 65536 x 2048, 12 ragged sequences: fp32 zigzag forward 261 us,
+// 0.91; bf16 backward 305 us, 0.93.
 //
 // The backward recomputes h inside each group from the state before the
 // group's first token (the carry, fp32, 4 bytes per 16 tokens, that the
@@ -557,20 +560,32 @@ glr_step_kernel(const T *__restrict__ x, const float *__restrict__ g, const floa
     *reinterpret_cast<float2 *>(state_out + so) = h;
 }
 
-// CTAs of a cluster.  One CTA's share of the longest sequence should be no
-// more than half of what a CTA slot gets of all tokens, or it runs alone in
-// the end (packed 65536 x 2048 in 12 ragged sequences, backward: 308 us; all
-// of it 316, a quarter 340; 313 with a cluster of one); and a cluster has no
-// more CTAs than that sequence has tiles.
+// CTAs of a cluster, by an estimate of the time in tokens that one CTA takes:
+// the longest sequence's share, or all items' over the clusters that run at
+// once, with a quarter of an item for the last round's gaps; an exchange costs
+// 4% per CTA.  Measured with clusters of 1, 2, 4 and 8 (us): one sequence of
+// 32768 x 2048, forward 399, 230, 125, 93 and backward 597, 315, 167, 257 (of
+// eight, 15 clusters run at once); 12 ragged sequences in 65536 x 2048,
+// backward 311, 305, 338, 472; 64 of 1024 x 2048, forward 165, 186, 238, 353.
 int pick_cluster(const cpdr_ctx *c, int slices, int tile, int per_sm) {
     const auto &pl = c->plan;
-    const int64_t slots = (int64_t)per_sm * device_sms(c->device);
-    const int64_t tokens = (int64_t)pl.B * pl.T;
-    int z = 1;
-    while (z < kMaxCluster && pl.glr_longest > (int64_t)z * tile &&
-           (double)pl.glr_longest / z > 0.5 * (double)tokens * slices / (double)slots)
-        z *= 2;
-    return z;
+    const int64_t items = (int64_t)pl.glr_spans.size() * slices;
+    const double all = (double)pl.B * (double)pl.T * slices;
+    int best = 1;
+    double cost = 0;
+    for (int z = 1; z <= kMaxCluster && (z == 1 || pl.glr_longest > (int64_t)(z / 2) * tile); z *= 2) {
+        // the GPU's parts do not all hold a multiple of z CTAs
+        const double fit = z <= 2 ? 1.0 : z == 8 && per_sm == 1 ? 0.79 : 0.95;
+        const int64_t at_once = std::max<int64_t>(1, (int64_t)(device_sms(c->device) * per_sm * fit / z));
+        double t = (double)pl.glr_longest / z;
+        if (items > at_once) t = std::max(t, all / (z * at_once)) + 0.25 * all / items / z;
+        t *= 1.0 + 0.04 * z;
+        if (z == 1 || t < cost) {
+            cost = t;
+            best = z;
+        }
+    }
+    return best;
 }
 
 template <typename K>

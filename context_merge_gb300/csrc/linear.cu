@@ -16,15 +16,18 @@
 //  * wide_kernel, bound by the tensor cores: pairs of CTAs (cta_group::2) own
 //    256 x 256 tiles.  Per 128 bytes of r each CTA fetches 128 rows of A and
 //    128 of B, 32 KiB per 512 tensor-core cycles: half of what a single CTA
-//    with a 128 x 256 tile would draw from the L2, which could not keep up.
-//    Six stages of TMA loads, one issuing thread, two accumulators of 256
-//    TMEM columns, so that eight epilogue warps empty one while the other
-//    fills; outputs leave through swizzled staging tiles by TMA, which also
-//    cuts what lies outside the matrix.
+//    with a 128 x 256 tile would draw from the L2.  Six stages of TMA loads,
+//    one issuing thread, two accumulators of 256 TMEM columns, so that eight
+//    epilogue warps empty one while the other fills; outputs leave through
+//    swizzled staging tiles by TMA, which also cuts what lies outside the
+//    matrix.  bf16 32768 x 2048 x 6144: 417 us, 1.98 PFLOP/s (the library's
+//    product 415); e4m3 252 us, 3.27 PFLOP/s; tensor pipe 92% and 86% active.
 //  * narrow_kernel, for few rows of x, bound by reading w: 128 rows of w (the
 //    128 lanes) by 16 to 128 rows of x (the columns) per CTA, with r split
 //    over a cluster of up to 8 CTAs, whose partial sums meet in distributed
-//    shared memory in the order of the CTAs.
+//    shared memory in the order of the CTAs.  16 x 2048 x 6144: 9.7 us (25 MB
+//    of w; the library's product 6.3), of which 1.3 between kernels, 5.6 until
+//    the last byte of w, 1.9 for the partial sums and the epilogue.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
