@@ -32,6 +32,7 @@
 #include <type_traits>
 
 #include "cpdr_internal.hpp"
+#include "launch.cuh"
 #include "tc_common.cuh"
 #include "vec_io.cuh"
 
@@ -322,6 +323,8 @@ __global__ void __launch_bounds__(32 * WARPS, 2) glr_fwd_kernel(Params p, int nz
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = nz > 1 ? cluster_rank() : 0u;
     const int item = blockIdx.x / nz;
+    next_grid_may_start();
+    previous_grid_done();
     const GlrSpan sp = p.spans[item / p.slices];
     const int c0 = (item % p.slices) * kSlice, c = c0 + 2 * lane;
     const bool live = c < p.channels;
@@ -411,6 +414,8 @@ __global__ void __launch_bounds__(32 * WARPS, 1) glr_bwd_kernel(Params p, int nz
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = nz > 1 ? cluster_rank() : 0u;
     const int item = blockIdx.x / nz;
+    next_grid_may_start();
+    previous_grid_done();
     const GlrSpan sp = p.spans[item / p.slices];
     const int c0 = (item % p.slices) * kSlice, c = c0 + 2 * lane;
     const bool live = c < p.channels;
@@ -529,6 +534,8 @@ template <typename T>
 __global__ void __launch_bounds__(kStepThreads)
 glr_step_kernel(const T *__restrict__ x, const float *__restrict__ g, const float *state, float *state_out,
                 const int32_t *__restrict__ slots, int n, int num_slots, int channels, T *y) {
+    next_grid_may_start();
+    previous_grid_done();
     const int row = blockIdx.y;
     const int c = (blockIdx.x * kStepThreads + threadIdx.x) * 2;
     int slot = row;
@@ -599,20 +606,7 @@ int launch(const cpdr_ctx *c, K kernel, int warps, int per_sm, size_t bytes, Par
     const int64_t items = (int64_t)pl.glr_spans.size() * p.slices;
     const int nz = pick_cluster(c, p.slices, warps * kGlrGroup, per_sm);
     if (items * nz > (int64_t)0x7fffffff) return (int)cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e != cudaSuccess) return (int)e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(items * nz));
-    cfg.blockDim = dim3(32 * warps);
-    cfg.dynamicSmemBytes = bytes;
-    cfg.stream = (cudaStream_t)stream;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = (unsigned)nz;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = nz > 1 ? 1 : 0;
-    return (int)cudaLaunchKernelEx(&cfg, kernel, p, nz);
+    return launch_early(kernel, dim3((unsigned)(items * nz)), 32 * warps, bytes, nz, stream, p, nz);
 }
 
 static_assert(sizeof(FwdShared<float, kFwdWarps>) <= 227 * 1024 && sizeof(BwdShared<float, kBwdWarps<float>>) <= 227 * 1024 &&
@@ -668,14 +662,11 @@ int launch_glr_step(const cpdr_ctx *c, const void *x, const float *g, const floa
                     const int32_t *slots, int n, int num_slots, int channels, void *y, void *stream) {
     if (n == 0) return 0;
     const dim3 grid((unsigned)((channels + 2 * kStepThreads - 1) / (2 * kStepThreads)), (unsigned)n);
-    cudaStream_t st = (cudaStream_t)stream;
     if (c->plan.in_dtype == CPDR_DTYPE_F32)
-        glr_step_kernel<float><<<grid, kStepThreads, 0, st>>>((const float *)x, g, state, state_out, slots, n, num_slots,
-                                                          channels, (float *)y);
-    else
-        glr_step_kernel<__nv_bfloat16><<<grid, kStepThreads, 0, st>>>((const __nv_bfloat16 *)x, g, state, state_out, slots,
-                                                                  n, num_slots, channels, (__nv_bfloat16 *)y);
-    return (int)cudaGetLastError();
+        return launch_early(glr_step_kernel<float>, grid, kStepThreads, 0, 1, stream, (const float *)x, g, state, state_out, slots,
+                            n, num_slots, channels, (float *)y);
+    return launch_early(glr_step_kernel<__nv_bfloat16>, grid, kStepThreads, 0, 1, stream, (const __nv_bfloat16 *)x, g, state,
+                        state_out, slots, n, num_slots, channels, (__nv_bfloat16 *)y);
 }
 
 }  // namespace cpdr

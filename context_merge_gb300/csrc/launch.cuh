@@ -1,0 +1,45 @@
+// Launches that begin while the kernel before them on the stream ends.
+//
+// A kernel launched by launch_early may start once every block of the kernel
+// before it has called next_grid_may_start() (or has ended), and sets itself
+// up meanwhile: barriers, TMEM, tensor maps.  It must call
+// previous_grid_done() in every thread before that thread reads or writes
+// global memory: the call returns when the kernels before it have ended and
+// what they wrote can be seen.  Measured: a chain of 16 x 2048 x 6144 products
+// 9.3 -> 7.5 us each.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <utility>
+
+namespace cpdr {
+
+__device__ __forceinline__ void next_grid_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void previous_grid_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// `bytes`: dynamic shared memory (the kernel's limit is raised where it is
+// over the default); `cluster`: blocks of a cluster along x.
+template <typename... P, typename... A>
+int launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t bytes, int cluster, void *stream, A &&...args) {
+    if (bytes > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e != cudaSuccess) return (int)e;
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute at[2]{};
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return (int)cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
+}  // namespace cpdr

@@ -35,6 +35,7 @@
 #include <algorithm>
 
 #include "cpdr_internal.hpp"
+#include "launch.cuh"
 #include "tc_common.cuh"
 #include "vec_io.cuh"
 
@@ -71,9 +72,9 @@ __device__ __forceinline__ uint32_t ctarank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// True in one thread of the warp, always the same, which the compiler then knows to be one: by
-// "lane == 0" it wraps every product and copy in a loop over the active
-// threads, 152 cycles a product where the tensor cores need 128.
+// True in one thread of the warp, always the same, which the compiler then
+// knows to be one: by "lane == 0" it wraps every product and copy in a loop
+// over the active threads, 152 cycles a product where the tensor cores need 128.
 __device__ __forceinline__ bool elected() {
     uint32_t e;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
@@ -280,6 +281,7 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = ctarank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, tiles = a.tiles_p * a.tiles_q;
+    next_grid_may_start();
     if (threadIdx.x == 0) {
         b.ctl.abort = 0;
         for (int s = 0; s < STAGES; s++) {
@@ -308,6 +310,7 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
     __syncthreads();
     cluster_sync();
     tc_fence_after();
+    previous_grid_done();
     const uint32_t tmem = b.tmem;
 
     if (w == kEpiWarps) {
@@ -543,6 +546,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
         load_stage<1, A_MN, E4M3>(dst, &mw, bar, (int)q0, k0 + it);
         load_stage<1, false, E4M3>(dst + 128 * kRBytes, &mx, bar, (int)p0, k0 + it);
     };
+    next_grid_may_start();
     if (w == 4) {
         // the first loads do not wait for the rest to be set up
         if (elected()) {
@@ -556,6 +560,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
             mbar_init(&b.done, 1);
             mbar_init(&b.summed, 1);
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            previous_grid_done();
             for (int it = 0; it < min(n, STAGES); it++) load(it);
         }
     } else if (w == 5) {
@@ -566,11 +571,16 @@ narrow_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    previous_grid_done();
     // waited for before the sums go out: the CTAs of the cluster have all begun
     if (split > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     const uint32_t tmem = b.tmem;
     bool ok = true;
-    float v[QN];
+    float v[QN], bias = 0.f, ws = 1.f;
+    if (w < 4 && q0 + threadIdx.x < a.Q) {
+        if (a.e.bias) bias = a.e.bias[q0 + threadIdx.x];
+        if (a.e.ws) ws = a.e.ws[q0 + threadIdx.x];
+    }
     if (w == 4) {
         if (elected()) {
             for (int it = STAGES; it < n; it++) {
@@ -611,7 +621,6 @@ narrow_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
     // groups of 4 columns whose sums a CTA of the cluster takes
     const int per = (QN / 4 + split - 1) / split, g0 = per * rank, groups = min(per, QN / 4 - g0);
     const bool mine = w < 4 && q < a.Q && ok;
-    const float bias = mine && a.e.bias ? a.e.bias[q] : 0.f, ws = mine && a.e.ws ? a.e.ws[q] : 1.f;
     if (split > 1) {
         // every partial sum goes to the CTA that adds its group, which counts
         // the bytes; no CTA leaves before all of its own have come
@@ -703,6 +712,8 @@ dz_kernel(const __nv_bfloat16 *__restrict__ dy, const __nv_bfloat16 *__restrict_
           __nv_bfloat16 *__restrict__ dz, float *__restrict__ part) {
     constexpr int AHEAD = 4;
     __shared__ float sh[8][256];
+    next_grid_may_start();
+    previous_grid_done();
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int col = blockIdx.y * 256 + tx * 8;
     const int64_t r0 = (int64_t)blockIdx.x * per, r1 = min(rows, r0 + per);
@@ -791,24 +802,6 @@ bool encode(CUtensorMap *m, const Operand &o, bool e4m3, int tile_rows) {
 }
 
 
-template <typename K>
-int launch_cluster(K kernel, dim3 grid, int threads, int cluster, size_t bytes, cudaStream_t st, void **args) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e != cudaSuccess) return (int)e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = bytes;
-    cfg.stream = st;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = (unsigned)cluster;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = cluster > 1 ? 1 : 0;
-    return (int)cudaLaunchKernelExC(&cfg, (const void *)kernel, args);
-}
-
 int64_t up(int64_t x, int64_t d) { return (x + d - 1) / d; }
 
 template <bool E4M3, bool A_MN, bool B_MN, bool RES = false>
@@ -823,17 +816,16 @@ int wide(const Operand &A, const Operand &B, Args a, void *y, void *z, int sms, 
     const int64_t tiles = (int64_t)a.tiles_p * a.tiles_q;
     if (tiles > (int64_t)0x3fffffff) return (int)cudaErrorInvalidValue;
     const int pairs = (int)std::min<int64_t>(tiles, sms / 2);
-    void *args[] = {&ma, &mb, &my, &mz, &mr, &a};
-    return launch_cluster(wide_kernel<E4M3, A_MN, B_MN, RES>, dim3(2 * pairs), kWideThreads, 2, kWideBytes<RES>, st, args);
+    return launch_early(wide_kernel<E4M3, A_MN, B_MN, RES>, dim3(2 * pairs), kWideThreads, kWideBytes<RES>, 2, st, ma, mb, my, mz,
+                        mr, a);
 }
 
 template <int QN, bool E4M3, bool A_MN>
 int narrow(const Operand &W, const Operand &X, Args a, int split, cudaStream_t st) {
     CUtensorMap mw, mx;
     if (!encode(&mw, W, E4M3, 128) || !encode(&mx, X, E4M3, QN)) return (int)cudaErrorInvalidValue;
-    void *args[] = {&mw, &mx, &a};
     const dim3 grid((unsigned)split, (unsigned)((a.Q + 127) / 128), (unsigned)((a.P + QN - 1) / QN));
-    return launch_cluster(narrow_kernel<QN, E4M3, A_MN>, grid, kNarrowThreads, split, kNarrowBytes<QN>, st, args);
+    return launch_early(narrow_kernel<QN, E4M3, A_MN>, grid, kNarrowThreads, kNarrowBytes<QN>, split, st, mw, mx, a);
 }
 
 // Which kernel runs a product whose rows p are rows of x, by an estimate of
@@ -928,9 +920,8 @@ int launch_linear_bwd(const cpdr_ctx *c, int64_t rows, int K, int N, const void 
         const int per = dz_rows_per_block(rows, N, sms);
         const int64_t parts = (rows + per - 1) / per;
         auto kernel = act == 0 ? dz_kernel<0> : act == 1 ? dz_kernel<1> : dz_kernel<2>;
-        kernel<<<dim3((unsigned)parts, (unsigned)((N + 255) / 256)), 256, 0, st>>>(
-            (const __nv_bfloat16 *)dy, (const __nv_bfloat16 *)z, rows, N, per, (__nv_bfloat16 *)dz, dbias ? part : nullptr);
-        rc = (int)cudaGetLastError();
+        rc = launch_early(kernel, dim3((unsigned)parts, (unsigned)((N + 255) / 256)), 256, 0, 1, st, (const __nv_bfloat16 *)dy,
+                          (const __nv_bfloat16 *)z, rows, N, per, (__nv_bfloat16 *)dz, dbias ? part : nullptr);
         if (rc) return rc;
         if (dbias) rc = launch_column_sums(part, (int)parts, N, dbias, stream);
         if (rc) return rc;

@@ -22,6 +22,7 @@
 #include <algorithm>
 
 #include "cpdr_internal.hpp"
+#include "launch.cuh"
 #include "vec_io.cuh"
 
 namespace cpdr {
@@ -87,6 +88,8 @@ template <typename T, int TPR, int NV, bool E4M3>
 __global__ void __launch_bounds__(kBlock<TPR>) rmsnorm_fwd_kernel(FwdParams p) {
     constexpr int V = kVecOf<T>;
     __shared__ float2 sh[64];
+    next_grid_may_start();
+    previous_grid_done();
     const int64_t row = (int64_t)blockIdx.x * (kBlock<TPR> / TPR) + threadIdx.x / TPR;
     const int t = threadIdx.x % TPR;
     const bool live = row < p.rows;
@@ -188,6 +191,8 @@ __global__ void __launch_bounds__(kBlock<TPR>) rmsnorm_bwd_kernel(BwdParams p) {
     constexpr int G = kBlock<TPR> / TPR;
     __shared__ float2 sh[64];
     extern __shared__ float dw_sh[];
+    next_grid_may_start();
+    previous_grid_done();
     const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
     const int64_t stride = (int64_t)gridDim.x * G;
     const T *sp = (const T *)p.s, *dyp = (const T *)p.dy, *dsp = (const T *)p.dsum;
@@ -281,6 +286,8 @@ constexpr int kSumCols = 32, kSumRows = 16;
 __global__ void __launch_bounds__(kSumCols *kSumRows)
 column_sums_kernel(const float *__restrict__ part, int nparts, int width, float *__restrict__ out) {
     __shared__ float sh[kSumRows][kSumCols + 1];
+    next_grid_may_start();
+    previous_grid_done();
     const int cx = threadIdx.x % kSumCols, ry = threadIdx.x / kSumCols;
     const int col = blockIdx.x * kSumCols + cx;
     float v = 0.f;
@@ -301,11 +308,8 @@ int fwd(const FwdParams &p, cudaStream_t st) {
     constexpr int per = kBlock<TPR> / TPR;
     const int64_t grid = (p.rows + per - 1) / per;
     if (grid > (int64_t)0x7fffffff) return (int)cudaErrorInvalidValue;
-    if (p.y8)
-        rmsnorm_fwd_kernel<T, TPR, NV, true><<<(unsigned)grid, kBlock<TPR>, 0, st>>>(p);
-    else
-        rmsnorm_fwd_kernel<T, TPR, NV, false><<<(unsigned)grid, kBlock<TPR>, 0, st>>>(p);
-    return (int)cudaGetLastError();
+    return launch_early(p.y8 ? rmsnorm_fwd_kernel<T, TPR, NV, true> : rmsnorm_fwd_kernel<T, TPR, NV, false>,
+                        dim3((unsigned)grid), kBlock<TPR>, 0, 1, st, p);
 }
 
 template <typename T, int TPR, int NV>
@@ -313,9 +317,8 @@ int bwd(const BwdParams &p, int grid, float *dw, cudaStream_t st) {
     constexpr int G = kBlock<TPR> / TPR;
     const size_t smem = G > 1 ? (size_t)G * TPR * NV * kVecOf<T> * sizeof(float) : 0;
     static_assert((G > 1 ? G * TPR * NV * kVecOf<T> * 4 : 0) <= 48 * 1024, "dw staging within the default shared memory");
-    rmsnorm_bwd_kernel<T, TPR, NV><<<grid, kBlock<TPR>, smem, st>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return (int)e;
+    const int rc = launch_early(rmsnorm_bwd_kernel<T, TPR, NV>, dim3((unsigned)grid), kBlock<TPR>, smem, 1, st, p);
+    if (rc) return rc;
     return launch_column_sums(p.part, grid, p.width, dw, st);
 }
 
@@ -351,9 +354,8 @@ int rows_per_block(int width, bool f32) {
 static_assert(kMaxNormWidth <= 1024 * 4 * kVecOf<float> && kMaxNormWidth <= 1024 * 2 * kVecOf<__nv_bfloat16>, "a row fits the registers of one block");
 
 int launch_column_sums(const float *part, int nparts, int width, float *out, void *stream) {
-    column_sums_kernel<<<(width + kSumCols - 1) / kSumCols, kSumCols * kSumRows, 0, (cudaStream_t)stream>>>(part, nparts,
-                                                                                                            width, out);
-    return (int)cudaGetLastError();
+    return launch_early(column_sums_kernel, dim3((unsigned)((width + kSumCols - 1) / kSumCols)), kSumCols * kSumRows, 0, 1, stream,
+                        part, nparts, width, out);
 }
 
 int launch_rmsnorm_fwd(const cpdr_ctx *c, int64_t rows, int width, const void *x, const void *residual,

@@ -335,3 +335,44 @@ def test_calls_on_two_streams_at_once():
     for r, many in zip(ref, outs):
         for one in many:
             assert all(torch.equal(a, b) for a, b in zip(r, one))
+
+
+def test_a_chain_of_calls_equals_the_calls_one_by_one():
+    """Kernels may begin while the one before them ends: a long chain of calls, each reading what the one
+    before wrote (and writing what it read), against the same calls with a synchronisation after each."""
+    D, C, S = 136, 264, 9
+    w = cuda(weights(D, C, 21))
+    ctx = cpdr.Context(1, 1, 1, 64, 1, dtype="bf16")
+    seq = cpdr.Context(1, 700, 1, 64, 1, dtype="bf16")
+
+    def chain(wait):
+        gen = torch.Generator(device="cuda").manual_seed(22)
+        x = torch.randn((700, D), generator=gen, device="cuda").bfloat16()
+        g = -torch.rand((1, 700, C), generator=gen, device="cuda")
+        state, carry = torch.zeros(S, C, device="cuda"), torch.empty(seq.glr_carry_shape(C), device="cuda")
+        n, few, u, h = x.clone(), x[:S].clone(), *(torch.zeros(700, C, device="cuda").bfloat16() for _ in range(2))
+        ws = torch.empty(ctx.linear_bwd_workspace_bytes(700, D, C, "silu"), dtype=torch.uint8, device="cuda")
+        grads = dict(dx=torch.empty_like(x), dw=torch.empty_like(w["w_in"]), dbias=torch.empty(C, device="cuda"))
+        out = []
+
+        def step(f, *a, **k):
+            f(*a, **k)
+            if wait:
+                torch.cuda.synchronize()
+
+        for _ in range(12):
+            step(ctx.rmsnorm_fwd, x, w["norm"], y=n)
+            step(ctx.linear_fwd, n, w["w_in"], u, bias=w["b_in"], activation="silu", z=h)
+            step(ctx.linear_bwd, n, w["w_in"], u, z=h, activation="silu", out=grads, workspace=ws)
+            step(seq.glr_fwd, u.view(1, 700, C), g, h.view(1, 700, C), carry=carry)
+            step(ctx.linear_fwd, h, w["w_out"], x, residual=x)
+            step(ctx.rmsnorm_fwd, few, w["norm"], residual=x[:S], sum_out=few, y=n[:S])
+            step(ctx.linear_fwd, n[:S], w["w_in"], u[:S])
+            step(ctx.glr_step, u[:S], g[0, :S], state, h[:S])
+            step(ctx.linear_fwd, h[:S], w["w_out"], few, residual=few)
+            out += [t.clone() for t in (x, few, state, carry, *grads.values())]
+        torch.cuda.synchronize()
+        return out
+
+    for a, b in zip(chain(True), chain(False)):
+        assert torch.equal(a, b)
