@@ -36,6 +36,7 @@ EXPORTED = ["cpdr_ctx_create", "cpdr_ctx_destroy", "cpdr_buffer_sizes", "cpdr_pl
             "cpdr_linear_bwd_workspace_bytes", "cpdr_linear_bwd", "cpdr_last_error", "cpdr_version"]
 
 
+_F32, _BF16, _E4M3 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
 ACTIVATIONS = {None: 0, "none": 0, "silu": 1, "gelu": 2}
 
 
@@ -125,8 +126,6 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _bad_tensor(name: str, t, shape, dtype, dev):
-    if t is None:
-        raise ValueError(f"{name} is missing")
     if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {list(shape)} {dtype} tensor, got {list(t.shape)} {t.dtype}")
     raise ValueError(f"{name} must be on the context's device {dev}, got {t.device}")
@@ -134,16 +133,14 @@ def _bad_tensor(name: str, t, shape, dtype, dev):
 
 def _addr(name: str, t, shape, dtype, dev):
     """The address of t, which must be a contiguous CUDA tensor of that shape
-    and dtype on device index ``dev`` (a decoding step is bound by what the
-    host does, so the checks are few and cheap)."""
-    if t is None or t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev:
+    and dtype on device index ``dev``; None (NULL) for None, which the library
+    refuses where it must not be.  (A decoding step is bound by what the host
+    does: the checks are few and cheap.)"""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev:
         _bad_tensor(name, t, shape, dtype, dev)
     return t.data_ptr()
-
-
-def _opt(name: str, t, shape, dtype, dev):
-    """_addr of a tensor that may be None (NULL)."""
-    return None if t is None else _addr(name, t, shape, dtype, dev)
 
 
 def _stream(stream) -> ctypes.c_void_p:
@@ -418,27 +415,28 @@ class Context:
         h0 and hT [N, C] fp32 or None; carry (``glr_carry_shape``) keeps what
         ``glr_bwd`` needs."""
         C, tok, st = self._glr_shapes(x)
-        f32, dt, dev = torch.float32, self.torch_dtype, self._dev
-        keep = None if carry is None else _addr("carry", carry, self.glr_carry_shape(C), f32, dev)
-        _check(self._lib.cpdr_glr_fwd(self._h, _addr("x", x, tok, dt, dev), _addr("g", g, tok, f32, dev),
-                                      _opt("h0", h0, st, f32, dev), C, _addr("y", y, tok, dt, dev),
-                                      _opt("hT", hT, st, f32, dev), keep, _raw_stream(stream, dev)))
+        dt, dev = self.torch_dtype, self._dev
+        keep = None if carry is None else _addr("carry", carry, self.glr_carry_shape(C), _F32, dev)
+        _check(self._lib.cpdr_glr_fwd(self._h, _addr("x", x, tok, dt, dev), _addr("g", g, tok, _F32, dev),
+                                      _addr("h0", h0, st, _F32, dev), C, _addr("y", y, tok, dt, dev),
+                                      _addr("hT", hT, st, _F32, dev), keep, _raw_stream(stream, dev)))
 
     def glr_bwd(self, x, g, carry, dy, dhT=None, out=None, stream=None):
         """Gradients of sum <dy, y> + sum <dhT, hT>: a dict of dx (input
         dtype), dg and dh0 (fp32), written into ``out``'s tensors if given
         (dh0 may be None there)."""
         C, tok, st = self._glr_shapes(x)
-        f32, dt, dev = torch.float32, self.torch_dtype, self._dev
-        args = (_addr("x", x, tok, dt, dev), _addr("g", g, tok, f32, dev),
-                _addr("carry", carry, self.glr_carry_shape(C), f32, dev), _addr("dy", dy, tok, dt, dev),
-                _opt("dhT", dhT, st, f32, dev))
+        dt, dev = self.torch_dtype, self._dev
+        args = (_addr("x", x, tok, dt, dev), _addr("g", g, tok, _F32, dev),
+                _addr("carry", carry, self.glr_carry_shape(C), _F32, dev), _addr("dy", dy, tok, dt, dev),
+                _addr("dhT", dhT, st, _F32, dev))
         if out is None:
             with _owned_by(stream):
                 out = dict(dx=torch.empty_like(x), dg=torch.empty_like(g),
-                           dh0=torch.empty(st, dtype=f32, device=x.device))
+                           dh0=torch.empty(st, dtype=_F32, device=x.device))
         _check(self._lib.cpdr_glr_bwd(self._h, *args, C, _addr("dx", out["dx"], tok, dt, dev),
-                                      _addr("dg", out["dg"], tok, f32, dev), _opt("dh0", out.get("dh0"), st, f32, dev),
+                                      _addr("dg", out["dg"], tok, _F32, dev),
+                                      _addr("dh0", out.get("dh0"), st, _F32, dev),
                                       _raw_stream(stream, dev)))
         return out
 
@@ -451,13 +449,13 @@ class Context:
         if x.dim() != 2 or state.dim() != 2:
             raise ValueError("x must be [n, C] and state [S, C]")
         rows, st = x.shape, state.shape
-        f32, dt, dev = torch.float32, self.torch_dtype, self._dev
+        dt, dev = self.torch_dtype, self._dev
         if st[1] != rows[1]:
             raise ValueError(f"state must have {rows[1]} channels, got {st[1]}")
-        old = _addr("state", state, st, f32, dev)
-        _check(self._lib.cpdr_glr_step(self._h, _addr("x", x, rows, dt, dev), _addr("g", g, rows, f32, dev), old,
-                                       old if state_out is None else _addr("state_out", state_out, st, f32, dev),
-                                       _opt("slots", slots, rows[:1], torch.int32, dev), rows[0], st[0], rows[1],
+        old = _addr("state", state, st, _F32, dev)
+        _check(self._lib.cpdr_glr_step(self._h, _addr("x", x, rows, dt, dev), _addr("g", g, rows, _F32, dev), old,
+                                       old if state_out is None else _addr("state_out", state_out, st, _F32, dev),
+                                       _addr("slots", slots, rows[:1], torch.int32, dev), rows[0], st[0], rows[1],
                                        _addr("y", y, rows, dt, dev), _raw_stream(stream, dev)))
 
     # ---- RMS norm --------------------------------------------------------
@@ -474,13 +472,14 @@ class Context:
         (fp32): s into ``sum_out``, the norm into ``y`` (input dtype) and/or
         ``y8`` (float8_e4m3fn) with ``scale`` (fp32, one per row)."""
         rows, width = self._rows(x)
-        f32, dt, dev, sh = torch.float32, self.torch_dtype, self._dev, x.shape
+        dt, dev, sh = self.torch_dtype, self._dev, x.shape
         _check(self._lib.cpdr_rmsnorm_fwd(self._h, rows, width, _addr("x", x, sh, dt, dev),
-                                          _opt("residual", residual, sh, dt, dev),
-                                          _addr("weight", weight, sh[-1:], f32, dev), eps,
-                                          _opt("sum_out", sum_out, sh, dt, dev), _opt("y", y, sh, dt, dev),
-                                          _opt("y8", y8, sh, torch.float8_e4m3fn, dev),
-                                          _opt("scale", scale, sh[:-1], f32, dev), _raw_stream(stream, dev)))
+                                          _addr("residual", residual, sh, dt, dev),
+                                          _addr("weight", weight, (width,), _F32, dev), eps,
+                                          _addr("sum_out", sum_out, sh, dt, dev), _addr("y", y, sh, dt, dev),
+                                          _addr("y8", y8, sh, _E4M3, dev),
+                                          None if scale is None else _addr("scale", scale, sh[:-1], _F32, dev),
+                                          _raw_stream(stream, dev)))
 
     def rmsnorm_bwd_workspace_bytes(self, rows, width):
         n = ctypes.c_size_t()
@@ -492,9 +491,9 @@ class Context:
         gradient ``dsum`` that reaches s past the norm: a dict of ds (input
         dtype; of x and residual alike) and dweight (fp32)."""
         rows, width = self._rows(s)
-        f32, dt, dev, sh = torch.float32, self.torch_dtype, self._dev, s.shape
-        args = (_addr("s", s, sh, dt, dev), _addr("weight", weight, sh[-1:], f32, dev), eps,
-                _addr("dy", dy, sh, dt, dev), _opt("dsum", dsum, sh, dt, dev))
+        dt, dev, sh = self.torch_dtype, self._dev, s.shape
+        args = (_addr("s", s, sh, dt, dev), _addr("weight", weight, sh[-1:], _F32, dev), eps,
+                _addr("dy", dy, sh, dt, dev), _addr("dsum", dsum, sh, dt, dev))
         with _owned_by(stream):
             if out is None:
                 out = dict(ds=torch.empty_like(s), dweight=torch.empty_like(weight))
@@ -502,7 +501,7 @@ class Context:
                 workspace = torch.empty(self.rmsnorm_bwd_workspace_bytes(rows, width), dtype=torch.uint8,
                                         device=s.device)
         _check(self._lib.cpdr_rmsnorm_bwd(self._h, rows, width, *args, _addr("ds", out["ds"], sh, dt, dev),
-                                          _addr("dweight", out["dweight"], sh[-1:], f32, dev), *_space(workspace, dev),
+                                          _addr("dweight", out["dweight"], sh[-1:], _F32, dev), *_space(workspace, dev),
                                           _raw_stream(stream, dev)))
         return out
 
@@ -514,19 +513,20 @@ class Context:
         ``w_scale`` [N]; y, residual and z (the value before the activation)
         [.., N] bf16; bias [N] fp32; activation None, "silu" or "gelu"."""
         rows, K = self._rows(x)
-        f32, bf16, dev, sh = torch.float32, torch.bfloat16, self._dev, x.shape
-        it = bf16 if x_scale is None else torch.float8_e4m3fn
+        dev, sh = self._dev, x.shape
+        it = _BF16 if x_scale is None else _E4M3
         if w.dim() != 2:
             raise ValueError(f"w must be a [N, {K}] tensor, got {list(w.shape)}")
         N = w.shape[0]
-        out, n = (*sh[:-1], N), (N,)
+        out, n = ((rows, N) if len(sh) == 2 else (*sh[:-1], N)), (N,)
         if (x_scale is None) != (w_scale is None):
             raise ValueError("x_scale and w_scale come together")
-        _check(self._lib.cpdr_linear_fwd(self._h, rows, K, N, _addr("x", x, sh, it, dev), _addr("w", w, (N, K), it, dev),
-                                         _opt("x_scale", x_scale, sh[:-1], f32, dev),
-                                         _opt("w_scale", w_scale, n, f32, dev), _opt("bias", bias, n, f32, dev),
-                                         ACTIVATIONS[activation], _opt("residual", residual, out, bf16, dev),
-                                         _opt("z", z, out, bf16, dev), _addr("y", y, out, bf16, dev),
+        _check(self._lib.cpdr_linear_fwd(self._h, rows, K, N, _addr("x", x, sh, it, dev),
+                                         _addr("w", w, (N, K), it, dev),
+                                         None if x_scale is None else _addr("x_scale", x_scale, sh[:-1], _F32, dev),
+                                         _addr("w_scale", w_scale, n, _F32, dev), _addr("bias", bias, n, _F32, dev),
+                                         ACTIVATIONS[activation], _addr("residual", residual, out, _BF16, dev),
+                                         _addr("z", z, out, _BF16, dev), _addr("y", y, out, _BF16, dev),
                                          _raw_stream(stream, dev)))
 
     def linear_bwd_workspace_bytes(self, rows, K, N, activation=None):
@@ -540,11 +540,13 @@ class Context:
         (bf16) and dbias (fp32).  Of a given ``out`` only the entries that it
         holds are computed."""
         rows, K = self._rows(x)
-        bf16, dev, act = torch.bfloat16, self._dev, ACTIVATIONS[activation]
+        dev, act = self._dev, ACTIVATIONS[activation]
         N = w.shape[0]
         wide = (*x.shape[:-1], N)
-        args = (_addr("x", x, x.shape, bf16, dev), _addr("w", w, (N, K), bf16, dev),
-                _addr("z", z, wide, bf16, dev) if act else None, _addr("dy", dy, wide, bf16, dev), act)
+        if act and z is None:
+            raise ValueError("z is missing: the gradient of an activation needs it")
+        args = (_addr("x", x, x.shape, _BF16, dev), _addr("w", w, (N, K), _BF16, dev),
+                _addr("z", z, wide, _BF16, dev), _addr("dy", dy, wide, _BF16, dev), act)
         with _owned_by(stream):
             if out is None:
                 out = dict(dx=torch.empty_like(x), dw=torch.empty_like(w),
@@ -552,9 +554,9 @@ class Context:
             if workspace is None:
                 workspace = torch.empty(self.linear_bwd_workspace_bytes(rows, K, N, activation), dtype=torch.uint8,
                                         device=x.device)
-        _check(self._lib.cpdr_linear_bwd(self._h, rows, K, N, *args, _opt("dx", out.get("dx"), x.shape, bf16, dev),
-                                         _opt("dw", out.get("dw"), w.shape, bf16, dev),
-                                         _opt("dbias", out.get("dbias"), (N,), torch.float32, dev),
+        _check(self._lib.cpdr_linear_bwd(self._h, rows, K, N, *args, _addr("dx", out.get("dx"), x.shape, _BF16, dev),
+                                         _addr("dw", out.get("dw"), w.shape, _BF16, dev),
+                                         _addr("dbias", out.get("dbias"), (N,), torch.float32, dev),
                                          *_space(workspace, dev), _raw_stream(stream, dev)))
         return out
 
