@@ -25,14 +25,16 @@
 //  * narrow_kernel, for few rows of x, bound by reading w: 128 rows of w (the
 //    128 lanes) by 16 to 128 rows of x (the columns) per CTA, with r split
 //    over a cluster of up to 8 CTAs, whose partial sums meet in distributed
-//    shared memory in the order of the CTAs.  16 x 2048 x 6144: 9.7 us (25 MB
-//    of w; the library's product 6.3), of which 1.3 between kernels, 5.6 until
-//    the last byte of w, 1.9 for the partial sums and the epilogue.
+//    shared memory in the order of the CTAs.  16 x 2048 x 6144: 8.5 us (25 MB
+//    of w, 3.7 us at the measured copy rate; the library's product 6.3): 2 us
+//    until the unit has fetched the tensors' maps and the first bytes are
+//    there, 3 us until the last of w, 1.5 for the partial sums and the epilogue.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "cpdr_internal.hpp"
 #include "launch.cuh"
@@ -657,38 +659,68 @@ narrow_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
             float xs[M];
 #pragma unroll
             for (int j = 0; j < M; j++) {
-                r[j] = a.e.residual && j < n ? a.e.residual[o + j * a.Q] : __nv_bfloat16(0.f);
-                xs[j] = a.e.ws && j < n ? a.e.xs[p + j] * ws : 1.f;
+                r[j] = __nv_bfloat16(0.f);
+                xs[j] = 1.f;
+            }
+            if (a.e.residual) {
+#pragma unroll
+                for (int j = 0; j < M; j++)
+                    if (j < n) r[j] = a.e.residual[o + j * a.Q];
+            }
+            if (a.e.ws) {
+#pragma unroll
+                for (int j = 0; j < M; j++)
+                    if (j < n) xs[j] = a.e.xs[p + j] * ws;
+            }
+            if (a.e.ws) {
+#pragma unroll
+                for (int j = 0; j < M; j++) d[j] *= xs[j];
             }
 #pragma unroll
-            for (int j = 0; j < M; j++) {
-                if (a.e.ws) d[j] *= xs[j];
-                d[j] += bias;
-                if (a.e.has_z && j < n) a.z[o + j * a.Q] = __float2bfloat16_rn(d[j]);
-            }
-            if (a.e.act) {
+            for (int j = 0; j < M; j++) d[j] += bias;
+            if (a.e.has_z) {
 #pragma unroll
-                for (int j = 0; j < M; j++) d[j] = a.e.act == 1 ? silu(d[j]) : gelu(d[j]);
+                for (int j = 0; j < M; j++)
+                    if (j < n) a.z[o + j * a.Q] = __float2bfloat16_rn(d[j]);
+            }
+            if (a.e.act == 1) {
+#pragma unroll
+                for (int j = 0; j < M; j++) d[j] = silu(d[j]);
+            } else if (a.e.act == 2) {
+#pragma unroll
+                for (int j = 0; j < M; j++) d[j] = gelu(d[j]);
             }
 #pragma unroll
             for (int j = 0; j < M; j++)
                 if (j < n) a.y[o + j * a.Q] = __float2bfloat16_rn(d[j] + __bfloat162float(r[j]));
         };
         if (split > 1) {
-            // this CTA's groups, each summed in the order of the CTAs
-            for (int i = 0; i < groups && p0 + 4 * (g0 + i) < a.P; i++) {
-                float d[4] = {};
-                const float4 *s = sums + i * split * 128 + row;
-                switch (split) {
-                    case 2: add_group<2>(s, d); break;
-                    case 3: add_group<3>(s, d); break;
-                    case 4: add_group<4>(s, d); break;
-                    case 5: add_group<5>(s, d); break;
-                    case 6: add_group<6>(s, d); break;
-                    case 7: add_group<7>(s, d); break;
-                    default: add_group<8>(s, d); break;
+            // this CTA's groups, each summed in the order of the CTAs; four
+            // groups at a time, which fill one another's latencies
+            auto run = [&](auto s) {
+                constexpr int S = decltype(s)::value;
+                int i = 0;
+                for (; i + 4 <= groups && p0 + 4 * (g0 + i) < a.P; i += 4) {
+                    float d[16] = {};
+#pragma unroll
+                    for (int g = 0; g < 4; g++)
+                        add_group<S>(sums + (i + g) * S * 128 + row, *reinterpret_cast<float(*)[4]>(&d[4 * g]));
+                    out(4 * (g0 + i), d);
                 }
-                out(4 * (g0 + i), d);
+                for (; i < groups && p0 + 4 * (g0 + i) < a.P; i++) {
+                    float d[4] = {};
+                    add_group<S>(sums + i * S * 128 + row, d);
+                    out(4 * (g0 + i), d);
+                }
+            };
+            switch (split) {
+                case 2: run(std::integral_constant<int, 2>()); break;
+                case 3: run(std::integral_constant<int, 3>()); break;
+                case 4: run(std::integral_constant<int, 4>()); break;
+                case 5: run(std::integral_constant<int, 5>()); break;
+                case 6: run(std::integral_constant<int, 6>()); break;
+                case 7: run(std::integral_constant<int, 7>()); break;
+                default: run(std::integral_constant<int, 8>()); break;
             }
         } else {
 #pragma unroll
@@ -829,8 +861,8 @@ int narrow(const Operand &W, const Operand &X, Args a, int split, cudaStream_t s
 }
 
 // Which kernel runs a product whose rows p are rows of x, by an estimate of
-// its cycles from measured parts (16 x 2048 x 6144: 9.7 us narrow, 17 wide;
-// 256 x 2048 x 6144: 38 us narrow, 18 wide).
+// its cycles from measured parts (64 x 2048 x 6144: 10.4 us narrow, 16 wide;
+// 256 x 2048 x 6144: 38 us narrow with 128 rows of x a tile, 16 wide).
 struct Choice {
     int qn = 0, split = 1;   // qn 0: wide_kernel
 };
@@ -839,7 +871,7 @@ Choice choose(int64_t P, int64_t Q, int blocks, int sms) {
     // tiles one after the other: 590 cycles for a block (512 are the products'),
     // 7000 for an epilogue that goes on meanwhile; the first load and the last
     // epilogue alone
-    double cost = (double)up(up(P, kTile) * up(Q, kTile), sms / 2) * std::max(blocks * 590.0, 7000.0) + 11500.0;
+    double cost = (double)up(up(P, kTile) * up(Q, kTile), sms / 2) * std::max(blocks * 590.0, 7000.0) + 10500.0;
     for (int qn = 16; qn <= 128; qn *= 2) {
         if (up(Q, 128) > 65535 || up(P, qn) > 65535) continue;
         const int64_t tiles = up(P, qn) * up(Q, 128);
@@ -851,7 +883,7 @@ Choice choose(int64_t P, int64_t Q, int blocks, int sms) {
             const int64_t waves = up(tiles * split, room);
             const double together = waves > 1 ? fit : (double)up(tiles * split, sms);
             // a column's epilogue, or its partial sums to send and to add
-            const double columns = split > 1 ? 1500.0 + 50.0 * qn : 150.0 * qn;
+            const double columns = split > 1 ? 1500.0 + 40.0 * qn : 100.0 * qn;
             const double c = waves * (up(blocks, split) * block * together + 7000.0 + columns);
             if (c < cost) {
                 cost = c;
