@@ -18,11 +18,12 @@ namespace cpdr {
 __device__ __forceinline__ void next_grid_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void previous_grid_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// `bytes`: dynamic shared memory (the kernel's limit is raised where it is
-// over the default); `cluster`: blocks of a cluster along x.
+// `bytes`: dynamic shared memory.  The kernel's limit is raised where, with up
+// to 8 KB of static shared memory, it could pass the default of 48 KB.
+// `cluster`: blocks of a cluster along x.
 template <typename... P, typename... A>
 int launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t bytes, int cluster, void *stream, A &&...args) {
-    if (bytes > 48 * 1024) {
+    if (bytes > 40 * 1024) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
         if (e != cudaSuccess) return (int)e;
     }

@@ -9,12 +9,17 @@
 //     dw_i = sum over rows of dy_i s_i rstd.
 //
 // Bound by HBM: every tensor is read and written once.  A row lives in the
-// registers of one group of threads (1 to 1024 of them, one to four 16-byte
+// registers of one group of threads (1 to 512 of them, one to eight 16-byte
 // vectors each), which needs one reduction for everything: the e4m3 row's
 // largest |s w| comes with the sum of squares, since rounding is monotonic
 // and rstd is one number per row, so max|y| is max|s w| times rstd exactly.
 // Sums, statistics and dw are fp32; s is rounded once where it is stored, and
 // y is computed from the unrounded sum.
+//
+// Measured over 0.4 GB a tensor: forward 6.8 to 7.1 TB/s (bf16 with a
+// residual, 72 to 12288 columns) and 6.4 to 7.1 (fp32); backward 4.1 to 6.1
+// TB/s up to 8192 columns of bf16, 5.8 to 6.7 up to 2560 of fp32, and 3.8 to
+// 5.7 for wider rows: few rows an SM are in flight there.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -83,9 +88,15 @@ struct FwdParams {
     float eps, inv_width;
 };
 
-// grid: row blocks of kBlock / TPR rows
-template <typename T, int TPR, int NV, bool E4M3>
-__global__ void __launch_bounds__(kBlock<TPR>) rmsnorm_fwd_kernel(FwdParams p) {
+// Wide fp32 rows without a residual have few loads in flight: they take 64
+// registers a thread, 1024 threads an SM (16384 columns 4.5 -> 6.9 TB/s; with
+// a residual that costs spills, 6.9 -> 5.9).
+template <typename T, int NV, bool RES>
+constexpr bool kFwdSlim = kVecOf<T> == 4 && NV >= 4 && !RES;
+
+// grid: row blocks of kBlock / TPR rows; RES: a residual may be given
+template <typename T, int TPR, int NV, bool E4M3, bool RES>
+__global__ void __launch_bounds__(kBlock<TPR>, kFwdSlim<T, NV, RES> ? 1024 / TPR : 1) rmsnorm_fwd_kernel(FwdParams p) {
     constexpr int V = kVecOf<T>;
     __shared__ float2 sh[64];
     next_grid_may_start();
@@ -95,7 +106,7 @@ __global__ void __launch_bounds__(kBlock<TPR>) rmsnorm_fwd_kernel(FwdParams p) {
     const bool live = row < p.rows;
     const int64_t o = row * p.width;
     const T *x = (const T *)p.x + o;
-    const T *res = p.res ? (const T *)p.res + o : nullptr;
+    const T *res = RES && p.res ? (const T *)p.res + o : nullptr;
     uint4 xr[NV], rr[NV];
 #pragma unroll
     for (int i = 0; i < NV; i++) {
@@ -182,90 +193,120 @@ struct BwdParams {
     float eps, inv_width;
 };
 
+// Blocks of an SM that the backward's registers leave room for: its grid, one
+// wave of them, and the bound that holds the compiler to it.  Spills cost more
+// than the missing warps: rows of 12288 ran at 1.6 TB/s as 1024 threads of 64
+// registers, at 4.3 (bf16) and 5.2 (fp32) as 512 of 128.
+template <typename T, int TPR, int NV>
+constexpr int kBwdPerSm = kBlock<TPR> > 256 ? 1 : NV == 1 ? 4 : kVecOf<T> == 8 ? 2 : 3;
+// The next row's loads are kept in flight while a row is summed, where its
+// vectors leave registers for them (bf16 rows of 8192 3.7 -> 5.2 TB/s; fp32
+// rows of 768, three vectors, run at 6.7 without them and at 5.8 with them).
+template <typename T, int NV>
+constexpr bool kBwdAhead = NV <= 2;
+
 // persistent: each group of TPR threads takes every (gridDim.x * groups)-th
 // row, with the next row's loads in flight, and sums its rows' dw terms in
-// registers; the block's sum goes to its row of `part`.
+// registers; the block's sum goes to its row of `part`.  The weights lie in
+// shared memory and the row stays as it was loaded (widened where it is used,
+// twice), so that registers are left for the loads in flight.
 template <typename T, int TPR, int NV>
-__global__ void __launch_bounds__(kBlock<TPR>) rmsnorm_bwd_kernel(BwdParams p) {
+__global__ void __launch_bounds__(kBlock<TPR>, kBwdPerSm<T, TPR, NV>) rmsnorm_bwd_kernel(BwdParams p) {
     constexpr int V = kVecOf<T>;
-    constexpr int G = kBlock<TPR> / TPR;
+    constexpr int G = kBlock<TPR> / TPR, ROW = TPR * NV * V;
+    constexpr bool AHEAD = kBwdAhead<T, NV>;
     __shared__ float2 sh[64];
-    extern __shared__ float dw_sh[];
+    extern __shared__ __align__(16) float row_sh[];   // ROW weights; at the end the groups' dw
     next_grid_may_start();
     previous_grid_done();
     const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
     const int64_t stride = (int64_t)gridDim.x * G;
     const T *sp = (const T *)p.s, *dyp = (const T *)p.dy, *dsp = (const T *)p.dsum;
-    float w[NV][V], dw[NV][V];
+    for (int i = threadIdx.x; i < ROW; i += kBlock<TPR>) row_sh[i] = i < p.width ? p.w[i] : 0.f;
+    float dw[NV][V];
 #pragma unroll
-    for (int i = 0; i < NV; i++) {
-        const int col = (i * TPR + t) * V;
+    for (int i = 0; i < NV; i++)
 #pragma unroll
-        for (int j = 0; j < V; j++) {
-            w[i][j] = col < p.width ? p.w[col + j] : 0.f;
-            dw[i][j] = 0.f;
-        }
-    }
-    uint4 sr[NV], dr[NV], ur[NV];
-    auto load = [&](int64_t row) {
+        for (int j = 0; j < V; j++) dw[i][j] = 0.f;
+    struct Raw {
+        uint4 s[NV], d[NV], u[NV];
+    };
+    auto load = [&](Raw &r, int64_t row) {
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             const int col = (i * TPR + t) * V;
-            sr[i] = dr[i] = ur[i] = make_uint4(0, 0, 0, 0);
+            r.s[i] = r.d[i] = r.u[i] = make_uint4(0, 0, 0, 0);
             if (row < p.rows && col < p.width) {
                 const int64_t o = row * p.width + col;
-                sr[i] = load16(sp + o);
-                dr[i] = load16(dyp + o);
-                if (dsp) ur[i] = load16(dsp + o);
+                r.s[i] = load16(sp + o);
+                r.d[i] = load16(dyp + o);
+                if (dsp) r.u[i] = load16(dsp + o);
             }
         }
     };
+    auto weights = [&](int i, float (&w)[V]) {
+#pragma unroll
+        for (int j = 0; j < V; j += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(row_sh + (i * TPR + t) * V + j);
+            w[j] = v.x;
+            w[j + 1] = v.y;
+            w[j + 2] = v.z;
+            w[j + 3] = v.w;
+        }
+    };
+    __syncthreads();
     int64_t row = (int64_t)blockIdx.x * G + grp;
-    load(row);
+    Raw cur, next;
+    if (AHEAD) load(cur, row);
     int par = 0;
     // every group of the block makes the same number of turns (the barriers)
     for (int64_t base = (int64_t)blockIdx.x * G; base < p.rows; base += stride, row += stride, par ^= 1) {
-        float s[NV][V], d[NV][V], u[NV][V];
+        if (AHEAD) load(next, row + stride);
+        else load(cur, row);
         float ss = 0.f, dot = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            widen16(sr[i], s[i]);
-            widen16(dr[i], d[i]);
-            widen16(ur[i], u[i]);
-        }
-        load(row + stride);
-#pragma unroll
-        for (int i = 0; i < NV; i++)
+            float s[V], d[V], w[V];
+            widen16(cur.s[i], s);
+            widen16(cur.d[i], d);
+            weights(i, w);
 #pragma unroll
             for (int j = 0; j < V; j++) {
-                ss = fmaf(s[i][j], s[i][j], ss);
-                dot = fmaf(s[i][j], w[i][j] * d[i][j], dot);
+                ss = fmaf(s[j], s[j], ss);
+                dot = fmaf(s[j], w[j] * d[j], dot);
             }
+        }
         const float2 st = row_reduce<TPR, false>(ss, dot, sh, par);
         const float rstd = rsqrtf(fmaf(st.x, p.inv_width, p.eps));
         const float k = rstd * rstd * (st.y * p.inv_width);
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             const int col = (i * TPR + t) * V;
-            float ds[V];
+            float s[V], d[V], u[V], w[V], ds[V];
+            widen16(cur.s[i], s);
+            widen16(cur.d[i], d);
+            widen16(cur.u[i], u);
+            weights(i, w);
 #pragma unroll
             for (int j = 0; j < V; j++) {
-                dw[i][j] = fmaf(d[i][j], s[i][j] * rstd, dw[i][j]);
-                ds[j] = fmaf(rstd, fmaf(w[i][j], d[i][j], -k * s[i][j]), u[i][j]);
+                dw[i][j] = fmaf(d[j], s[j] * rstd, dw[i][j]);
+                ds[j] = fmaf(rstd, fmaf(w[j], d[j], -k * s[j]), u[j]);
             }
             if (row < p.rows && col < p.width) store16((T *)p.ds + row * p.width + col, ds);
         }
+        if (AHEAD) cur = next;
     }
     float *part = p.part + (int64_t)blockIdx.x * p.width;
     if (G > 1) {
+        __syncthreads();   // the weights have been read
 #pragma unroll
         for (int i = 0; i < NV; i++)
 #pragma unroll
-            for (int j = 0; j < V; j++) dw_sh[grp * (TPR * NV * V) + (i * TPR + t) * V + j] = dw[i][j];
+            for (int j = 0; j < V; j++) row_sh[grp * ROW + (i * TPR + t) * V + j] = dw[i][j];
         __syncthreads();
         for (int col = threadIdx.x; col < p.width; col += kBlock<TPR>) {
             float v = 0.f;
-            for (int i = 0; i < G; i++) v += dw_sh[i * (TPR * NV * V) + col];
+            for (int i = 0; i < G; i++) v += row_sh[i * ROW + col];
             part[col] = v;
         }
     } else {
@@ -303,55 +344,103 @@ column_sums_kernel(const float *__restrict__ part, int nparts, int width, float 
     }
 }
 
-template <typename T, int TPR, int NV>
-int fwd(const FwdParams &p, cudaStream_t st) {
+template <typename T, int TPR, int NV, bool RES>
+int fwd_as(const FwdParams &p, cudaStream_t st) {
     constexpr int per = kBlock<TPR> / TPR;
     const int64_t grid = (p.rows + per - 1) / per;
     if (grid > (int64_t)0x7fffffff) return (int)cudaErrorInvalidValue;
-    return launch_early(p.y8 ? rmsnorm_fwd_kernel<T, TPR, NV, true> : rmsnorm_fwd_kernel<T, TPR, NV, false>,
+    return launch_early(p.y8 ? rmsnorm_fwd_kernel<T, TPR, NV, true, RES> : rmsnorm_fwd_kernel<T, TPR, NV, false, RES>,
                         dim3((unsigned)grid), kBlock<TPR>, 0, 1, st, p);
+}
+template <typename T, int TPR, int NV>
+int fwd(const FwdParams &p, cudaStream_t st) {
+    if constexpr (kFwdSlim<T, NV, false>) {
+        if (!p.res) return fwd_as<T, TPR, NV, false>(p, st);
+    }
+    return fwd_as<T, TPR, NV, true>(p, st);
 }
 
 template <typename T, int TPR, int NV>
 int bwd(const BwdParams &p, int grid, float *dw, cudaStream_t st) {
     constexpr int G = kBlock<TPR> / TPR;
-    const size_t smem = G > 1 ? (size_t)G * TPR * NV * kVecOf<T> * sizeof(float) : 0;
-    static_assert((G > 1 ? G * TPR * NV * kVecOf<T> * 4 : 0) <= 48 * 1024, "dw staging within the default shared memory");
+    constexpr size_t smem = (size_t)G * TPR * NV * kVecOf<T> * sizeof(float);
+    static_assert(smem * kBwdPerSm<T, TPR, NV> <= 220 * 1024, "the blocks of an SM fit its shared memory");
     const int rc = launch_early(rmsnorm_bwd_kernel<T, TPR, NV>, dim3((unsigned)grid), kBlock<TPR>, smem, 1, st, p);
     if (rc) return rc;
     return launch_column_sums(p.part, grid, p.width, dw, st);
 }
 
-// Threads per row: one 16-byte vector each for rows of up to 32 vectors, two
-// for wider ones, four for the widest fp32 rows.
+template <int TPR, int NV, typename F>
+int with(F f) {
+    return f(std::integral_constant<int, TPR>(), std::integral_constant<int, NV>());
+}
+
+// Threads per row, and 16-byte vectors for each of them: groups of up to 256
+// threads with one or two vectors, three where two would leave a quarter of
+// the threads idle or more (bf16 rows of 264, forward 6.1 -> 7.0 TB/s and
+// backward 3.3 -> 5.1), and up to eight for wide rows.
+template <typename T, typename F>
+int narrow_row(int vecs, F f) {
+    if (vecs <= 1) return with<1, 1>(f);
+    if (vecs <= 2) return with<2, 1>(f);
+    if (vecs <= 4) return with<4, 1>(f);
+    if (vecs <= 8) return with<8, 1>(f);
+    if (vecs <= 12) return with<4, 3>(f);
+    if (vecs <= 16) return with<16, 1>(f);
+    if (vecs <= 24) return with<8, 3>(f);
+    if (vecs <= 32) return with<32, 1>(f);
+    if (vecs <= 48) return with<16, 3>(f);
+    if (vecs <= 64) return with<32, 2>(f);
+    if (vecs <= 96) return with<32, 3>(f);
+    if (vecs <= 128) return with<64, 2>(f);
+    if (vecs <= 192) return with<64, 3>(f);
+    if (vecs <= 256) return with<128, 2>(f);
+    if (vecs <= 384) return with<128, 3>(f);
+    if (vecs <= 512) return with<256, 2>(f);
+    return with<256, 3>(f);
+}
 template <typename T, typename F>
 int by_width(int width, F f) {
     const int vecs = (width + kVecOf<T> - 1) / kVecOf<T>;
-    if (vecs <= 1) return f(std::integral_constant<int, 1>(), std::integral_constant<int, 1>());
-    if (vecs <= 2) return f(std::integral_constant<int, 2>(), std::integral_constant<int, 1>());
-    if (vecs <= 4) return f(std::integral_constant<int, 4>(), std::integral_constant<int, 1>());
-    if (vecs <= 8) return f(std::integral_constant<int, 8>(), std::integral_constant<int, 1>());
-    if (vecs <= 16) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 1>());
-    if (vecs <= 32) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 1>());
-    if (vecs <= 64) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 2>());
-    if (vecs <= 128) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 2>());
-    if (vecs <= 256) return f(std::integral_constant<int, 128>(), std::integral_constant<int, 2>());
-    if (vecs <= 512) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 2>());
-    if (vecs <= 1024) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 2>());
+    if (vecs <= 768) return narrow_row<T>(vecs, f);
+    if (vecs <= 1024) return with<256, 4>(f);
+    if (vecs <= 1536) return with<256, 6>(f);
     if constexpr (kVecOf<T> == 4) {
-        if (vecs > 2048) return f(std::integral_constant<int, 1024>(), std::integral_constant<int, 4>());
+        if (vecs > 2048) return with<512, 8>(f);
     }
-    return f(std::integral_constant<int, 1024>(), std::integral_constant<int, 2>());
+    return with<256, 8>(f);
+}
+// The same for the backward, whose thread holds dw besides: blocks of 512
+// threads from 768 vectors on.
+template <typename T, typename F>
+int by_width_bwd(int width, F f) {
+    const int vecs = (width + kVecOf<T> - 1) / kVecOf<T>;
+    if (vecs <= 768) return narrow_row<T>(vecs, f);
+    if (vecs <= 1024) return with<512, 2>(f);
+    if (vecs <= 1536) return with<512, 3>(f);
+    if constexpr (kVecOf<T> == 4) {
+        if (vecs > 2048) return with<512, 8>(f);
+    }
+    return with<512, 4>(f);
 }
 
-int rows_per_block(int width, bool f32) {
-    auto g = [](auto tpr, auto) { return kBlock<decltype(tpr)::value> / decltype(tpr)::value; };
-    return f32 ? by_width<float>(width, g) : by_width<__nv_bfloat16>(width, g);
+struct Shape {
+    int rows, per_sm;   // rows of a block, blocks of an SM
+};
+template <typename T>
+Shape bwd_shape(int width) {
+    Shape s{};
+    by_width_bwd<T>(width, [&](auto tpr, auto nv) {
+        constexpr int TPR = decltype(tpr)::value;
+        s = Shape{kBlock<TPR> / TPR, kBwdPerSm<T, TPR, decltype(nv)::value>};
+        return CPDR_OK;
+    });
+    return s;
 }
 
 }  // namespace
 
-static_assert(kMaxNormWidth <= 1024 * 4 * kVecOf<float> && kMaxNormWidth <= 1024 * 2 * kVecOf<__nv_bfloat16>, "a row fits the registers of one block");
+static_assert(kMaxNormWidth <= 512 * 8 * kVecOf<float> && kMaxNormWidth <= 512 * 4 * kVecOf<__nv_bfloat16>, "a row fits the registers of one block");
 
 int launch_column_sums(const float *part, int nparts, int width, float *out, void *stream) {
     return launch_early(column_sums_kernel, dim3((unsigned)((width + kSumCols - 1) / kSumCols)), kSumCols * kSumRows, 0, 1, stream,
@@ -372,13 +461,11 @@ int launch_rmsnorm_fwd(const cpdr_ctx *c, int64_t rows, int width, const void *x
     });
 }
 
-// Blocks of the backward: four per SM (one for rows of 1024 threads), and no
-// more than there are rows.
+// Blocks of the backward: one wave, and no more than there are rows.
 int rmsnorm_bwd_grid(const cpdr_ctx *c, int64_t rows, int width) {
-    const int per = rows_per_block(width, c->plan.in_dtype == CPDR_DTYPE_F32);
-    const int64_t blocks = (rows + per - 1) / per;
-    const int64_t most = (int64_t)device_sms(c->device) * (width > 4096 ? 2 : 4);
-    return (int)std::max<int64_t>(1, std::min(blocks, most));
+    const Shape s = c->plan.in_dtype == CPDR_DTYPE_F32 ? bwd_shape<float>(width) : bwd_shape<__nv_bfloat16>(width);
+    const int64_t blocks = (rows + s.rows - 1) / s.rows;
+    return (int)std::max<int64_t>(1, std::min(blocks, (int64_t)device_sms(c->device) * s.per_sm));
 }
 
 int launch_rmsnorm_bwd(const cpdr_ctx *c, int64_t rows, int width, const void *s, const float *weight, float eps,
@@ -387,10 +474,10 @@ int launch_rmsnorm_bwd(const cpdr_ctx *c, int64_t rows, int width, const void *s
     const int grid = rmsnorm_bwd_grid(c, rows, width);
     cudaStream_t st = (cudaStream_t)stream;
     if (c->plan.in_dtype == CPDR_DTYPE_F32)
-        return by_width<float>(width, [&](auto tpr, auto nv) {
+        return by_width_bwd<float>(width, [&](auto tpr, auto nv) {
             return bwd<float, decltype(tpr)::value, decltype(nv)::value>(p, grid, dweight, st);
         });
-    return by_width<__nv_bfloat16>(width, [&](auto tpr, auto nv) {
+    return by_width_bwd<__nv_bfloat16>(width, [&](auto tpr, auto nv) {
         return bwd<__nv_bfloat16, decltype(tpr)::value, decltype(nv)::value>(p, grid, dweight, st);
     });
 }

@@ -88,6 +88,12 @@ def test_widths(width, dtype):
         close(out["dweight"], b["dweight"], b["e_dweight"], "fp32")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("width", [40, 48, 72, 88, 96, 192, 384, 776, 1536, 2560, 5208, 6144, 10000, 12288, 12296, 16376])
+def test_widths_between(width, dtype):
+    test_widths(width, dtype)
+
+
 @pytest.mark.parametrize("rows,width", [(1, 64), (2, 2048), (3, 128), (15, 8), (16, 128), (17, 128), (3001, 128),
                                         (2049, 264), (700, 2048)])
 def test_rows(rows, width):
