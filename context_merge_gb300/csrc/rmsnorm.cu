@@ -277,7 +277,8 @@ __global__ void __launch_bounds__(kBlock<TPR>, kBwdPerSm<T, TPR, NV>) rmsnorm_bw
             }
         }
         const float2 st = row_reduce<TPR, false>(ss, dot, sh, par);
-        const float rstd = rsqrtf(fmaf(st.x, p.inv_width, p.eps));
+        // rows past the last are zeros: with eps of 0 their rstd would be infinite
+        const float rstd = row < p.rows ? rsqrtf(fmaf(st.x, p.inv_width, p.eps)) : 0.f;
         const float k = rstd * rstd * (st.y * p.inv_width);
 #pragma unroll
         for (int i = 0; i < NV; i++) {

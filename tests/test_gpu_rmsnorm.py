@@ -88,6 +88,22 @@ def test_widths(width, dtype):
         close(out["dweight"], b["dweight"], b["e_dweight"], "fp32")
 
 
+@pytest.mark.parametrize("rows,width", [(1, 8), (3, 64), (37, 136), (700, 264), (5, 776)])
+def test_eps_of_zero(rows, width):
+    # groups of threads without a row of their own must not reach dweight
+    d = draw(rows, width, "fp32", 11)
+    c = {k: v.cuda() for k, v in d.items()}
+    ctx = context("fp32")
+    f, b = ol.rmsnorm_forward(d["x"], d["w"], 0.0), ol.rmsnorm_backward(d["x"], d["w"], 0.0, d["dy"])
+    y = torch.empty_like(c["x"])
+    ctx.rmsnorm_fwd(c["x"], c["w"], y=y, eps=0.0)
+    out = ctx.rmsnorm_bwd(c["x"], c["w"], c["dy"], eps=0.0)
+    torch.cuda.synchronize()
+    close(y, f["y"], ol.ROW * np.abs(f["y"]), "fp32")
+    close(out["ds"], b["ds"], b["e_ds"], "fp32")
+    close(out["dweight"], b["dweight"], b["e_dweight"], "fp32")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("width", [40, 48, 72, 88, 96, 192, 384, 776, 1536, 2560, 5208, 6144, 10000, 12288, 12296, 16376])
 def test_widths_between(width, dtype):
