@@ -17,9 +17,9 @@
 // y is computed from the unrounded sum.
 //
 // Measured over 0.4 GB a tensor: forward 6.8 to 7.1 TB/s (bf16 with a
-// residual, 72 to 12288 columns) and 6.4 to 7.1 (fp32); backward 4.1 to 6.1
-// TB/s up to 8192 columns of bf16, 5.8 to 6.7 up to 2560 of fp32, and 3.8 to
-// 5.7 for wider rows: few rows an SM are in flight there.
+// residual, 72 to 12288 columns) and 6.4 to 7.1 (fp32); backward 4.0 to 6.0
+// TB/s up to 8192 columns of bf16, 5.9 to 6.7 up to 6144 of fp32, and 3.8 to
+// 5.7 for wider rows: few of them are in flight in an SM.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -196,22 +196,28 @@ struct BwdParams {
 // Blocks of an SM that the backward's registers leave room for: its grid, one
 // wave of them, and the bound that holds the compiler to it.  Spills cost more
 // than the missing warps: rows of 12288 ran at 1.6 TB/s as 1024 threads of 64
-// registers, at 4.3 (bf16) and 5.2 (fp32) as 512 of 128.
+// registers, at 4.3 (bf16) and 5.3 (fp32) as 512 of 128.
 template <typename T, int TPR, int NV>
-constexpr int kBwdPerSm = kBlock<TPR> > 256 ? 1 : NV == 1 ? 4 : kVecOf<T> == 8 ? 2 : 3;
-// The next row's loads are kept in flight while a row is summed, where its
-// vectors leave registers for them (bf16 rows of 8192 3.7 -> 5.2 TB/s; fp32
-// rows of 768, three vectors, run at 6.7 without them and at 5.8 with them).
+constexpr int bwd_per_sm() {
+    constexpr bool f32 = kVecOf<T> == 4;
+    if (kBlock<TPR> > 256) return 1;
+    if (NV == 1) return f32 ? 6 : 5;
+    if (!f32 || NV > 3) return 2;
+    return NV == 2 ? 4 : 3;
+}
+// More blocks do more than the next row's loads in flight (128 columns 5.2 ->
+// 6.0 TB/s in bf16, fp32 rows of 4096 4.2 -> 6.1), but for two bf16 vectors,
+// whose 32 sums and products leave two blocks an SM (8192 columns 5.3 TB/s
+// with the loads ahead, 3.7 without).
 template <typename T, int NV>
-constexpr bool kBwdAhead = NV <= 2;
+constexpr bool kBwdAhead = NV == 2 && kVecOf<T> == 8;
 
 // persistent: each group of TPR threads takes every (gridDim.x * groups)-th
-// row, with the next row's loads in flight, and sums its rows' dw terms in
-// registers; the block's sum goes to its row of `part`.  The weights lie in
+// row and sums its rows' dw terms in registers; the block's sum goes to its row of `part`.  The weights lie in
 // shared memory and the row stays as it was loaded (widened where it is used,
 // twice), so that registers are left for the loads in flight.
 template <typename T, int TPR, int NV>
-__global__ void __launch_bounds__(kBlock<TPR>, kBwdPerSm<T, TPR, NV>) rmsnorm_bwd_kernel(BwdParams p) {
+__global__ void __launch_bounds__(kBlock<TPR>, bwd_per_sm<T, TPR, NV>()) rmsnorm_bwd_kernel(BwdParams p) {
     constexpr int V = kVecOf<T>;
     constexpr int G = kBlock<TPR> / TPR, ROW = TPR * NV * V;
     constexpr bool AHEAD = kBwdAhead<T, NV>;
@@ -365,7 +371,7 @@ template <typename T, int TPR, int NV>
 int bwd(const BwdParams &p, int grid, float *dw, cudaStream_t st) {
     constexpr int G = kBlock<TPR> / TPR;
     constexpr size_t smem = (size_t)G * TPR * NV * kVecOf<T> * sizeof(float);
-    static_assert(smem * kBwdPerSm<T, TPR, NV> <= 220 * 1024, "the blocks of an SM fit its shared memory");
+    static_assert(smem * bwd_per_sm<T, TPR, NV>() <= 220 * 1024, "the blocks of an SM fit its shared memory");
     const int rc = launch_early(rmsnorm_bwd_kernel<T, TPR, NV>, dim3((unsigned)grid), kBlock<TPR>, smem, 1, st, p);
     if (rc) return rc;
     return launch_column_sums(p.part, grid, p.width, dw, st);
@@ -411,16 +417,26 @@ int by_width(int width, F f) {
     }
     return with<256, 8>(f);
 }
-// The same for the backward, whose thread holds dw besides: blocks of 512
-// threads from 768 vectors on.
+// The same for the backward, whose thread holds dw besides: 512 threads a row
+// where the eight values of a bf16 vector, or eight vectors, would take too
+// many registers (fp32 rows of 6144 run at 6.6 TB/s as 256 x 6, at 4.9 as
+// 512 x 3; bf16 rows of 12288 at 4.0 and 4.3), and one bf16 vector instead of
+// two up to 128 threads (1024 columns 4.5 -> 5.3).
 template <typename T, typename F>
 int by_width_bwd(int width, F f) {
     const int vecs = (width + kVecOf<T> - 1) / kVecOf<T>;
+    if constexpr (kVecOf<T> == 8) {
+        if (vecs > 48 && vecs <= 64) return with<64, 1>(f);
+        if (vecs > 96 && vecs <= 128) return with<128, 1>(f);
+    }
     if (vecs <= 768) return narrow_row<T>(vecs, f);
-    if (vecs <= 1024) return with<512, 2>(f);
-    if (vecs <= 1536) return with<512, 3>(f);
     if constexpr (kVecOf<T> == 4) {
+        if (vecs <= 1024) return with<256, 4>(f);
+        if (vecs <= 1536) return with<256, 6>(f);
         if (vecs > 2048) return with<512, 8>(f);
+    } else {
+        if (vecs <= 1024) return with<512, 2>(f);
+        if (vecs <= 1536) return with<512, 3>(f);
     }
     return with<512, 4>(f);
 }
@@ -433,7 +449,7 @@ Shape bwd_shape(int width) {
     Shape s{};
     by_width_bwd<T>(width, [&](auto tpr, auto nv) {
         constexpr int TPR = decltype(tpr)::value;
-        s = Shape{kBlock<TPR> / TPR, kBwdPerSm<T, TPR, decltype(nv)::value>};
+        s = Shape{kBlock<TPR> / TPR, bwd_per_sm<T, TPR, decltype(nv)::value>()};
         return CPDR_OK;
     });
     return s;
