@@ -60,7 +60,8 @@ struct Args {
     Epilogue e;
     int64_t P, Q;            // rows and columns of D
     int blocks;              // stages of r
-    int tiles_p, tiles_q;
+    int tiles_p, tiles_q;    // wide_kernel: tiles, and how many of them stay whole
+    int whole;
     __nv_bfloat16 *y, *z;    // narrow_kernel
     int32_t *status;
 };
@@ -269,12 +270,26 @@ __device__ __forceinline__ void tile_at(const Args &a, int i, int &tp, int &tq) 
     tq = r / rows;
     tp = 8 * g + (r - tq * rows);
 }
+// The work of a pair: the first `whole` items are tiles, two each of those
+// behind them are a tile's halves of 128 columns (whole_tiles).
+struct Item {
+    int p, q;      // first row and column
+    bool half;
+};
+__device__ __forceinline__ int item_count(const Args &a) { return 2 * a.tiles_p * a.tiles_q - a.whole; }
+__device__ __forceinline__ Item item_at(const Args &a, int i) {
+    const int over = i - a.whole;
+    const bool half = over >= 0;
+    int tp, tq;
+    tile_at(a, half ? a.whole + (over >> 1) : i, tp, tq);
+    return Item{tp * kTile, tq * kTile + (half ? (over & 1) * (kTile / 2) : 0), half};
+}
 
 template <bool E4M3, bool A_MN, bool B_MN, bool RES>
 __global__ void __launch_bounds__(kWideThreads, 1)
 wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
             const __grid_constant__ CUtensorMap my, const __grid_constant__ CUtensorMap mz,
-            const __grid_constant__ CUtensorMap mr, Args a) {
+            const __grid_constant__ CUtensorMap mr, const __grid_constant__ CUtensorMap mbh, Args a) {
     constexpr int STAGES = kWideStages<RES>;
     extern __shared__ unsigned char raw[];
     unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -282,7 +297,7 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
     WideBars &b = *reinterpret_cast<WideBars *>(staging + kEpiWarps * kStaging<RES>);
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = ctarank();
-    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, tiles = a.tiles_p * a.tiles_q;
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, items = item_count(a);
     next_grid_may_start();
     if (threadIdx.x == 0) {
         b.ctl.abort = 0;
@@ -320,28 +335,31 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
         if (elected()) {
             const uint32_t full0 = remote(&b.full[0], 0);
             int it = 0;
-            for (int t = pair; t < tiles && !b.ctl.abort; t += pairs) {
-                int tp, tq;
-                tile_at(a, t, tp, tq);
-                const int p0 = tp * kTile + (int)rank * 128, q0 = tq * kTile + (int)rank * 128;
+            for (int t = pair; t < items && !b.ctl.abort; t += pairs) {
+                const Item job = item_at(a, t);
+                const int p0 = job.p + (int)rank * 128, q0 = job.q + (int)rank * (job.half ? 64 : 128);
                 for (int k = 0; k < a.blocks; k++, it++) {
                     const int s = it % STAGES;
                     if (!mbar_wait(&b.empty[s], (uint32_t)(it / STAGES + 1) & 1u, &b.ctl, a.status, 160)) break;
-                    if (rank == 0) mbar_arrive_expect_tx(&b.full[s], 2 * kWideStage);
+                    if (rank == 0) mbar_arrive_expect_tx(&b.full[s], job.half ? kWideStage + kHalfStage : 2 * kWideStage);
                     const uint32_t dst = smem_u32(base + s * kWideStage), bar = full0 + 8u * s;
                     load_stage<2, A_MN, E4M3>(dst, &ma, bar, p0, k);
-                    load_stage<2, B_MN, E4M3>(dst + kHalfStage, &mb, bar, q0, k);
+                    if (!job.half)
+                        load_stage<2, B_MN, E4M3>(dst + kHalfStage, &mb, bar, q0, k);
+                    else   // 64 rows: one box of either form
+                        tma_load<2>(dst + kHalfStage, &mbh, bar, B_MN ? q0 : k * (E4M3 ? 128 : 64), B_MN ? k * 64 : q0);
                 }
             }
         }
     } else if (w == kEpiWarps + 1) {
         // -------------------------------------------------------- products
         if (rank == 0 && elected()) {
-            constexpr uint32_t id = idesc_of<E4M3, A_MN, B_MN>(256, 256);
+            constexpr uint32_t id_whole = idesc_of<E4M3, A_MN, B_MN>(256, 256), id_half = idesc_of<E4M3, A_MN, B_MN>(256, 128);
             const uint64_t ad = stage_desc<A_MN>(smem_u32(base)), bd = stage_desc<B_MN>(smem_u32(base + kHalfStage));
             int it = 0, n = 0;
-            for (int t = pair; t < tiles && !b.ctl.abort; t += pairs, n++) {
+            for (int t = pair; t < items && !b.ctl.abort; t += pairs, n++) {
                 const int acc = n & 1;
+                const uint32_t id = t < a.whole ? id_whole : id_half;
                 if (!mbar_wait(&b.acc_empty[acc], (uint32_t)((n >> 1) + 1) & 1u, &b.ctl, a.status, 161)) break;
                 tc_fence_after();
                 for (int k = 0; k < a.blocks; k++, it++) {
@@ -360,23 +378,23 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
     } else {
         // -------------------------------------------------------- epilogue
         // warp w: TMEM lanes (rows) 32 (w % 4) .. + 31, columns 128 (w / 4) ..
-        // + 127, in two pieces of 64.  The residual's pieces come into the
+        // + 127 in two pieces of 64 (of half a tile: 64 (w / 4) .. + 63).  The residual's pieces come into the
         // staging tiles by TMA while the products run (a lane owns a row, and 32
         // rows are 32 lines to a load instruction: fetched by loads they took
         // 3000 cycles of a tile), and y takes their place.
         // Where z is wanted too, a second pass over the piece writes it.
-        const int quad = w & 3, c0 = (w >> 2) * kEpiCols;
+        const int quad = w & 3;
         unsigned char *mine = staging + w * kStaging<RES>;
         const uint32_t empty0 = remote(&b.acc_empty[0], 0);
         int n = 0, fetched = 0;
-        for (int t = pair; t < tiles; t += pairs, n++) {
+        for (int t = pair; t < items; t += pairs, n++) {
             const int acc = n & 1;
-            int tp, tq;
-            tile_at(a, t, tp, tq);
-            const int64_t p0 = (int64_t)tp * kTile + rank * 128 + quad * 32, p = p0 + lane;
-            const int64_t q0 = (int64_t)tq * kTile + c0;
+            const Item it = item_at(a, t);
+            const int last = it.half ? 0 : 1, c0 = (w >> 2) * (it.half ? kEpiCols / 2 : kEpiCols);
+            const int64_t p0 = (int64_t)it.p + rank * 128 + quad * 32, p = p0 + lane;
+            const int64_t q0 = (int64_t)it.q + c0;
             const float xs = a.e.xs && p < a.P ? a.e.xs[p] : 1.f;
-            const int pieces = p0 < a.P ? (q0 + 64 < a.Q ? 2 : q0 < a.Q ? 1 : 0) : 0;   // that hold any of D
+            const int pieces = p0 < a.P ? (q0 + 64 < a.Q ? 1 + last : q0 < a.Q ? 1 : 0) : 0;   // that hold any of D
             if (RES && pieces && elected()) {
                 tma_store_wait();   // the staging tiles have been read
                 const uint32_t bar = smem_u32(&b.residual[w]);
@@ -401,7 +419,7 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
             tc_fence_after();
             if (RES && pieces && !warp_wait_all(&b.residual[w], (uint32_t)(fetched++) & 1u, &b.ctl, a.status, 164)) break;
 #pragma unroll 1
-            for (int i = 0; i < 2; i++) {
+            for (int i = 0; i <= last; i++) {
                 unsigned char *tile = RES ? mine + i * kPiece : mine;
 #pragma unroll 1
                 for (int pass = 0; pass <= a.e.has_z; pass++) {
@@ -415,7 +433,7 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
                         float v[32];
                         tmem_ld32(tmem + acc * 256 + c0 + 64 * i + 32 * ch + ((uint32_t)(32 * quad) << 16), v);
                         tmem_ld_wait();
-                        if (i == 1 && ch == 1 && pass == a.e.has_z) {
+                        if (i == last && ch == 1 && pass == a.e.has_z) {
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0) arrive_remote(empty0 + 8u * acc);
@@ -836,20 +854,30 @@ bool encode(CUtensorMap *m, const Operand &o, bool e4m3, int tile_rows) {
 
 int64_t up(int64_t x, int64_t d) { return (x + d - 1) / d; }
 
+// The last round's tiles are halved where that fits the pairs: a half's block
+// of r takes 430 cycles (what its operands take to come) instead of 590, and
+// half the epilogue (4096 x 4096 x 4096: 102 -> 93 us, e4m3 48 -> 44;
+// 256 x 2048 x 6144: 16.2 -> 13.5, with GELU and a residual 21.1 -> 16.4).
+int64_t whole_tiles(int64_t tiles, int pairs) {
+    const int64_t rem = tiles % pairs;
+    return 2 * rem <= pairs ? tiles - rem : tiles;
+}
+
 template <bool E4M3, bool A_MN, bool B_MN, bool RES = false>
 int wide(const Operand &A, const Operand &B, Args a, void *y, void *z, int sms, cudaStream_t st) {
-    CUtensorMap ma, mb, my, mz, mr;
-    if (!encode(&ma, A, E4M3, 128) || !encode(&mb, B, E4M3, 128) || !encode(&my, y, false, a.P, a.Q, 64, 32) ||
+    CUtensorMap ma, mb, mbh, my, mz, mr;
+    if (!encode(&ma, A, E4M3, 128) || !encode(&mb, B, E4M3, 128) || !encode(&mbh, B, E4M3, 64) || !encode(&my, y, false, a.P, a.Q, 64, 32) ||
         !encode(&mz, z ? z : y, false, a.P, a.Q, 64, 32) ||
         !encode(&mr, a.e.residual ? a.e.residual : y, false, a.P, a.Q, 64, 32))
         return (int)cudaErrorInvalidValue;
     a.tiles_p = (int)up(a.P, kTile);
     a.tiles_q = (int)up(a.Q, kTile);
     const int64_t tiles = (int64_t)a.tiles_p * a.tiles_q;
-    if (tiles > (int64_t)0x3fffffff) return (int)cudaErrorInvalidValue;
-    const int pairs = (int)std::min<int64_t>(tiles, sms / 2);
+    if (tiles > (int64_t)0x1fffffff) return (int)cudaErrorInvalidValue;
+    a.whole = (int)whole_tiles(tiles, sms / 2);
+    const int pairs = (int)std::min<int64_t>(2 * tiles - a.whole, sms / 2);
     return launch_early(wide_kernel<E4M3, A_MN, B_MN, RES>, dim3(2 * pairs), kWideThreads, kWideBytes<RES>, 2, st, ma, mb, my, mz,
-                        mr, a);
+                        mr, mbh, a);
 }
 
 template <int QN, bool E4M3, bool A_MN>
@@ -861,8 +889,8 @@ int narrow(const Operand &W, const Operand &X, Args a, int split, cudaStream_t s
 }
 
 // Which kernel runs a product whose rows p are rows of x, by an estimate of
-// its cycles from measured parts (64 x 2048 x 6144: 10.4 us narrow, 16 wide;
-// 256 x 2048 x 6144: 38 us narrow with 128 rows of x a tile, 16 wide).
+// its cycles from measured parts (64 x 2048 x 6144: 10.4 us narrow, 12.4 wide;
+// 256 x 2048 x 6144: 38 us narrow with 128 rows of x a tile, 13.4 wide).
 struct Choice {
     int qn = 0, split = 1;   // qn 0: wide_kernel
 };
@@ -870,20 +898,22 @@ Choice choose(int64_t P, int64_t Q, int blocks, int sms) {
     Choice best;
     // tiles one after the other: 590 cycles for a block (512 are the products'),
     // 7000 for an epilogue that goes on meanwhile; the first load and the last
-    // epilogue alone
-    double cost = (double)up(up(P, kTile) * up(Q, kTile), sms / 2) * std::max(blocks * 590.0, 7000.0) + 10500.0;
+    // epilogue alone.  A round of halves: see whole_tiles.
+    const int64_t wide_tiles = up(P, kTile) * up(Q, kTile), whole = whole_tiles(wide_tiles, sms / 2);
+    double cost = (double)up(whole, sms / 2) * std::max(blocks * 590.0, 7000.0);
+    cost += whole < wide_tiles ? std::max(blocks * 430.0, 3500.0) + 12000.0 : 10500.0;
     for (int qn = 16; qn <= 128; qn *= 2) {
         if (up(Q, 128) > 65535 || up(P, qn) > 65535) continue;
         const int64_t tiles = up(P, qn) * up(Q, 128);
         const int fit = qn <= 32 ? 2 : 1;
-        const double block = std::max(2.0 * qn, (128 + qn) * kRBytes / 30.0);   // what an SM fetches in a cycle
+        const double block = std::max(2.0 * qn, (128 + qn) * kRBytes / 45.0);   // what an SM fetches in a cycle
         for (int split = 1; split <= kMaxSplit && split <= blocks; split++) {
             // a cluster of more than two finds no place on some of the last SMs
             const int64_t room = (int64_t)sms * fit * (split > 2 ? 15 : 16) / 16;
             const int64_t waves = up(tiles * split, room);
             const double together = waves > 1 ? fit : (double)up(tiles * split, sms);
             // a column's epilogue, or its partial sums to send and to add
-            const double columns = split > 1 ? 1500.0 + 40.0 * qn : 100.0 * qn;
+            const double columns = split > 1 ? 1500.0 + 20.0 * qn * split : 200.0 * qn;
             const double c = waves * (up(blocks, split) * block * together + 7000.0 + columns);
             if (c < cost) {
                 cost = c;

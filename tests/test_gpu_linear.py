@@ -100,6 +100,20 @@ def test_long_reduction_and_many_tiles(ctx):
     forward(ctx, 5000, 1096, 2056, act=None)
 
 
+# 90 tiles, the last 14 in halves, one of them with 8 columns; and 24 tiles all in halves
+@pytest.mark.parametrize("M,K,N", [(2500, 80, 2184), (900, 336, 1288)])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_whole_and_halved_tiles(ctx, M, K, N, residual, e4m3):
+    forward(ctx, M, K, N, act="silu", residual=residual, z=True, e4m3=e4m3)
+    forward(ctx, M, K, N, act="gelu", residual=residual, e4m3=e4m3)
+
+
+@pytest.mark.parametrize("M,K,N", [(2500, 2184, 72), (136, 2184, 2504), (900, 1288, 72), (136, 1288, 904)])
+def test_gradients_of_whole_and_halved_tiles(ctx, M, K, N):
+    backward(ctx, M, K, N, None)
+
+
 def test_leading_dimensions_are_rows(ctx):
     d = {k: v.cuda() for k, v in draw(24, 64, 72).items()}
     y, y3 = torch.empty(24, 72, device="cuda").bfloat16(), torch.empty(2, 12, 72, device="cuda").bfloat16()
