@@ -528,6 +528,13 @@ struct NarrowBars {
 template <int QN>
 constexpr size_t kNarrowBytes = (size_t)kNarrowStages<QN> * kNarrowStage<QN> + kNarrowSums<QN> + sizeof(NarrowBars) + 1024;
 static_assert(kNarrowStages<16> <= 8 && kNarrowStages<64> <= 8 && kNarrowStages<128> >= 3, "stages and their barriers");
+// A kernel that started early waits for the one before it with its TMEM
+// allocated, and must not hold what a block of that one still asks for: a wide
+// block (all 512 columns) never shares its SM with another, and two narrow
+// ones together take 256 columns at most.
+static_assert(kWideBytes<true> + kNarrowBytes<16> > 228 * 1024 && kWideBytes<false> + kNarrowBytes<16> > 228 * 1024 &&
+                  kWideBytes<true> + kNarrowBytes<32> > 228 * 1024 && kWideBytes<false> + kNarrowBytes<32> > 228 * 1024,
+              "no block is left without its TMEM columns");
 
 // The sum of a group of 4 columns over the CTAs of a cluster, in their order.
 template <int SPLIT>
