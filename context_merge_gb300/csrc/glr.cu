@@ -532,8 +532,8 @@ __global__ void __launch_bounds__(32 * WARPS, 1) glr_bwd_kernel(Params p, int nz
 // them all, the others leave.
 template <typename T>
 __global__ void __launch_bounds__(kStepThreads)
-glr_step_kernel(const T *__restrict__ x, const float *__restrict__ g, const float *state, float *state_out,
-                const int32_t *__restrict__ slots, int n, int num_slots, int channels, T *y) {
+glr_step_kernel(const T *x, const float *g, const float *state, float *state_out,
+                const int32_t *slots, int n, int num_slots, int channels, T *y) {
     next_grid_may_start();
     previous_grid_done();
     const int row = blockIdx.y;

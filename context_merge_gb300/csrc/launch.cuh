@@ -5,8 +5,10 @@
 // up meanwhile: barriers, TMEM, tensor maps.  It must call
 // previous_grid_done() in every thread before that thread reads or writes
 // global memory: the call returns when the kernels before it have ended and
-// what they wrote can be seen.  Measured: a chain of 16 x 2048 x 6144 products
-// 9.3 -> 7.5 us each.
+// what they wrote can be seen.  Its parameters are not __restrict__ and it uses
+// no read-only loads: those are for memory that nothing writes while the kernel
+// is resident, and neither the wait nor its clobber orders them.  Measured: a
+// chain of 16 x 2048 x 6144 products 9.3 -> 7.5 us each.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -765,8 +765,8 @@ narrow_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
 // thread 8 columns of every 8th row, four rows' loads at a time.
 template <int ACT>
 __global__ void __launch_bounds__(256)
-dz_kernel(const __nv_bfloat16 *__restrict__ dy, const __nv_bfloat16 *__restrict__ z, int64_t rows, int width, int per,
-          __nv_bfloat16 *__restrict__ dz, float *__restrict__ part) {
+dz_kernel(const __nv_bfloat16 *dy, const __nv_bfloat16 *z, int64_t rows, int width, int per,
+          __nv_bfloat16 *dz, float *part) {
     constexpr int AHEAD = 4;
     __shared__ float sh[8][256];
     next_grid_may_start();

@@ -332,7 +332,7 @@ constexpr int kSumCols = 32, kSumRows = 16;
 // out[col] = sum of part[:, col], in a fixed order: 16 strided sums per
 // column, then those 16.
 __global__ void __launch_bounds__(kSumCols *kSumRows)
-column_sums_kernel(const float *__restrict__ part, int nparts, int width, float *__restrict__ out) {
+column_sums_kernel(const float *part, int nparts, int width, float *out) {
     __shared__ float sh[kSumRows][kSumCols + 1];
     next_grid_may_start();
     previous_grid_done();
