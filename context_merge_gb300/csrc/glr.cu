@@ -79,46 +79,53 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
+// exp(g) for |g| <= 1/4: 1 + g + g^2 q(g), q of degree 3 interpolated at
+// Chebyshev points (off by 0.7 half steps at 1/4, by 0.1 up to 1/10), rounded
+// once: five instructions for two channels.
+__device__ __forceinline__ float2 exp_near_zero(float2 g) {
+    constexpr float kC[4] = {0.49999931454658508f, 0.16666656732559204f, 0.041753556579351425f, 0.0083457436412572861f};
+    float2 r = fma2(g, both(kC[3]), both(kC[2]));
+    r = fma2(g, r, both(kC[1]));
+    r = fma2(g, r, both(kC[0]));
+    r = fma2(g, r, both(1.f));
+    return fma2(g, r, both(1.f));
+}
+// exp(g) elsewhere: 2^t (1 + e ln 2) with t = g log2(e) rounded, log2(e) in
+// two parts, and e what t misses; the fast power of two is off by up to two
+// units in the last place.  Gates from -87.4 down give 0; a NaN stays one.
+__device__ __forceinline__ float2 exp_far(float2 g) {
+    constexpr float kL = 1.44269504088896341f, kLow = 1.92596299e-8f, kLn2 = 0.693147180559945309f;
+    // -infinity would meet itself in e; 2^-185 is flushed to zero
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(g.x) : "f"(-128.f));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(g.y) : "f"(-128.f));
+    const float2 t = mul2(g, both(kL));
+    const float2 e = fma2(g, both(-kLow), fma2(g, both(-kL), t));   // minus what is missing
+    float2 r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(t.y));
+    return fma2(mul2(r, both(-kLn2)), e, r);
+}
 // a = exp(g) for a group's gates, in place.
 // Gates next to 0 make a long memory, which adds the errors of many steps up:
-// they need an a that leans to no side.  Where every channel's squares sum to
-// at most 1/16 over the group (so |g| <= 1/4), a = 1 + g + g^2 q(g), q of
-// degree 3 interpolated at Chebyshev points (off by 0.7 half steps of a at
-// 1/4, by 0.1 up to 1/10), rounded once: six instructions for two channels.
-// Elsewhere the state forgets in a few steps, and the fast power of two does
-// (off by up to 3 half steps, leaning by 0.4: alone, it cost the states of a
-// long memory 1e-6): a = 2^t (1 + e ln 2) with t = g log2(e) rounded and e what
-// the fused product finds missing.  Gates from -87.4 down give 0; a NaN stays
-// one.  (One polynomial with a reduction for all gates: 18 instructions, the
-// forward at 262144 x 2048 in 0.79 instead of 0.68 ms.)
+// they need an a that leans to no side (the fast power leans by 0.4 half steps:
+// alone, it cost the states of a long memory 1e-6).  Each token's gate decides
+// for itself, so that a channel's bits do not depend on the channels beside it;
+// where every channel's squares sum to at most 1/16 over the group (so that all
+// |g| <= 1/4) the other form is left out: 131072 x 2048 bf16 forward 339 us, with
+// both forms 418 (the far one alone 343), backward 635 and 699.
 __device__ __forceinline__ void exp_of_gates(float2 (&g)[kGlrGroup]) {
     float2 sq[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
 #pragma unroll
     for (int u = 0; u < kGlrGroup; u++) sq[u & 3] = fma2(g[u], g[u], sq[u & 3]);
     const float2 sum = add2(add2(sq[0], sq[1]), add2(sq[2], sq[3]));
     if (__all_sync(0xffffffffu, sum.x <= 0.0625f && sum.y <= 0.0625f)) {
-        constexpr float kC[4] = {0.49999931454658508f, 0.16666656732559204f, 0.041753556579351425f, 0.0083457436412572861f};
 #pragma unroll
-        for (int u = 0; u < kGlrGroup; u++) {
-            float2 r = fma2(g[u], both(kC[3]), both(kC[2]));
-            r = fma2(g[u], r, both(kC[1]));
-            r = fma2(g[u], r, both(kC[0]));
-            r = fma2(g[u], r, both(1.f));
-            g[u] = fma2(g[u], r, both(1.f));
-        }
+        for (int u = 0; u < kGlrGroup; u++) g[u] = exp_near_zero(g[u]);
     } else {
-        constexpr float kL = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 #pragma unroll
         for (int u = 0; u < kGlrGroup; u++) {
-            // -infinity would meet itself in e; 2^-185 is flushed to zero
-            asm("max.NaN.f32 %0, %0, %1;" : "+f"(g[u].x) : "f"(-128.f));
-            asm("max.NaN.f32 %0, %0, %1;" : "+f"(g[u].y) : "f"(-128.f));
-            const float2 t = mul2(g[u], both(kL));
-            const float2 e = fma2(g[u], both(-kL), t);   // minus what is missing
-            float2 r;
-            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(t.x));
-            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(t.y));
-            g[u] = fma2(mul2(r, both(-kLn2)), e, r);
+            const float2 near = exp_near_zero(g[u]), far = exp_far(g[u]);
+            g[u] = make_float2(fabsf(g[u].x) <= 0.25f ? near.x : far.x, fabsf(g[u].y) <= 0.25f ? near.y : far.y);
         }
     }
 }
