@@ -111,9 +111,16 @@ __device__ __forceinline__ float2 exp_far(float2 g) {
 // alone, it cost the states of a long memory 1e-6).  Each token's gate decides
 // for itself, so that a channel's bits do not depend on the channels beside it;
 // where every channel's squares sum to at most 1/16 over the group (so that all
-// |g| <= 1/4) the other form is left out: 131072 x 2048 bf16 forward 339 us, with
-// both forms 418 (the far one alone 343), backward 635 and 699.
-__device__ __forceinline__ void exp_of_gates(float2 (&g)[kGlrGroup]) {
+// |g| <= 1/4) the other form is left out: 131072 x 2048 bf16 forward 341 us, with
+// both forms 429; backward 599 and 683.  (A third form for warps whose channels
+// all forget at once, the far one alone: 395 and 614 there, but 466 where
+// slow and fast channels lie side by side.)
+// Returns what the group's map starts from, for each channel: 1, or a NaN where
+// positive gates sum to more than 1, so that the map must not be composed
+// (Exchange).  Squares of at most 1/16 keep the sum of 16 gates below 1, and a
+// group of negative gates has none.
+__device__ __forceinline__ float2 exp_of_gates(float2 (&g)[kGlrGroup]) {
+    float2 one = both(1.f);
     float2 sq[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
 #pragma unroll
     for (int u = 0; u < kGlrGroup; u++) sq[u & 3] = fma2(g[u], g[u], sq[u & 3]);
@@ -122,12 +129,23 @@ __device__ __forceinline__ void exp_of_gates(float2 (&g)[kGlrGroup]) {
 #pragma unroll
         for (int u = 0; u < kGlrGroup; u++) g[u] = exp_near_zero(g[u]);
     } else {
+        uint32_t signs = ~0u;
+#pragma unroll
+        for (int u = 0; u < kGlrGroup; u++) signs &= __float_as_uint(g[u].x) & __float_as_uint(g[u].y);
+        if (__any_sync(0xffffffffu, (int32_t)signs >= 0)) {
+            float2 growth = both(0.f);
+#pragma unroll
+            for (int u = 0; u < kGlrGroup; u++) growth = add2(growth, make_float2(fmaxf(g[u].x, 0.f), fmaxf(g[u].y, 0.f)));
+            if (growth.x > 1.f) one.x = __int_as_float(0x7fffffff);
+            if (growth.y > 1.f) one.y = __int_as_float(0x7fffffff);
+        }
 #pragma unroll
         for (int u = 0; u < kGlrGroup; u++) {
             const float2 near = exp_near_zero(g[u]), far = exp_far(g[u]);
             g[u] = make_float2(fabsf(g[u].x) <= 0.25f ? near.x : far.x, fabsf(g[u].y) <= 0.25f ? near.y : far.y);
         }
     }
+    return one;
 }
 
 // A pair of maps h -> A h + B.
@@ -147,6 +165,16 @@ __device__ __forceinline__ void send(const Map *place, uint64_t *bar, uint32_t r
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rb) : "r"(tc::smem_u32(bar)), "r"(rank));
     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(ra),
                  "f"(v.A.x), "f"(v.A.y), "f"(v.B.x), "f"(v.B.y), "r"(rb)
+                 : "memory");
+}
+
+// The same for a pair of states.
+__device__ __forceinline__ void send(const float2 *place, uint64_t *bar, uint32_t rank, float2 h) {
+    uint32_t ra, rb;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(tc::smem_u32(place)), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rb) : "r"(tc::smem_u32(bar)), "r"(rank));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(ra), "f"(h.x),
+                 "f"(h.y), "r"(rb)
                  : "memory");
 }
 
@@ -188,9 +216,11 @@ __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A warp's group of one tensor: kGlrGroup rows of the slice, in shared memory.
+// A warp's group of one tensor: kGlrGroup rows of the slice, in shared memory,
+// whole lines of it (131072 x 2048 bf16 forward 346 us; tiles that begin 32
+// bytes into a line 364, 16 bytes 422).
 template <typename T>
-struct Tile {
+struct alignas(128) Tile {
     T v[kGlrGroup][kSlice];
     // Starts the copies of the group's n rows; what lies behind the rows or
     // the channels becomes zero.
@@ -219,21 +249,42 @@ struct Tile {
 
 // The maps of one cluster step.  REV: groups and CTAs follow one another from
 // the last to the first.
+//
+// Maps compose safely where A stays in fp32's range.  Positive gates can take
+// it out of range although the states are finite (zero or small states, a reset
+// behind the growth), and infinity times zero would be NaN.  A group whose
+// positive gates sum to at most 1 multiplies by at most e, a step's 64 groups by
+// e^64: nothing overflows, and what an A too small for fp32 loses is at most
+// 2^-149 e^64 = 1e-17 of the state before the step.  Any other group's map starts
+// from a NaN (exp_of_gates), which stays through every composition; a step
+// that meets one runs token by token for its channels, the groups one behind
+// the other.  The other channels keep what the maps gave them, to the last bit.
 template <int WARPS, bool REV>
-struct Exchange {
+struct alignas(16) Exchange {
     Map grp[2][WARPS][32];          // each group's, for every channel pair, by parity of the step
     Map cta[2][kMaxCluster][32];    // each CTA's of the cluster
     uint64_t bar[2];                // the CTAs' maps of a step have arrived, by parity
+    // a step token by token: the states behind each warp's group, before this
+    // CTA's groups and behind the step, and the barriers that they are there
+    float2 behind[WARPS][32], enter[32], leave[32];
+    uint64_t done[WARPS], entered, left;
 
     tc::Ctl ctl;
 
     // The whole cluster calls it before the first step ...
     __device__ __forceinline__ void open(uint32_t nz) {
-        if (nz == 1) return;
         if (threadIdx.x == 0) {
             ctl.abort = 0;
             tc::mbar_init(&bar[0], 1);
             tc::mbar_init(&bar[1], 1);
+#pragma unroll
+            for (int i = 0; i < WARPS; i++) tc::mbar_init(&done[i], 1);
+            tc::mbar_init(&entered, 1);
+            tc::mbar_init(&left, 1);
+        }
+        if (nz == 1) {
+            __syncthreads();
+            return;
         }
         cluster_arrive();
         cluster_wait();
@@ -271,23 +322,80 @@ struct Exchange {
     }
     // Second half: the value before this warp's group, from the value `carry`
     // before the step, which becomes the value behind it.  `phase`: how often
-    // this parity's barrier has completed, modulo 2.
-    __device__ __forceinline__ float2 start(int par, uint32_t phase, int lane, uint32_t rank, uint32_t nz,
-                                            const Map &before, const Map &all, float2 &carry, int32_t *status) {
-        float2 s = carry;
+    // this parity's barrier has completed, modulo 2.  `group` takes a value
+    // through this warp's group; `turns`: the steps that ran token by token.
+    template <typename F>
+    __device__ __forceinline__ float2 start(int par, uint32_t phase, int w, int lane, uint32_t rank, uint32_t nz,
+                                            const Map &before, const Map &all, float2 &carry, int32_t *status,
+                                            uint32_t &turns, F group) {
+        float2 s = carry, v = carry;
         if (nz > 1) {
             tc::mbar_wait(&bar[par], phase, &ctl, status, REV ? 151 : 150);
-            float2 v = carry;
             for (uint32_t i = 0; i < nz; i++) {
                 const uint32_t z = REV ? nz - 1 - i : i;
                 if (z == rank) s = v;
                 v = apply(cta[par][z][lane], v);
             }
-            carry = v;
         } else {
-            carry = apply(all, carry);
+            v = apply(all, carry);
         }
-        return apply(before, s);
+        s = apply(before, s);
+        // a NaN: of a map that must not be composed, or (nothing is lost then but
+        // time) of the state itself.  The whole cluster goes this way or that as one.
+        const bool x = v.x != v.x, y = v.y != v.y;
+        if (__any_sync(0xffffffffu, x || y)) {
+            float2 end;
+            const float2 h = in_turn(w, lane, rank, nz, carry, end, status, turns++ & 1u, group);
+            s = make_float2(x ? h.x : s.x, y ? h.y : s.y);
+            v = make_float2(x ? end.x : v.x, y ? end.y : v.y);
+        }
+        carry = v;
+        return s;
+    }
+    // The groups of a step one behind the other: the state goes from warp to warp
+    // through shared memory, from CTA to CTA and at last to all of them by remote
+    // stores.  Every barrier here completes once in such a step, and none is used
+    // again before the whole cluster has published the next step's maps, which
+    // each warp does behind its last wait here.
+    template <typename F>
+    __device__ __forceinline__ float2 in_turn(int w, int lane, uint32_t rank, uint32_t nz, float2 before_step, float2 &end,
+                                              int32_t *status, uint32_t phase, F group) {
+        constexpr uint32_t kBytes = 32 * sizeof(float2);
+        const int site = REV ? 153 : 152;
+        end = before_step;
+        if (ctl.abort) return before_step;   // nothing is counted after a wait that gave up
+        const uint32_t c = REV ? nz - 1 - rank : rank;         // this CTA's place in the order,
+        const int i = REV ? WARPS - 1 - w : w;                 // and this warp's
+        if (threadIdx.x == 0 && nz > 1) {
+            if (c > 0) tc::mbar_arrive_expect_tx(&entered, kBytes);
+            tc::mbar_arrive_expect_tx(&left, kBytes);
+        }
+        float2 h = before_step;
+        if (i > 0) {
+            tc::mbar_wait(&done[i - 1], phase, &ctl, status, site);
+            h = behind[i - 1][lane];
+        } else if (c > 0) {
+            tc::mbar_wait(&entered, phase, &ctl, status, site);
+            h = enter[lane];
+        }
+        const float2 first = h;
+        h = group(h);
+        if (i + 1 < WARPS) {
+            behind[i][lane] = h;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&done[i]);
+        } else if (c + 1 < nz) {
+            send(&enter[lane], &entered, REV ? rank - 1 : rank + 1, h);
+        } else if (nz > 1) {
+            for (uint32_t z = 0; z < nz; z++) send(&leave[lane], &left, z, h);
+        } else {
+            leave[lane] = h;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&left);
+        }
+        tc::mbar_wait(&left, phase, &ctl, status, site);
+        end = leave[lane];
+        return first;
     }
 };
 
@@ -312,7 +420,7 @@ struct BwdShared {
 template <typename S>
 constexpr int kPerSm = (228 * 1024) / ((int)sizeof(S) + 1024);
 
-extern __shared__ __align__(16) unsigned char smem[];
+extern __shared__ __align__(128) unsigned char smem[];
 
 // The loop of both directions, over cluster steps i: the maps of step i + 1
 // are taken and published, then step i's tokens run from their start and go
@@ -367,14 +475,23 @@ __global__ void __launch_bounds__(32 * WARPS, 2) glr_fwd_kernel(Params p, int nz
         }
         __syncwarp();
         fetch(at + 2 * step, stage);
-        exp_of_gates(v.a);   // behind the tokens g = 0: the state stays
-        Map m{both(1.f), both(0.f)};
+        Map m{exp_of_gates(v.a), both(0.f)};   // behind the tokens g = 0: the state stays
 #pragma unroll
         for (int u = 0; u < kGlrGroup; u++) m = after(Map{v.a[u], widen(v.x[u])}, m);
         sh.ex.publish(stage, w, lane, rank, (uint32_t)nz, m, before, all);
     };
     const int64_t steps = (sp.len + step - 1) / step;
     float2 h = both(0.f);
+    uint32_t turns = 0;
+    // The state before step i's group, from its maps; all that it needs of the group else.
+    auto start = [&](const Group &v, int64_t i, int parity) {
+        return sh.ex.start(parity, (uint32_t)(i >> 1) & 1u, w, lane, rank, (uint32_t)nz, before, all, carry, p.status, turns,
+                           [&](float2 s) {
+#pragma unroll
+                               for (int u = 0; u < kGlrGroup; u++) s = fma2(v.a[u], s, widen(v.x[u]));
+                               return s;
+                           });
+    };
     // One step: the next one's maps, this one's outputs, the next one's starts.
     auto turn = [&](const Group &v, Group &next, int64_t i, int parity) {
         if (i + 1 < steps) take(next, p0 + step, parity ^ 1);
@@ -393,8 +510,7 @@ __global__ void __launch_bounds__(32 * WARPS, 2) glr_fwd_kernel(Params p, int nz
         };
         if (!ZIGZAG && n == kGlrGroup) run(std::true_type());
         else run(std::false_type());
-        if (i + 1 < steps)
-            h = sh.ex.start(parity ^ 1, (uint32_t)((i + 1) >> 1) & 1u, lane, rank, (uint32_t)nz, before, all, carry, p.status);
+        if (i + 1 < steps) h = start(next, i + 1, parity ^ 1);
         p0 += step;
     };
     sh.ex.open((uint32_t)nz);
@@ -403,7 +519,7 @@ __global__ void __launch_bounds__(32 * WARPS, 2) glr_fwd_kernel(Params p, int nz
         fetch(p0, 0);
         fetch(p0 + step, 1);
         take(even, p0, 0);
-        h = sh.ex.start(0, 0, lane, rank, (uint32_t)nz, before, all, carry, p.status);
+        h = start(even, 0, 0);
         for (int64_t i = 0; i < steps; i += 2) {
             turn(even, odd, i, 0);
             if (i + 1 < steps) turn(odd, even, i + 1, 1);
@@ -464,7 +580,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) glr_bwd_kernel(Params p, int nz
             g[u] = *reinterpret_cast<const float2 *>(&r.g.v[u][2 * lane]);
             dy[u] = load2(&r.dy.v[u][2 * lane]);
         }
-        exp_of_gates(g);
+        m.A = exp_of_gates(g);
 #pragma unroll
         for (int u = kGlrGroup - 1; u >= 0; u--) {
             *reinterpret_cast<float2 *>(&r.g.v[u][2 * lane]) = g[u];
@@ -473,6 +589,18 @@ __global__ void __launch_bounds__(32 * WARPS, 1) glr_bwd_kernel(Params p, int nz
         sh.ex.publish(par, w, lane, rank, (uint32_t)nz, m, before, all);
     };
     float2 q = make_float2(0.f, 0.f), h = q, h_next = q;
+    uint32_t turns = 0;
+    // q behind step i's group, from its maps (the group lies in `stage`)
+    auto start = [&](int64_t i, int stage, int par) {
+        return sh.ex.start(par, (uint32_t)(i >> 1) & 1u, w, lane, rank, (uint32_t)nz, before, all, carry, p.status, turns,
+                           [&](float2 s) {
+                               const auto &r = sh.ring[w][stage];
+                               for (int u = kGlrGroup - 1; u >= 0; u--)
+                                   s = mul2(*reinterpret_cast<const float2 *>(&r.g.v[u][2 * lane]),
+                                            add2(widen(load2(&r.dy.v[u][2 * lane])), s));
+                               return s;
+                           });
+    };
     sh.ex.open((uint32_t)nz);
     if (steps > 0) {
 #pragma unroll
@@ -481,7 +609,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) glr_bwd_kernel(Params p, int nz
         cp_wait<kStages - 1>();
         __syncwarp();
         map(0, 0);
-        q = sh.ex.start(0, 0, lane, rank, (uint32_t)nz, before, all, carry, p.status);
+        q = start(0, 0, 0);
     }
     int stage = 0, par = 0;
     for (int64_t i = 0; i < steps; i++, p0 -= step) {
@@ -525,8 +653,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) glr_bwd_kernel(Params p, int nz
         stage = next;
         par ^= 1;
         h = h_next;
-        if (i + 1 < steps)
-            q = sh.ex.start(par, (uint32_t)((i + 1) >> 1) & 1u, lane, rank, (uint32_t)nz, before, all, carry, p.status);
+        if (i + 1 < steps) q = start(i + 1, stage, par);
     }
     cp_wait<0>();
     sh.ex.close((uint32_t)nz);

@@ -327,9 +327,13 @@ cpdr_status cpdr_bwd(const cpdr_ctx *ctx, const void *q, const void *k, const vo
  *     h_t = a_t h_{t-1} + x_t,    y_t = h_t,
  * from h0 (or zero) at the sequence's start; hT is the state behind its last
  * token (h0, or zero, for an empty sequence).  gate is a natural-log gate, at
- * most 88; -infinity is one (a_t = 0: the state is dropped).  x and h0 are
- * finite.  Sequences and token layout are the context's (packed batches,
- * zigzag); its segments play no part.
+ * most 88; -infinity is one (a_t = 0: the state is dropped); from -87.4 down
+ * a_t is 0.  x and h0 are finite, and so is the state that the same x would
+ * give from zero at any token.  Positive gates that sum to more than 1 over 16
+ * tokens (or a NaN) cost time: up to 1024 tokens around them run one 16 behind
+ * the other.  What falls below 1e-17 of the largest state of the last 1024
+ * tokens counts as zero.  Sequences and token layout are the context's (packed
+ * batches, zigzag); its segments play no part.
  * Layout: x, y [B, T, channels] in the context's token order and input dtype;
  * gate [B, T, channels] fp32; h0, hT [N, channels] fp32, either may be NULL
  * (hT may be h0 itself); channels % 8 == 0, at most 2^24.
