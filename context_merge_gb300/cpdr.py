@@ -31,7 +31,7 @@ EXPORTED = ["cpdr_ctx_create", "cpdr_ctx_destroy", "cpdr_buffer_sizes", "cpdr_pl
             "cpdr_merge", "cpdr_fwd", "cpdr_host_workspace_bytes",
             "cpdr_forward_host", "cpdr_forward_noalloc", "cpdr_check_device_status", "cpdr_selftest_wait_timeout",
             "cpdr_conv1d_fwd", "cpdr_plan_conv_tokens", "cpdr_bwd_workspace_bytes", "cpdr_bwd",
-            "cpdr_glr_carry_bytes", "cpdr_glr_fwd", "cpdr_glr_bwd", "cpdr_glr_step", "cpdr_rmsnorm_fwd",
+            "cpdr_glr_carry_bytes", "cpdr_plan_glr", "cpdr_glr_fwd", "cpdr_glr_bwd", "cpdr_glr_step", "cpdr_rmsnorm_fwd",
             "cpdr_rmsnorm_bwd_workspace_bytes", "cpdr_rmsnorm_bwd", "cpdr_linear_fwd",
             "cpdr_linear_bwd_workspace_bytes", "cpdr_linear_bwd", "cpdr_last_error", "cpdr_version"]
 
@@ -95,6 +95,7 @@ def load():
         lib.cpdr_forward_noalloc.argtypes = [vp] * 9
         i32, i64, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
         lib.cpdr_glr_carry_bytes.argtypes = [vp, i32, ctypes.POINTER(sz)]
+        lib.cpdr_plan_glr.argtypes = [vp, i32, i32, ctypes.POINTER(i32)]
         lib.cpdr_glr_fwd.argtypes = [vp] * 4 + [i32] + [vp] * 4
         lib.cpdr_glr_bwd.argtypes = [vp] * 6 + [i32] + [vp] * 4
         lib.cpdr_glr_step.argtypes = [vp] * 6 + [i32] * 3 + [vp] * 2
@@ -402,6 +403,13 @@ class Context:
         n = ctypes.c_size_t()
         _check(self._lib.cpdr_glr_carry_bytes(self._h, int(channels), ctypes.byref(n)))
         return (n.value // (4 * int(channels)), int(channels))
+
+    def glr_plan(self, channels, backward=False):
+        """How the recurrence runs with that many channels: CTAs of a cluster,
+        CTAs of an SM that the choice counts on, and those that the device holds."""
+        out = (ctypes.c_int32 * 3)()
+        _check(self._lib.cpdr_plan_glr(self._h, int(channels), int(backward), out))
+        return dict(zip(("cluster", "per_sm", "resident"), out))
 
     def _glr_shapes(self, x):
         if x.dim() != 3 or tuple(x.shape[:2]) != (self.B, self.T):

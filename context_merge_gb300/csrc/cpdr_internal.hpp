@@ -255,6 +255,7 @@ int launch_glr_bwd(const cpdr_ctx *c, const void *x, const float *g, const float
                    const float *dhT, int channels, void *dx, float *dg, float *dh0, void *stream);
 int launch_glr_step(const cpdr_ctx *c, const void *x, const float *g, const float *state, float *state_out,
                     const int32_t *slots, int n, int num_slots, int channels, void *y, void *stream);
+int glr_plan(const cpdr_ctx *c, int channels, bool backward, int32_t out[3]);
 // out[col] = sum over parts of part[:, col] (rmsnorm.cu).
 int launch_column_sums(const float *part, int nparts, int width, float *out, void *stream);
 // Matrix product with its epilogue (linear.cu).  dz: rows x N bf16 (where

@@ -416,9 +416,11 @@ struct BwdShared {
     } ring[WARPS][kStages];
 };
 
-// CTAs of an SM, by shared memory (1 KiB of it is the system's for each).
-template <typename S>
-constexpr int kPerSm = (228 * 1024) / ((int)sizeof(S) + 1024);
+// CTAs of an SM: what the kernels' registers are bounded for, where shared memory
+// holds as many (1 KiB of it is the system's for each).
+constexpr int kFwdPerSm = 2, kBwdPerSm = 1;
+template <typename S, int BOUND>
+constexpr int kPerSm = (228 * 1024) / ((int)sizeof(S) + 1024) < BOUND ? (228 * 1024) / ((int)sizeof(S) + 1024) : BOUND;
 
 extern __shared__ __align__(128) unsigned char smem[];
 
@@ -433,7 +435,7 @@ extern __shared__ __align__(128) unsigned char smem[];
 //
 // grid: (span, channel slice) items x cluster CTAs; cluster (nz, 1, 1)
 template <typename T, int WARPS, bool ZIGZAG>
-__global__ void __launch_bounds__(32 * WARPS, 2) glr_fwd_kernel(Params p, int nz) {
+__global__ void __launch_bounds__(32 * WARPS, kFwdPerSm) glr_fwd_kernel(Params p, int nz) {
     auto &sh = *reinterpret_cast<FwdShared<T, WARPS> *>(smem);
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = nz > 1 ? cluster_rank() : 0u;
@@ -532,7 +534,7 @@ __global__ void __launch_bounds__(32 * WARPS, 2) glr_fwd_kernel(Params p, int nz
 }
 
 template <typename T, int WARPS, bool ZIGZAG>
-__global__ void __launch_bounds__(32 * WARPS, 1) glr_bwd_kernel(Params p, int nz) {
+__global__ void __launch_bounds__(32 * WARPS, kBwdPerSm) glr_bwd_kernel(Params p, int nz) {
     auto &sh = *reinterpret_cast<BwdShared<T, WARPS> *>(smem);
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = nz > 1 ? cluster_rank() : 0u;
@@ -729,8 +731,33 @@ int pick_cluster(const cpdr_ctx *c, int slices, int tile, int per_sm) {
     return best;
 }
 
-template <typename K>
-int launch(const cpdr_ctx *c, K kernel, int warps, int per_sm, size_t bytes, Params p, void *stream) {
+// How a direction runs: its kernel, warps and shared memory of a CTA, and the
+// CTAs of an SM that the cluster size is chosen for.
+struct Form {
+    void (*kernel)(Params, int);
+    int warps, per_sm;
+    size_t bytes;
+};
+template <typename T>
+Form fwd(const cpdr_ctx *c) {
+    constexpr int W = kFwdWarps;
+    using S = FwdShared<T, W>;
+    return Form{c->plan.flags & CPDR_FLAG_LAYOUT_ZIGZAG ? glr_fwd_kernel<T, W, true> : glr_fwd_kernel<T, W, false>, W,
+                kPerSm<S, kFwdPerSm>, sizeof(S)};
+}
+template <typename T>
+Form bwd(const cpdr_ctx *c) {
+    constexpr int W = kBwdWarps<T>;
+    using S = BwdShared<T, W>;
+    return Form{c->plan.flags & CPDR_FLAG_LAYOUT_ZIGZAG ? glr_bwd_kernel<T, W, true> : glr_bwd_kernel<T, W, false>, W,
+                kPerSm<S, kBwdPerSm>, sizeof(S)};
+}
+Form form(const cpdr_ctx *c, bool backward) {
+    if (c->plan.in_dtype == CPDR_DTYPE_F32) return backward ? bwd<float>(c) : fwd<float>(c);
+    return backward ? bwd<__nv_bfloat16>(c) : fwd<__nv_bfloat16>(c);
+}
+
+int launch(const cpdr_ctx *c, const Form &f, Params p, void *stream) {
     const auto &pl = c->plan;
     p.spans = c->dev.glr_spans;
     p.status = c->dev.status;
@@ -738,29 +765,30 @@ int launch(const cpdr_ctx *c, K kernel, int warps, int per_sm, size_t bytes, Par
     p.parts = (pl.flags & CPDR_FLAG_LAYOUT_ZIGZAG) ? pl.R : 0;
     p.slices = (p.channels + kSlice - 1) / kSlice;
     const int64_t items = (int64_t)pl.glr_spans.size() * p.slices;
-    const int nz = pick_cluster(c, p.slices, warps * kGlrGroup, per_sm);
+    const int nz = pick_cluster(c, p.slices, f.warps * kGlrGroup, f.per_sm);
     if (items * nz > (int64_t)0x7fffffff) return (int)cudaErrorInvalidValue;
-    return launch_early(kernel, dim3((unsigned)(items * nz)), 32 * warps, bytes, nz, stream, p, nz);
+    return launch_early(f.kernel, dim3((unsigned)(items * nz)), 32 * f.warps, f.bytes, nz, stream, p, nz);
 }
 
 static_assert(sizeof(FwdShared<float, kFwdWarps>) <= 227 * 1024 && sizeof(BwdShared<float, kBwdWarps<float>>) <= 227 * 1024 &&
                   sizeof(BwdShared<__nv_bfloat16, kBwdWarps<__nv_bfloat16>>) <= 227 * 1024,
               "a CTA's stages fit its shared memory");
 
-template <typename T>
-int fwd(const cpdr_ctx *c, const Params &p, void *stream) {
-    constexpr int W = kFwdWarps;
-    auto kernel = c->plan.flags & CPDR_FLAG_LAYOUT_ZIGZAG ? glr_fwd_kernel<T, W, true> : glr_fwd_kernel<T, W, false>;
-    return launch(c, kernel, W, kPerSm<FwdShared<T, W>>, sizeof(FwdShared<T, W>), p, stream);
-}
-template <typename T>
-int bwd(const cpdr_ctx *c, const Params &p, void *stream) {
-    constexpr int W = kBwdWarps<T>;
-    auto kernel = c->plan.flags & CPDR_FLAG_LAYOUT_ZIGZAG ? glr_bwd_kernel<T, W, true> : glr_bwd_kernel<T, W, false>;
-    return launch(c, kernel, W, kPerSm<BwdShared<T, W>>, sizeof(BwdShared<T, W>), p, stream);
-}
-
 }  // namespace
+
+int glr_plan(const cpdr_ctx *c, int channels, bool backward, int32_t out[3]) {
+    const Form f = form(c, backward);
+    out[0] = pick_cluster(c, (channels + kSlice - 1) / kSlice, f.warps * kGlrGroup, f.per_sm);
+    out[1] = f.per_sm;
+    out[2] = 0;
+    if (!c->has_device) return 0;
+    cudaError_t e = cudaFuncSetAttribute(f.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)f.bytes);
+    if (e != cudaSuccess) return (int)e;
+    int n = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, f.kernel, 32 * f.warps, f.bytes);
+    out[2] = n;
+    return (int)e;
+}
 
 int launch_glr_fwd(const cpdr_ctx *c, const void *x, const float *g, const float *h0, int channels, void *y,
                    float *hT, float *carry, void *stream) {
@@ -772,8 +800,7 @@ int launch_glr_fwd(const cpdr_ctx *c, const void *x, const float *g, const float
     p.hT = hT;
     p.carry = carry;
     p.channels = channels;
-    return c->plan.in_dtype == CPDR_DTYPE_F32 ? fwd<float>(c, p, stream)
-                                              : fwd<__nv_bfloat16>(c, p, stream);
+    return launch(c, form(c, false), p, stream);
 }
 
 int launch_glr_bwd(const cpdr_ctx *c, const void *x, const float *g, const float *carry, const void *dy,
@@ -788,8 +815,7 @@ int launch_glr_bwd(const cpdr_ctx *c, const void *x, const float *g, const float
     p.dg = dg;
     p.hT = dh0;
     p.channels = channels;
-    return c->plan.in_dtype == CPDR_DTYPE_F32 ? bwd<float>(c, p, stream)
-                                              : bwd<__nv_bfloat16>(c, p, stream);
+    return launch(c, form(c, true), p, stream);
 }
 
 int launch_glr_step(const cpdr_ctx *c, const void *x, const float *g, const float *state, float *state_out,

@@ -113,6 +113,13 @@ cpdr_status cpdr_glr_carry_bytes(const cpdr_ctx *c, int32_t channels, size_t *by
     return CPDR_OK;
 }
 
+cpdr_status cpdr_plan_glr(const cpdr_ctx *c, int32_t channels, int32_t backward, int32_t out[3]) {
+    if (!c || !out) return fail_with(CPDR_ERR_INVALID, "null argument");
+    if (c->has_device) CPDR_TRY(check_launch_ctx(c));
+    CPDR_TRY(check_channels("cpdr_plan_glr", channels));
+    return check_launched(cpdr::glr_plan(c, channels, backward != 0, out), "cpdr_plan_glr");
+}
+
 cpdr_status cpdr_glr_fwd(const cpdr_ctx *c, const void *x, const float *gate, const float *h0, int32_t channels,
                          void *y, float *hT, float *carry, void *stream) {
     CPDR_TRY(check_launch_ctx(c));

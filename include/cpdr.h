@@ -346,6 +346,14 @@ cpdr_status cpdr_glr_fwd(const cpdr_ctx *ctx, const void *x, const float *gate, 
                          void *y, float *hT, float *carry, void *stream);
 
 /*
+ * Plan introspection: how cpdr_glr_fwd (backward 0) or cpdr_glr_bwd (1) runs
+ * over the context's sequences with that many channels.  out = {CTAs of a
+ * cluster, CTAs of an SM that the choice counts on, CTAs of an SM that the
+ * device holds (0 for a host-only context)}.
+ */
+cpdr_status cpdr_plan_glr(const cpdr_ctx *ctx, int32_t channels, int32_t backward, int32_t out[3]);
+
+/*
  * Its backward: the gradients of  sum_t <dy_t, y_t> + sum_n <dhT_n, hT_n>,
  *     dh_t = dy_t + a_{t+1} dh_{t+1}  (dhT in the place of the last product),
  *     dx_t = dh_t,   dgate_t = dh_t a_t h_{t-1},   dh0 = a_0 dh_0.
