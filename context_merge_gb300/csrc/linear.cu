@@ -260,6 +260,25 @@ struct WideBars {
 };
 static_assert(sizeof(WideBars) <= 256, "barriers");
 
+// Waits until accumulator `acc` has its tile.  The products take as long as their
+// blocks of r: the usual limit and 2000 cycles for each of them (they take up
+// to 600; a sum over 6e8 rows lasts longer than the usual limit).
+__device__ __noinline__ bool wait_products(WideBars *b, int acc, uint32_t phase, int blocks, int32_t *status) {
+    const long long t0 = clock64(), limit = kWaitCycles + 2000LL * blocks;
+    while (!mbar_try_wait_sleep(&b->acc_full[acc], phase, 200000u)) {
+        if (b->ctl.abort) return false;
+        if (clock64() - t0 > limit) {
+            if (atomicCAS(status, 0, 1) == 0) {
+                status[1] = 163;
+                status[2] = (int32_t)blockIdx.x;
+            }
+            b->ctl.abort = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
 // Tiles in groups of 8 rows of tiles, column by column inside a group, so
 // that the tiles that run together share their operands in the L2.  (One B
 // fetched for two pairs by multicast, in clusters of 4: 0.92 to 1.09 of these
@@ -415,7 +434,11 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
                 }
             };
             columns(q0);
-            if (!warp_wait_all(&b.acc_full[acc], (uint32_t)(n >> 1) & 1u, &b.ctl, a.status, 163)) break;
+            {
+                const uint32_t phase = (uint32_t)(n >> 1) & 1u;
+                const bool ok = mbar_try_wait(&b.acc_full[acc], phase) || wait_products(&b, acc, phase, a.blocks, a.status);
+                if (!__all_sync(0xffffffffu, ok)) break;
+            }
             tc_fence_after();
             if (RES && pieces && !warp_wait_all(&b.residual[w], (uint32_t)(fetched++) & 1u, &b.ctl, a.status, 164)) break;
 #pragma unroll 1
