@@ -32,7 +32,7 @@ EXPORTED = ["cpdr_ctx_create", "cpdr_ctx_destroy", "cpdr_buffer_sizes", "cpdr_pl
             "cpdr_forward_host", "cpdr_forward_noalloc", "cpdr_check_device_status", "cpdr_selftest_wait_timeout",
             "cpdr_conv1d_fwd", "cpdr_plan_conv_tokens", "cpdr_bwd_workspace_bytes", "cpdr_bwd",
             "cpdr_glr_carry_bytes", "cpdr_plan_glr", "cpdr_glr_fwd", "cpdr_glr_bwd", "cpdr_glr_step", "cpdr_rmsnorm_fwd",
-            "cpdr_rmsnorm_bwd_workspace_bytes", "cpdr_rmsnorm_bwd", "cpdr_linear_fwd",
+            "cpdr_rmsnorm_bwd_workspace_bytes", "cpdr_rmsnorm_bwd", "cpdr_plan_linear", "cpdr_linear_fwd",
             "cpdr_linear_bwd_workspace_bytes", "cpdr_linear_bwd", "cpdr_last_error", "cpdr_version"]
 
 
@@ -102,6 +102,7 @@ def load():
         lib.cpdr_rmsnorm_fwd.argtypes = [vp, i64, i32, vp, vp, vp, f32] + [vp] * 5
         lib.cpdr_rmsnorm_bwd_workspace_bytes.argtypes = [vp, i64, i32, ctypes.POINTER(sz)]
         lib.cpdr_rmsnorm_bwd.argtypes = [vp, i64, i32, vp, vp, f32] + [vp] * 5 + [sz, vp]
+        lib.cpdr_plan_linear.argtypes = [vp, i64, i32, i32, i32, ctypes.POINTER(i32)]
         lib.cpdr_linear_fwd.argtypes = [vp, i64, i32, i32] + [vp] * 5 + [i32] + [vp] * 4
         lib.cpdr_linear_bwd_workspace_bytes.argtypes = [vp, i64, i32, i32, i32, ctypes.POINTER(sz)]
         lib.cpdr_linear_bwd.argtypes = [vp, i64, i32, i32] + [vp] * 4 + [i32] + [vp] * 4 + [sz, vp]
@@ -536,6 +537,14 @@ class Context:
                                          ACTIVATIONS[activation], _addr("residual", residual, out, _BF16, dev),
                                          _addr("z", z, out, _BF16, dev), _addr("y", y, out, _BF16, dev),
                                          _raw_stream(stream, dev)))
+
+    def linear_plan(self, rows, K, N, e4m3=False):
+        """The form in which a product runs: (rows of x in a tile of the form for
+        few rows, or 0 for the other one; CTAs that K is split over).  The input
+        gradient of w [K, N] runs as a product of the same sizes."""
+        out = (ctypes.c_int32 * 2)()
+        _check(self._lib.cpdr_plan_linear(self._h, int(rows), int(K), int(N), int(e4m3), out))
+        return tuple(out)
 
     def linear_bwd_workspace_bytes(self, rows, K, N, activation=None):
         n = ctypes.c_size_t()

@@ -263,6 +263,7 @@ int launch_column_sums(const float *part, int nparts, int width, float *out, voi
 int launch_linear_fwd(const cpdr_ctx *c, int64_t rows, int K, int N, const void *x, const void *w, const float *x_scale,
                       const float *w_scale, const float *bias, int act, const void *residual, void *z, void *y,
                       void *stream);
+void linear_plan(const cpdr_ctx *c, int64_t rows, int K, int N, bool e4m3, int32_t out[2]);
 size_t linear_dz_parts(const cpdr_ctx *c, int64_t rows, int N);
 int launch_linear_bwd(const cpdr_ctx *c, int64_t rows, int K, int N, const void *x, const void *w, const void *z,
                       const void *dy, int act, void *dx, void *dw, float *dbias, void *dz, float *part, void *stream);

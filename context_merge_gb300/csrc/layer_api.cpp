@@ -242,6 +242,14 @@ cpdr_status cpdr_rmsnorm_bwd(const cpdr_ctx *c, int64_t rows, int32_t width, con
                           "cpdr_rmsnorm_bwd");
 }
 
+cpdr_status cpdr_plan_linear(const cpdr_ctx *c, int64_t rows, int32_t K, int32_t N, int32_t e4m3, int32_t out[2]) {
+    if (!c || !out) return fail_with(CPDR_ERR_INVALID, "null argument");
+    CPDR_TRY(check_linear("cpdr_plan_linear", c, rows, K, N, 0, e4m3 != 0));
+    if (rows == 0) return fail_with(CPDR_ERR_INVALID, "cpdr_plan_linear: no rows");
+    cpdr::linear_plan(c, rows, K, N, e4m3 != 0, out);
+    return CPDR_OK;
+}
+
 cpdr_status cpdr_linear_fwd(const cpdr_ctx *c, int64_t rows, int32_t K, int32_t N, const void *x, const void *w,
                             const float *x_scale, const float *w_scale, const float *bias, int32_t activation,
                             const void *residual, void *z, void *y, void *stream) {

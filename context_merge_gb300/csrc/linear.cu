@@ -1005,6 +1005,12 @@ int launch_linear_fwd(const cpdr_ctx *c, int64_t rows, int K, int N, const void 
     return e4m3 ? product<true, false>(X, W, a, y, z, sms, st) : product<false, false>(X, W, a, y, z, sms, st);
 }
 
+void linear_plan(const cpdr_ctx *c, int64_t rows, int K, int N, bool e4m3, int32_t out[2]) {
+    const Choice ch = choose(rows, N, (K * (e4m3 ? 1 : 2) + kRBytes - 1) / kRBytes, device_sms(c->device));
+    out[0] = ch.qn;
+    out[1] = ch.split;
+}
+
 size_t linear_dz_parts(const cpdr_ctx *c, int64_t rows, int N) {
     const int per = dz_rows_per_block(rows, N, device_sms(c->device));
     return (size_t)((rows + per - 1) / per);

@@ -434,6 +434,13 @@ cpdr_status cpdr_linear_fwd(const cpdr_ctx *ctx, int64_t rows, int32_t K, int32_
                             const void *residual, void *z, void *y, void *stream);
 
 /*
+ * Plan introspection: the form in which cpdr_linear_fwd runs these sizes (and
+ * cpdr_linear_bwd the input gradient of w [K, N]).  out = {rows of x in a tile
+ * of the form for few rows, 0: the form for many; CTAs that K is split over}.
+ */
+cpdr_status cpdr_plan_linear(const cpdr_ctx *ctx, int64_t rows, int32_t K, int32_t N, int32_t e4m3, int32_t out[2]);
+
+/*
  * Its backward for bf16 operands, from dy [rows, N] bf16 (which is also the
  * residual's gradient):
  *     dz = dy act'(z),   dx = dz w,   dw = dz^T x,   dbias = sum over rows of dz.
