@@ -479,7 +479,7 @@ class Context:
     def rmsnorm_fwd(self, x, weight, residual=None, sum_out=None, y=None, y8=None, scale=None, eps=1e-6, stream=None):
         """RMS norm of s = x + residual over the last axis, times weight
         (fp32): s into ``sum_out``, the norm into ``y`` (input dtype) and/or
-        ``y8`` (float8_e4m3fn) with ``scale`` (fp32, one per row)."""
+        ``y8`` (float8_e4m3fn) with ``scale`` (fp32, one per row).  |s| up to 1e17."""
         rows, width = self._rows(x)
         dt, dev, sh = self.torch_dtype, self._dev, x.shape
         _check(self._lib.cpdr_rmsnorm_fwd(self._h, rows, width, _addr("x", x, sh, dt, dev),

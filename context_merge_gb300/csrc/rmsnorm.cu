@@ -2,7 +2,7 @@
 // `width` elements, with s = x + residual (or x),
 //     rstd = 1 / sqrt(mean(s^2) + eps),   y_i = (s_i w_i) rstd,
 // as T (fp32 or bf16), or as e4m3 with one scale per row,
-//     scale = max(max_i |y_i| / 448, 2^-126),   y8_i = e4m3(y_i / scale);
+//     scale = max(max_i |y_i| / 448, 2^-126),   y8_i = e4m3(y_i (1 / scale));
 // backward, from dy and (optionally) the gradient dsum that reaches s by the
 // residual stream,
 //     ds_i = rstd (w_i dy_i - s_i rstd^2 mean(s w dy)) + dsum_i,

@@ -387,8 +387,11 @@ cpdr_status cpdr_glr_step(const cpdr_ctx *ctx, const void *x, const float *gate,
  * [width] fp32.  sum_out (or NULL) receives s, rounded once; y is computed
  * from the unrounded sum.  y8 and scale (both or neither; y may be NULL then,
  * or given too): y in 8 bits, e4m3 [rows, width], with one fp32 scale per row,
- *     scale = max(max_i |y_i| / 448, 2^-126),   y8_i = e4m3(y_i / scale),
- * rounded to nearest even; a row with a NaN or an infinity has a NaN scale.
+ *     scale = max(max_i |y_i| / 448, 2^-126),   y8_i = e4m3(y_i (1 / scale)),
+ * rounded to nearest even, 1 / scale rounded to fp32 first (a quotient next to a
+ * tie may go the other way); a row with a NaN or an infinity has a NaN scale.
+ * Squares are summed in fp32: |s| up to 1e17 (a row whose sum passes fp32's
+ * range gives y = 0), and with eps = 0 from 1e-18 up.
  * sum_out and y may each be x or residual (in place; not both the same).
  * rows >= 0, width % 8 == 0, width <= 16384, 0 <= eps <= 1.  A row is
  * anything that is normalised as one: a token, or a head of d elements.
