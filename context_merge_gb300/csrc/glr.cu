@@ -18,9 +18,12 @@
 // sums run in a fixed order, and the result does not depend on timing.  A
 // step's exchange goes on while the step before it is written.
 //
-// Measured (of 6782 GB/s): forward 262144 x 2048 bf16, one sequence, 677 us,
-// 0.96; packed 65536 x 2048, 12 ragged sequences: fp32 zigzag forward 261 us,
-// 0.91; bf16 backward 305 us, 0.93.
+// Measured (of 6782 GB/s): forward 262144 x 2048 bf16, one sequence, 674 us,
+// 0.97; packed 65536 x 2048, 12 ragged sequences: fp32 zigzag forward 259 us,
+// 0.91; bf16 backward 304 us, 0.93.  Few channels leave SMs idle: one sequence of
+// 131072 x 64, forward 282 us, backward 307.  Where most groups have positive
+// gates that sum to more than 1, 32768 x 2048 takes 378 and 556 us (91 and 156
+// without).
 //
 // The backward recomputes h inside each group from the state before the
 // group's first token (the carry, fp32, 4 bytes per 16 tokens, that the
@@ -706,10 +709,11 @@ glr_step_kernel(const T *x, const float *g, const float *state, float *state_out
 // CTAs of a cluster, by an estimate of the time in tokens that one CTA takes:
 // the longest sequence's share, or all items' over the clusters that run at
 // once, with a quarter of an item for the last round's gaps; an exchange costs
-// 4% per CTA.  Measured with clusters of 1, 2, 4 and 8 (us): one sequence of
-// 32768 x 2048, forward 399, 230, 125, 93 and backward 597, 315, 167, 257 (of
+// 4% per CTA.  Measured with clusters of 1, 2, 4 and 8 (us, bf16): one sequence of
+// 32768 x 2048, forward 457, 269, 155, 93 and backward 549, 298, 159, 246 (of
 // eight, 15 clusters run at once); 12 ragged sequences in 65536 x 2048,
-// backward 311, 305, 338, 472; 64 of 1024 x 2048, forward 165, 186, 238, 353.
+// forward 193, 181, 181, 210 and backward 306, 306, 332, 465; 64 of 1024 x 2048,
+// forward 166, 193, 252, 378.
 int pick_cluster(const cpdr_ctx *c, int slices, int tile, int per_sm) {
     const auto &pl = c->plan;
     const int64_t items = (int64_t)pl.glr_spans.size() * slices;

@@ -21,11 +21,13 @@
 //    epilogue warps empty one while the other fills; outputs leave through
 //    swizzled staging tiles by TMA, which also cuts what lies outside the
 //    matrix.  bf16 32768 x 2048 x 6144: 417 us, 1.98 PFLOP/s (the library's
-//    product 415); e4m3 252 us, 3.27 PFLOP/s; tensor pipe 92% and 86% active.
+//    product 413); e4m3 255 us, 3.23 PFLOP/s, in short runs and 273 to 288 in
+//    longer ones; tensor pipe 92% and 86% active.
 //  * narrow_kernel, for few rows of x, bound by reading w: 128 rows of w (the
 //    128 lanes) by 16 to 128 rows of x (the columns) per CTA, with r split
 //    over a cluster of up to 8 CTAs, whose partial sums meet in distributed
-//    shared memory in the order of the CTAs.  16 x 2048 x 6144: 8.5 us (25 MB
+//    shared memory in the order of the CTAs.  16 x 2048 x 6144: 7.0 us
+//    in a chain of calls, 8.5 in a graph (25 MB
 //    of w, 3.7 us at the measured copy rate; the library's product 6.3): 2 us
 //    until the unit has fetched the tensors' maps and the first bytes are
 //    there, 3 us until the last of w, 1.5 for the partial sums and the epilogue.

@@ -17,9 +17,10 @@
 // y is computed from the unrounded sum.
 //
 // Measured over 0.4 GB a tensor: forward 6.8 to 7.1 TB/s (bf16 with a
-// residual, 72 to 12288 columns) and 6.4 to 7.1 (fp32); backward 4.0 to 6.0
-// TB/s up to 8192 columns of bf16, 5.9 to 6.7 up to 6144 of fp32, and 3.8 to
-// 5.7 for wider rows: few of them are in flight in an SM.
+// residual, 72 to 12288 columns; 6.1 at 16384) and 6.4 to 7.1 (fp32); backward
+// 4.9 to 6.1 TB/s up to 2048 columns of bf16, 4.1 to 5.3 up to 8192 and 3.8 to
+// 4.5 beyond, and of fp32 5.9 to 6.7 up to 6144 columns and 4.6 to 5.6 beyond:
+// few wide rows are in flight in an SM.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
