@@ -330,8 +330,8 @@ cpdr_status cpdr_bwd(const cpdr_ctx *ctx, const void *q, const void *k, const vo
  * most 88; -infinity is one (a_t = 0: the state is dropped); from -87.4 down
  * a_t is 0.  x and h0 are finite, and so is the state that the same x would
  * give from zero at any token.  Positive gates that sum to more than 1 over 16
- * tokens (or a NaN) cost time: up to 1024 tokens around them run one 16 behind
- * the other.  What falls below 1e-17 of the largest state of the last 1024
+ * tokens cost time: up to 1024 tokens around them run one 16 behind the other
+ * (and all that follow a NaN or an infinity).  What falls below 1e-17 of the largest state of the last 1024
  * tokens counts as zero.  Sequences and token layout are the context's (packed
  * batches, zigzag); its segments play no part.
  * Layout: x, y [B, T, channels] in the context's token order and input dtype;
