@@ -49,6 +49,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kFwdStages = 2;               // groups of a warp in shared memory, both on their way
 constexpr int kStages = 3;                  // backward: going out, being mapped, on its way
 constexpr int kStepThreads = 256;
+constexpr float kMaxFloat = 3.402823466e38f;
 // Warps of a CTA.  Forward: two CTAs of four per SM, whose steps hide one
 // another's (262144 x 2048 bf16, one sequence: 677 us; of six warps 709; three
 // of four 729).  Backward: one CTA of what three stages leave room for (packed
@@ -343,9 +344,10 @@ struct alignas(16) Exchange {
             v = apply(all, carry);
         }
         s = apply(before, s);
-        // a NaN: of a map that must not be composed, or (nothing is lost then but
-        // time) of the state itself.  The whole cluster goes this way or that as one.
-        const bool x = v.x != v.x, y = v.y != v.y;
+        // not finite: a map that must not be composed, one whose B overflows where the
+        // state does not, or (nothing is lost then but time) the state itself.
+        // The whole cluster sees the same maps and goes this way or that as one.
+        const bool x = !(fabsf(v.x) <= kMaxFloat), y = !(fabsf(v.y) <= kMaxFloat);
         if (__any_sync(0xffffffffu, x || y)) {
             float2 end;
             const float2 h = in_turn(w, lane, rank, nz, carry, end, status, turns++ & 1u, group);

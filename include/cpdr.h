@@ -328,12 +328,12 @@ cpdr_status cpdr_bwd(const cpdr_ctx *ctx, const void *q, const void *k, const vo
  * from h0 (or zero) at the sequence's start; hT is the state behind its last
  * token (h0, or zero, for an empty sequence).  gate is a natural-log gate, at
  * most 88; -infinity is one (a_t = 0: the state is dropped); from -87.4 down
- * a_t is 0.  x and h0 are finite, and so is the state that the same x would
- * give from zero at any token.  Positive gates that sum to more than 1 over 16
- * tokens cost time: up to 1024 tokens around them run one 16 behind the other
- * (and all that follow a NaN or an infinity).  What falls below 1e-17 of the largest state of the last 1024
- * tokens counts as zero.  Sequences and token layout are the context's (packed
- * batches, zigzag); its segments play no part.
+ * a_t is 0.  x and h0 are finite.  Positive gates that sum to more than 1 over
+ * 16 tokens cost time: up to 1024 tokens around them run 16 at a time, one group
+ * behind the other (so do all that follow a state that is not finite).  What
+ * falls below 1e-17 of the largest state of the last 1024 tokens counts as zero.
+ * Sequences and token layout are the context's (packed batches, zigzag); its
+ * segments play no part.
  * Layout: x, y [B, T, channels] in the context's token order and input dtype;
  * gate [B, T, channels] fp32; h0, hT [N, channels] fp32, either may be NULL
  * (hT may be h0 itself); channels % 8 == 0, at most 2^24.

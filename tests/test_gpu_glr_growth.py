@@ -77,6 +77,21 @@ def test_small_states_grow():
     both(inp, "fp32")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("first,second,back", [(0, 1, 2), (5, 20, 40), (3, 200, 1100)])
+def test_states_that_only_the_initial_state_keeps_finite(first, second, back, dtype):
+    """From -3e38, 3e38 twice and back: 0, 3e38, 0.  From zero the same terms would overflow."""
+    inp = draw(1, 1200, 64, 1, dtype, 10)
+    inp["g"].zero_()
+    inp["x"].zero_()
+    inp["x"][0, [first, second]] = 3e38
+    inp["x"][0, back] = -3e38
+    inp["h0"][:] = -inp["x"][0, first].float()
+    inp["dy"].mul_(1e-6)
+    inp["dhT"].mul_(1e-6)
+    both(inp, dtype)
+
+
 @pytest.mark.parametrize("gate", [0.06, 0.0625, 0.0626, 0.25])
 def test_slow_growth_on_both_sides_of_the_rule(gate):
     """Sums of positive gates next to the one over 16 tokens where the kernels change over."""
