@@ -33,7 +33,9 @@ EXPORTED = ["cpdr_ctx_create", "cpdr_ctx_destroy", "cpdr_buffer_sizes", "cpdr_pl
             "cpdr_conv1d_fwd", "cpdr_plan_conv_tokens", "cpdr_bwd_workspace_bytes", "cpdr_bwd",
             "cpdr_glr_carry_bytes", "cpdr_plan_glr", "cpdr_glr_fwd", "cpdr_glr_bwd", "cpdr_glr_step", "cpdr_rmsnorm_fwd",
             "cpdr_rmsnorm_bwd_workspace_bytes", "cpdr_rmsnorm_bwd", "cpdr_plan_linear", "cpdr_linear_fwd",
-            "cpdr_linear_bwd_workspace_bytes", "cpdr_linear_bwd", "cpdr_last_error", "cpdr_version"]
+            "cpdr_linear_bwd_workspace_bytes", "cpdr_linear_bwd", "cpdr_layernorm_fwd",
+            "cpdr_layernorm_bwd_workspace_bytes", "cpdr_layernorm_bwd", "cpdr_embed_fwd",
+            "cpdr_embed_bwd_workspace_bytes", "cpdr_embed_bwd", "cpdr_delta_step", "cpdr_conv1d_step", "cpdr_last_error", "cpdr_version"]
 
 
 _F32, _BF16, _E4M3 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
@@ -102,6 +104,14 @@ def load():
         lib.cpdr_rmsnorm_fwd.argtypes = [vp, i64, i32, vp, vp, vp, f32] + [vp] * 5
         lib.cpdr_rmsnorm_bwd_workspace_bytes.argtypes = [vp, i64, i32, ctypes.POINTER(sz)]
         lib.cpdr_rmsnorm_bwd.argtypes = [vp, i64, i32, vp, vp, f32] + [vp] * 5 + [sz, vp]
+        lib.cpdr_layernorm_fwd.argtypes = [vp, i64, i32] + [vp] * 4 + [f32] + [vp] * 5
+        lib.cpdr_layernorm_bwd_workspace_bytes.argtypes = [vp, i64, i32, ctypes.POINTER(sz)]
+        lib.cpdr_layernorm_bwd.argtypes = [vp, i64, i32, vp, vp, f32] + [vp] * 6 + [sz, vp]
+        lib.cpdr_embed_fwd.argtypes = [vp, vp, i64, vp, i32, i32, f32, vp, vp]
+        lib.cpdr_embed_bwd_workspace_bytes.argtypes = [vp, i64, i32, i32, ctypes.POINTER(sz)]
+        lib.cpdr_embed_bwd.argtypes = [vp, vp, i64, i32, i32, f32, vp, vp, vp, sz, vp]
+        lib.cpdr_delta_step.argtypes = [vp] * 9 + [i32] * 2 + [vp] * 2
+        lib.cpdr_conv1d_step.argtypes = [vp] * 7 + [i32] * 4 + [vp] * 2
         lib.cpdr_plan_linear.argtypes = [vp, i64, i32, i32, i32, ctypes.POINTER(i32)]
         lib.cpdr_linear_fwd.argtypes = [vp, i64, i32, i32] + [vp] * 5 + [i32] + [vp] * 4
         lib.cpdr_linear_bwd_workspace_bytes.argtypes = [vp, i64, i32, i32, i32, ctypes.POINTER(sz)]
@@ -513,6 +523,124 @@ class Context:
                                           _addr("dweight", out["dweight"], sh[-1:], _F32, dev), *_space(workspace, dev),
                                           _raw_stream(stream, dev)))
         return out
+
+    # ---- layer norm --------------------------------------------------------
+    def layernorm_fwd(self, x, weight, bias=None, residual=None, sum_out=None, y=None, y8=None, scale=None, eps=1e-5,
+                      stream=None):
+        """Layer norm of s = x + residual over the last axis, times weight plus
+        bias (fp32): s into ``sum_out``, the norm into ``y`` (input dtype)
+        and/or ``y8`` (float8_e4m3fn) with ``scale`` (fp32, one per row).  |s| up to 1e17."""
+        rows, width = self._rows(x)
+        dt, dev, sh = self.torch_dtype, self._dev, x.shape
+        _check(self._lib.cpdr_layernorm_fwd(self._h, rows, width, _addr("x", x, sh, dt, dev),
+                                            _addr("residual", residual, sh, dt, dev),
+                                            _addr("weight", weight, (width,), _F32, dev),
+                                            _addr("bias", bias, (width,), _F32, dev), eps,
+                                            _addr("sum_out", sum_out, sh, dt, dev), _addr("y", y, sh, dt, dev),
+                                            _addr("y8", y8, sh, _E4M3, dev),
+                                            None if scale is None else _addr("scale", scale, sh[:-1], _F32, dev),
+                                            _raw_stream(stream, dev)))
+
+    def layernorm_bwd_workspace_bytes(self, rows, width):
+        n = ctypes.c_size_t()
+        _check(self._lib.cpdr_layernorm_bwd_workspace_bytes(self._h, int(rows), int(width), ctypes.byref(n)))
+        return n.value
+
+    def layernorm_bwd(self, s, weight, dy, dsum=None, eps=1e-5, out=None, workspace=None, stream=None):
+        """Gradients of the norm from s (``sum_out``, or x), dy and the
+        gradient ``dsum`` that reaches s past the norm: a dict of ds (input
+        dtype; of x and residual alike), dweight and dbias (fp32; a given
+        ``out`` may lack dbias)."""
+        rows, width = self._rows(s)
+        dt, dev, sh = self.torch_dtype, self._dev, s.shape
+        args = (_addr("s", s, sh, dt, dev), _addr("weight", weight, sh[-1:], _F32, dev), eps,
+                _addr("dy", dy, sh, dt, dev), _addr("dsum", dsum, sh, dt, dev))
+        if out is None or workspace is None:
+            with _owned_by(stream):
+                if out is None:
+                    out = dict(ds=torch.empty_like(s), dweight=torch.empty_like(weight), dbias=torch.empty_like(weight))
+                if workspace is None:
+                    workspace = torch.empty(self.layernorm_bwd_workspace_bytes(rows, width), dtype=torch.uint8,
+                                            device=s.device)
+        _check(self._lib.cpdr_layernorm_bwd(self._h, rows, width, *args, _addr("ds", out["ds"], sh, dt, dev),
+                                            _addr("dweight", out["dweight"], sh[-1:], _F32, dev),
+                                            _addr("dbias", out.get("dbias"), sh[-1:], _F32, dev),
+                                            *_space(workspace, dev), _raw_stream(stream, dev)))
+        return out
+
+    # ---- embedding -----------------------------------------------------------
+    def embed_fwd(self, tokens, table, y, scale=1.0, stream=None):
+        """y = scale table[tokens]: tokens [..] int32, table [V, D] and y
+        [.., D] in the input dtype; tokens outside 0 .. V - 1 (padding) give
+        rows of zeros."""
+        if table.dim() != 2:
+            raise ValueError(f"table must be a [V, D] tensor, got {list(table.shape)}")
+        (V, D), dt, dev, sh = table.shape, self.torch_dtype, self._dev, tokens.shape
+        _check(self._lib.cpdr_embed_fwd(self._h, _addr("tokens", tokens, sh, torch.int32, dev), tokens.numel(),
+                                        _addr("table", table, (V, D), dt, dev), V, D, scale,
+                                        _addr("y", y, (*sh, D), dt, dev), _raw_stream(stream, dev)))
+
+    def embed_bwd_workspace_bytes(self, n, vocab, width):
+        b = ctypes.c_size_t()
+        _check(self._lib.cpdr_embed_bwd_workspace_bytes(self._h, int(n), int(vocab), int(width), ctypes.byref(b)))
+        return b.value
+
+    def embed_bwd(self, tokens, dy, dtable, scale=1.0, workspace=None, stream=None):
+        """The table's gradient from dy [.., D]: the whole of ``dtable`` [V, D]
+        (input dtype) is written, and returned."""
+        if dtable.dim() != 2:
+            raise ValueError(f"dtable must be a [V, D] tensor, got {list(dtable.shape)}")
+        (V, D), dt, dev, sh = dtable.shape, self.torch_dtype, self._dev, tokens.shape
+        n = tokens.numel()
+        args = (_addr("tokens", tokens, sh, torch.int32, dev), n, V, D, scale, _addr("dy", dy, (*sh, D), dt, dev),
+                _addr("dtable", dtable, (V, D), dt, dev))
+        if workspace is None:
+            with _owned_by(stream):
+                workspace = torch.empty(self.embed_bwd_workspace_bytes(n, V, D), dtype=torch.uint8, device=dtable.device)
+        _check(self._lib.cpdr_embed_bwd(self._h, *args, *_space(workspace, dev), _raw_stream(stream, dev)))
+        return dtable
+
+    # ---- token steps of the mixers over a pool of slots ------------------------
+    def delta_step(self, q, k, v, beta, g, state, o, slots=None, state_out=None, stream=None):
+        """The gated delta rule, one token for each row: q and o [n, Hq, d],
+        k and v [n, H, d], beta [n, H] in the input dtype, g [n, H] or
+        [n, H, d] fp32; row i continues the sequence whose states are slot
+        ``slots[i]`` (int32; None: i) of state [S, H, d, d] fp32 (as
+        ``fwd`` leaves ``final_state``), updated in place or into
+        ``state_out``.  Rows with a slot outside 0 .. S - 1 are left alone;
+        rows of one slot are its consecutive tokens."""
+        n, H, d = k.shape[0], self.H, self.d
+        dt, dev = self.torch_dtype, self._dev
+        wide, kv = (n, self.Hq, d), (n, H, d)
+        st = (state.shape[0], H, d, d)
+        old = _addr("state", state, st, _F32, dev)
+        _check(self._lib.cpdr_delta_step(self._h, _addr("q", q, wide, dt, dev), _addr("k", k, kv, dt, dev),
+                                         _addr("v", v, kv, dt, dev), _addr("beta", beta, (n, H), dt, dev),
+                                         _addr("g", g, (n, H) if self.gate == "gdn" else kv, _F32, dev), old,
+                                         old if state_out is None else _addr("state_out", state_out, st, _F32, dev),
+                                         _addr("slots", slots, (n,), torch.int32, dev), n, st[0],
+                                         _addr("o", o, wide, dt, dev), _raw_stream(stream, dev)))
+
+    def conv1d_step(self, x, weight, bias, state, y, slots=None, state_out=None, activation="silu", stream=None):
+        """The causal conv, one token for each row: x and y [n, C] in the input
+        dtype, weight [C, W] and bias [C] fp32; row i continues the sequence
+        whose last W - 1 inputs, oldest first, are slot ``slots[i]`` (int32;
+        None: i) of state [S, W - 1, C] (input dtype), moved on in place or
+        into ``state_out``.  Rows with a slot outside 0 .. S - 1 are left
+        alone; rows of one slot are its consecutive tokens."""
+        if x.dim() != 2 or state.dim() != 3:
+            raise ValueError("x must be [n, C] and state [S, W - 1, C]")
+        rows, W = x.shape, self.conv_width
+        dt, dev = self.torch_dtype, self._dev
+        st = (state.shape[0], max(0, W - 1), rows[1])
+        old = _addr("state", state, st, dt, dev)
+        _check(self._lib.cpdr_conv1d_step(self._h, _addr("x", x, rows, dt, dev),
+                                          _addr("weight", weight, (rows[1], W), _F32, dev),
+                                          _addr("bias", bias, rows[1:], _F32, dev), old,
+                                          old if state_out is None else _addr("state_out", state_out, st, dt, dev),
+                                          _addr("slots", slots, rows[:1], torch.int32, dev), rows[0], st[0], rows[1],
+                                          {"silu": 1, None: 0, "none": 0}[activation], _addr("y", y, rows, dt, dev),
+                                          _raw_stream(stream, dev)))
 
     # ---- matrix product with its epilogue ----------------------------------
     def linear_fwd(self, x, w, y, bias=None, activation=None, residual=None, z=None, x_scale=None, w_scale=None,

@@ -258,6 +258,8 @@ int launch_glr_step(const cpdr_ctx *c, const void *x, const float *g, const floa
 int glr_plan(const cpdr_ctx *c, int channels, bool backward, int32_t out[3]);
 // out[col] = sum over parts of part[:, col] (rmsnorm.cu).
 int launch_column_sums(const float *part, int nparts, int width, float *out, void *stream);
+// The same for two vectors side by side, part [nparts, 2 width]; out2 may be NULL.
+int launch_column_sums2(const float *part, int nparts, int width, float *out, float *out2, void *stream);
 // Matrix product with its epilogue (linear.cu).  dz: rows x N bf16 (where
 // there is an activation); part: linear_dz_parts() x N floats (for dbias).
 int launch_linear_fwd(const cpdr_ctx *c, int64_t rows, int K, int N, const void *x, const void *w, const float *x_scale,
@@ -273,6 +275,27 @@ int launch_rmsnorm_fwd(const cpdr_ctx *c, int64_t rows, int width, const void *x
 int rmsnorm_bwd_grid(const cpdr_ctx *c, int64_t rows, int width);
 int launch_rmsnorm_bwd(const cpdr_ctx *c, int64_t rows, int width, const void *s, const float *weight, float eps,
                        const void *dy, const void *dsum, void *ds, float *dweight, float *part, void *stream);
+// Layer norm (layernorm.cu); part: layernorm_bwd_grid() x 2 width floats.
+int launch_layernorm_fwd(const cpdr_ctx *c, int64_t rows, int width, const void *x, const void *residual,
+                         const float *weight, const float *bias, float eps, void *sum_out, void *y, void *y8,
+                         float *scale, void *stream);
+int layernorm_bwd_grid(const cpdr_ctx *c, int64_t rows, int width);
+int launch_layernorm_bwd(const cpdr_ctx *c, int64_t rows, int width, const void *s, const float *weight, float eps,
+                         const void *dy, const void *dsum, void *ds, float *dweight, float *dbias, float *part,
+                         void *stream);
+// Tokens over a pool of slots (token_step.cu).
+int launch_delta_step(const cpdr_ctx *c, const void *q, const void *k, const void *v, const void *beta, const float *g,
+                      const float *state, float *state_out, const int32_t *slots, int n, int num_slots, void *o,
+                      void *stream);
+int launch_conv1d_step(const cpdr_ctx *c, const void *x, const float *weight, const float *bias, const void *state,
+                       void *state_out, const int32_t *slots, int n, int num_slots, int channels, int activation, void *y,
+                       void *stream);
+// Embedding (embed.cu).
+int launch_embed_fwd(const cpdr_ctx *c, const int32_t *tokens, int64_t n, const void *table, int vocab, int width,
+                     float scale, void *y, void *stream);
+size_t embed_bwd_workspace(int64_t n, int width);
+int launch_embed_bwd(const cpdr_ctx *c, const int32_t *tokens, int64_t n, int vocab, int width, float scale,
+                     const void *dy, void *dtable, void *ws, void *stream);
 int launch_tc_fwd(const cpdr_ctx *c, const int32_t *items, int n_items, const void *q, const void *k, const void *v,
                   const float *g,
                   const void *wy, const float *S_init, void *o, float *final_state, void *stream);

@@ -1,5 +1,5 @@
 // C-ABI layer of the layer steps around the token mixers: the gated linear
-// recurrence, the RMS norm and the matrix product.  Argument validation and dispatch; contracts
+// recurrence, the norms, the matrix product, the embedding and the mixers' token steps.  Argument validation and dispatch; contracts
 // in include/cpdr.h.
 #include <cuda_runtime.h>
 
@@ -100,6 +100,33 @@ size_t linear_workspace(const cpdr_ctx *c, int64_t rows, int32_t N, int32_t act)
 
 size_t norm_workspace(const cpdr_ctx *c, int64_t rows, int width) {
     return (size_t)cpdr::rmsnorm_bwd_grid(c, rows, width) * (size_t)width * sizeof(float);
+}
+
+// dw's and db's rows of every block.
+size_t layernorm_workspace(const cpdr_ctx *c, int64_t rows, int width) {
+    return (size_t)cpdr::layernorm_bwd_grid(c, rows, width) * 2 * (size_t)width * sizeof(float);
+}
+
+// The arguments that every call over a pool of slots has.
+cpdr_status check_slots(const char *what, const int32_t *slots, int32_t n, int32_t num_slots) {
+    if (n < 0 || n > 65535) return fail_with(CPDR_ERR_INVALID, std::string(what) + ": n must be 0 .. 65535");
+    if (num_slots < 1) return fail_with(CPDR_ERR_INVALID, std::string(what) + ": num_slots must be positive");
+    if (!slots && n > num_slots)
+        return fail_with(CPDR_ERR_INVALID, std::string(what) + ": without slots, row i's state is slot i: n must be at most num_slots");
+    if (slots && ((uintptr_t)slots & 3u) != 0) return fail_with(CPDR_ERR_INVALID, std::string(what) + ": slots not 4-byte aligned");
+    return CPDR_OK;
+}
+
+cpdr_status check_embed(const char *what, const int32_t *tokens, int64_t n, int32_t vocab, int32_t width, float scale) {
+    if (n < 0 || n > (1 << 30)) return fail_with(CPDR_ERR_INVALID, std::string(what) + ": n must be 0 .. 2^30");
+    if (vocab < 1 || vocab > (1 << 30)) return fail_with(CPDR_ERR_INVALID, std::string(what) + ": vocab must be 1 .. 2^30");
+    if (width < 1 || width % 8 != 0)
+        return fail_with(CPDR_ERR_INVALID, std::string(what) + ": width must be a positive multiple of 8");
+    if (width > (1 << 20)) return fail_with(CPDR_ERR_UNSUPPORTED, std::string(what) + ": width is at most 2^20");
+    if (!(scale - scale == 0.f)) return fail_with(CPDR_ERR_INVALID, std::string(what) + ": scale must be finite");
+    if (n > 0 && !tokens) return fail_with(CPDR_ERR_INVALID, "null pointer: tokens");
+    if (((uintptr_t)tokens & 3u) != 0) return fail_with(CPDR_ERR_INVALID, std::string(what) + ": tokens not 4-byte aligned");
+    return CPDR_OK;
 }
 
 }  // namespace
@@ -240,6 +267,155 @@ cpdr_status cpdr_rmsnorm_bwd(const cpdr_ctx *c, int64_t rows, int32_t width, con
                            {{ds, dy}, {ds, dsum}}));
     return check_launched(cpdr::launch_rmsnorm_bwd(c, rows, width, s, weight, eps, dy, dsum, ds, dweight, (float *)ws, stream),
                           "cpdr_rmsnorm_bwd");
+}
+
+cpdr_status cpdr_layernorm_fwd(const cpdr_ctx *c, int64_t rows, int32_t width, const void *x, const void *residual,
+                               const float *weight, const float *bias, float eps, void *sum_out, void *y, void *y8,
+                               float *scale, void *stream) {
+    CPDR_TRY(check_launch_ctx(c));
+    CPDR_TRY(check_norm("cpdr_layernorm_fwd", rows, width, eps));
+    if (rows == 0) return CPDR_OK;
+    if (!y && !y8) return fail_with(CPDR_ERR_INVALID, "cpdr_layernorm_fwd: neither y nor y8 is given");
+    if ((y8 == nullptr) != (scale == nullptr))
+        return fail_with(CPDR_ERR_INVALID, "cpdr_layernorm_fwd: y8 and scale come together");
+    CPDR_TRY(check_device_ptr(x, "x"));
+    CPDR_TRY(check_device_ptr(residual, "residual", true));
+    CPDR_TRY(check_device_ptr(weight, "weight"));
+    CPDR_TRY(check_device_ptr(bias, "bias", true));
+    CPDR_TRY(check_device_ptr(sum_out, "sum_out", true));
+    CPDR_TRY(check_device_ptr(y, "y", true));
+    CPDR_TRY(check_device_ptr(y8, "y8", true));
+    CPDR_TRY(check_device_ptr(scale, "scale", true));
+    const size_t n = (size_t)rows * (size_t)width, es = elem_bytes(c), wb = (size_t)width * 4;
+    CPDR_TRY(check_outputs("cpdr_layernorm_fwd",
+                           {{sum_out, n * es, "sum_out"}, {y, n * es, "y"}, {y8, n, "y8"}, {scale, (size_t)rows * 4, "scale"}},
+                           {{x, n * es, "x"}, {residual, n * es, "residual"}, {weight, wb, "weight"}, {bias, wb, "bias"}},
+                           {{sum_out, x}, {sum_out, residual}, {y, x}, {y, residual}}));
+    return check_launched(
+        cpdr::launch_layernorm_fwd(c, rows, width, x, residual, weight, bias, eps, sum_out, y, y8, scale, stream),
+        "cpdr_layernorm_fwd");
+}
+
+cpdr_status cpdr_layernorm_bwd_workspace_bytes(const cpdr_ctx *c, int64_t rows, int32_t width, size_t *bytes) {
+    CPDR_TRY(check_launch_ctx(c));
+    if (!bytes) return fail_with(CPDR_ERR_INVALID, "null argument");
+    CPDR_TRY(check_norm("cpdr_layernorm_bwd_workspace_bytes", rows, width, 0.f));
+    *bytes = layernorm_workspace(c, rows, width);
+    return CPDR_OK;
+}
+
+cpdr_status cpdr_layernorm_bwd(const cpdr_ctx *c, int64_t rows, int32_t width, const void *s, const float *weight,
+                               float eps, const void *dy, const void *dsum, void *ds, float *dweight, float *dbias,
+                               void *ws, size_t ws_bytes, void *stream) {
+    CPDR_TRY(check_launch_ctx(c));
+    CPDR_TRY(check_norm("cpdr_layernorm_bwd", rows, width, eps));
+    CPDR_TRY(check_device_ptr(s, "s", rows == 0));
+    CPDR_TRY(check_device_ptr(weight, "weight"));
+    CPDR_TRY(check_device_ptr(dy, "dy", rows == 0));
+    CPDR_TRY(check_device_ptr(dsum, "dsum", true));
+    CPDR_TRY(check_device_ptr(ds, "ds", rows == 0));
+    CPDR_TRY(check_device_ptr(dweight, "dweight"));
+    CPDR_TRY(check_device_ptr(dbias, "dbias", true));
+    CPDR_TRY(check_device_ptr(ws, "workspace"));
+    const size_t n = (size_t)rows * (size_t)width, es = elem_bytes(c), wb = (size_t)width * 4;
+    const size_t need = layernorm_workspace(c, rows, width);
+    if (ws_bytes < need) return fail_with(CPDR_ERR_WORKSPACE, "cpdr_layernorm_bwd: workspace too small");
+    CPDR_TRY(check_outputs("cpdr_layernorm_bwd",
+                           {{ds, n * es, "ds"}, {dweight, wb, "dweight"}, {dbias, wb, "dbias"}, {ws, need, "workspace"}},
+                           {{s, n * es, "s"}, {weight, wb, "weight"}, {dy, n * es, "dy"}, {dsum, n * es, "dsum"}},
+                           {{ds, dy}, {ds, dsum}}));
+    return check_launched(
+        cpdr::launch_layernorm_bwd(c, rows, width, s, weight, eps, dy, dsum, ds, dweight, dbias, (float *)ws, stream),
+        "cpdr_layernorm_bwd");
+}
+
+cpdr_status cpdr_embed_fwd(const cpdr_ctx *c, const int32_t *tokens, int64_t n, const void *table, int32_t vocab,
+                           int32_t width, float scale, void *y, void *stream) {
+    CPDR_TRY(check_launch_ctx(c));
+    CPDR_TRY(check_embed("cpdr_embed_fwd", tokens, n, vocab, width, scale));
+    if (n == 0) return CPDR_OK;
+    CPDR_TRY(check_device_ptr(table, "table"));
+    CPDR_TRY(check_device_ptr(y, "y"));
+    const size_t row = (size_t)width * elem_bytes(c);
+    CPDR_TRY(check_outputs("cpdr_embed_fwd", {{y, (size_t)n * row, "y"}},
+                           {{tokens, (size_t)n * 4, "tokens"}, {table, (size_t)vocab * row, "table"}}));
+    return check_launched(cpdr::launch_embed_fwd(c, tokens, n, table, vocab, width, scale, y, stream), "cpdr_embed_fwd");
+}
+
+cpdr_status cpdr_embed_bwd_workspace_bytes(const cpdr_ctx *c, int64_t n, int32_t vocab, int32_t width, size_t *bytes) {
+    if (!c || !bytes) return fail_with(CPDR_ERR_INVALID, "null argument");
+    alignas(4) static const int32_t none = 0;
+    CPDR_TRY(check_embed("cpdr_embed_bwd_workspace_bytes", &none, n, vocab, width, 1.f));
+    *bytes = cpdr::embed_bwd_workspace(n, width);
+    return CPDR_OK;
+}
+
+cpdr_status cpdr_embed_bwd(const cpdr_ctx *c, const int32_t *tokens, int64_t n, int32_t vocab, int32_t width,
+                           float scale, const void *dy, void *dtable, void *ws, size_t ws_bytes, void *stream) {
+    CPDR_TRY(check_launch_ctx(c));
+    CPDR_TRY(check_embed("cpdr_embed_bwd", tokens, n, vocab, width, scale));
+    CPDR_TRY(check_device_ptr(dy, "dy", n == 0));
+    CPDR_TRY(check_device_ptr(dtable, "dtable"));
+    const size_t row = (size_t)width * elem_bytes(c), need = cpdr::embed_bwd_workspace(n, width);
+    CPDR_TRY(check_device_ptr(ws, "workspace", need == 0));
+    if (ws_bytes < need) return fail_with(CPDR_ERR_WORKSPACE, "cpdr_embed_bwd: workspace too small");
+    CPDR_TRY(check_outputs("cpdr_embed_bwd", {{dtable, (size_t)vocab * row, "dtable"}, {ws, need, "workspace"}},
+                           {{tokens, (size_t)n * 4, "tokens"}, {dy, (size_t)n * row, "dy"}}));
+    return check_launched(cpdr::launch_embed_bwd(c, tokens, n, vocab, width, scale, dy, dtable, ws, stream), "cpdr_embed_bwd");
+}
+
+cpdr_status cpdr_delta_step(const cpdr_ctx *c, const void *q, const void *k, const void *v, const void *beta,
+                            const float *gate, const float *state, float *state_out, const int32_t *slots, int32_t n,
+                            int32_t num_slots, void *o, void *stream) {
+    CPDR_TRY(check_launch_ctx(c));
+    CPDR_TRY(check_slots("cpdr_delta_step", slots, n, num_slots));
+    if (n == 0) return CPDR_OK;
+    CPDR_TRY(check_device_ptr(q, "q"));
+    CPDR_TRY(check_device_ptr(k, "k"));
+    CPDR_TRY(check_device_ptr(v, "v"));
+    CPDR_TRY(check_device_ptr(beta, "beta"));
+    CPDR_TRY(check_device_ptr(gate, "gate"));
+    CPDR_TRY(check_device_ptr(state, "state"));
+    CPDR_TRY(check_device_ptr(state_out, "state_out"));
+    CPDR_TRY(check_device_ptr(o, "o"));
+    const auto &pl = c->plan;
+    const size_t es = elem_bytes(c), hn = (size_t)n * (size_t)pl.H, d = (size_t)pl.dk;
+    const size_t hq = (size_t)n * (size_t)pl.Hq * d * es, st = (size_t)num_slots * (size_t)pl.H * d * d * 4;
+    CPDR_TRY(check_outputs("cpdr_delta_step", {{o, hq, "o"}, {state_out, st, "state_out"}},
+                           {{q, hq, "q"}, {k, hn * d * es, "k"}, {v, hn * d * es, "v"}, {beta, hn * es, "beta"},
+                            {gate, hn * (pl.gate_kind == CPDR_GATE_PER_DIM ? d : 1) * 4, "gate"}, {state, st, "state"},
+                            {slots, (size_t)n * 4, "slots"}},
+                           {{state_out, state}}));
+    return check_launched(cpdr::launch_delta_step(c, q, k, v, beta, gate, state, state_out, slots, n, num_slots, o, stream),
+                          "cpdr_delta_step");
+}
+
+cpdr_status cpdr_conv1d_step(const cpdr_ctx *c, const void *x, const float *weight, const float *bias,
+                             const void *state, void *state_out, const int32_t *slots, int32_t n, int32_t num_slots,
+                             int32_t channels, int32_t activation, void *y, void *stream) {
+    CPDR_TRY(check_launch_ctx(c));
+    const int W = c->plan.conv_width;
+    if (W == 0) return fail_with(CPDR_ERR_INVALID, "cpdr_conv1d_step: the context has no conv width");
+    CPDR_TRY(check_channels("cpdr_conv1d_step", channels));
+    if (activation != 0 && activation != 1)
+        return fail_with(CPDR_ERR_INVALID, "cpdr_conv1d_step: activation must be 0 (none) or 1 (SiLU)");
+    CPDR_TRY(check_slots("cpdr_conv1d_step", slots, n, num_slots));
+    if (n == 0) return CPDR_OK;
+    CPDR_TRY(check_device_ptr(x, "x"));
+    CPDR_TRY(check_device_ptr(weight, "weight"));
+    CPDR_TRY(check_device_ptr(bias, "bias", true));
+    CPDR_TRY(check_device_ptr(state, "state", W == 1));
+    CPDR_TRY(check_device_ptr(state_out, "state_out", W == 1));
+    CPDR_TRY(check_device_ptr(y, "y"));
+    const size_t ch = (size_t)channels, es = elem_bytes(c), e = (size_t)n * ch * es;
+    const size_t st = (size_t)num_slots * (size_t)(W - 1) * ch * es;
+    CPDR_TRY(check_outputs("cpdr_conv1d_step", {{y, e, "y"}, {state_out, st, "state_out"}},
+                           {{x, e, "x"}, {weight, ch * (size_t)W * 4, "weight"}, {bias, ch * 4, "bias"}, {state, st, "state"},
+                            {slots, (size_t)n * 4, "slots"}},
+                           {{state_out, state}}));
+    return check_launched(cpdr::launch_conv1d_step(c, x, weight, bias, state, state_out, slots, n, num_slots, channels,
+                                                   activation, y, stream),
+                          "cpdr_conv1d_step");
 }
 
 cpdr_status cpdr_plan_linear(const cpdr_ctx *c, int64_t rows, int32_t K, int32_t N, int32_t e4m3, int32_t out[2]) {

@@ -22,27 +22,20 @@
 // 4.5 beyond, and of fp32 5.9 to 6.7 up to 6144 columns and 4.6 to 5.6 beyond:
 // few wide rows are in flight in an SM.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 
 #include "cpdr_internal.hpp"
 #include "launch.cuh"
+#include "norm_rows.cuh"
 #include "vec_io.cuh"
 
 namespace cpdr {
 namespace {
 
 using namespace vio;
-
-constexpr float kE4m3Max = 448.f;
-
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
+using namespace norm;
 
 // Sum of `s` and combination of `m` (maximum, or sum) over the TPR threads
 // of a row; `sh` holds a pair per warp of the block, one half for each parity.
@@ -74,9 +67,6 @@ __device__ __forceinline__ float2 row_reduce(float s, float m, float2 *sh, int p
     }
     return make_float2(s, m);
 }
-
-template <int TPR>
-constexpr int kBlock = TPR < 256 ? 256 : TPR;
 
 struct FwdParams {
     const void *x, *res;
@@ -165,22 +155,7 @@ __global__ void __launch_bounds__(kBlock<TPR>, kFwdSlim<T, NV, RES> ? 1024 / TPR
 #pragma unroll
         for (int j = 0; j < V; j++) s[i][j] *= rstd;
         if (p.y) store16((T *)p.y + o + col, s[i]);
-        if (E4M3) {
-            uint32_t q[V / 4];
-#pragma unroll
-            for (int j = 0; j < V; j += 4) {
-                const uint32_t lo =
-                    __nv_cvt_float2_to_fp8x2(make_float2(s[i][j] * inv, s[i][j + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-                const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(s[i][j + 2] * inv, s[i][j + 3] * inv),
-                                                             __NV_SATFINITE, __NV_E4M3);
-                q[j / 4] = lo | hi << 16;
-            }
-            uint8_t *d = p.y8 + o + col;
-            if (V == 8)
-                *reinterpret_cast<uint2 *>(d) = make_uint2(q[0], q[V / 4 - 1]);
-            else
-                *reinterpret_cast<uint32_t *>(d) = q[0];
-        }
+        if (E4M3) store_e4m3(p.y8 + o + col, s[i], inv);
     }
 }
 
@@ -331,9 +306,9 @@ __global__ void __launch_bounds__(kBlock<TPR>, bwd_per_sm<T, TPR, NV>()) rmsnorm
 constexpr int kSumCols = 32, kSumRows = 16;
 
 // out[col] = sum of part[:, col], in a fixed order: 16 strided sums per
-// column, then those 16.
+// column, then those 16.  Columns from `split` on go to out2 (NULL: nowhere).
 __global__ void __launch_bounds__(kSumCols *kSumRows)
-column_sums_kernel(const float *part, int nparts, int width, float *out) {
+column_sums_kernel(const float *part, int nparts, int width, float *out, int split, float *out2) {
     __shared__ float sh[kSumRows][kSumCols + 1];
     next_grid_may_start();
     previous_grid_done();
@@ -348,7 +323,8 @@ column_sums_kernel(const float *part, int nparts, int width, float *out) {
         v = sh[0][cx];
 #pragma unroll
         for (int r = 1; r < kSumRows; r++) v += sh[r][cx];
-        out[col] = v;
+        if (col < split) out[col] = v;
+        else if (out2) out2[col - split] = v;
     }
 }
 
@@ -378,46 +354,6 @@ int bwd(const BwdParams &p, int grid, float *dw, cudaStream_t st) {
     return launch_column_sums(p.part, grid, p.width, dw, st);
 }
 
-template <int TPR, int NV, typename F>
-int with(F f) {
-    return f(std::integral_constant<int, TPR>(), std::integral_constant<int, NV>());
-}
-
-// Threads per row, and 16-byte vectors for each of them: groups of up to 256
-// threads with one or two vectors, three where two would leave a quarter of
-// the threads idle or more (bf16 rows of 264, forward 6.1 -> 7.0 TB/s and
-// backward 3.3 -> 5.1), and up to eight for wide rows.
-template <typename T, typename F>
-int narrow_row(int vecs, F f) {
-    if (vecs <= 1) return with<1, 1>(f);
-    if (vecs <= 2) return with<2, 1>(f);
-    if (vecs <= 4) return with<4, 1>(f);
-    if (vecs <= 8) return with<8, 1>(f);
-    if (vecs <= 12) return with<4, 3>(f);
-    if (vecs <= 16) return with<16, 1>(f);
-    if (vecs <= 24) return with<8, 3>(f);
-    if (vecs <= 32) return with<32, 1>(f);
-    if (vecs <= 48) return with<16, 3>(f);
-    if (vecs <= 64) return with<32, 2>(f);
-    if (vecs <= 96) return with<32, 3>(f);
-    if (vecs <= 128) return with<64, 2>(f);
-    if (vecs <= 192) return with<64, 3>(f);
-    if (vecs <= 256) return with<128, 2>(f);
-    if (vecs <= 384) return with<128, 3>(f);
-    if (vecs <= 512) return with<256, 2>(f);
-    return with<256, 3>(f);
-}
-template <typename T, typename F>
-int by_width(int width, F f) {
-    const int vecs = (width + kVecOf<T> - 1) / kVecOf<T>;
-    if (vecs <= 768) return narrow_row<T>(vecs, f);
-    if (vecs <= 1024) return with<256, 4>(f);
-    if (vecs <= 1536) return with<256, 6>(f);
-    if constexpr (kVecOf<T> == 4) {
-        if (vecs > 2048) return with<512, 8>(f);
-    }
-    return with<256, 8>(f);
-}
 // The same for the backward, whose thread holds dw besides: 512 threads a row
 // where the eight values of a bf16 vector, or eight vectors, would take too
 // many registers (fp32 rows of 6144 run at 6.6 TB/s as 256 x 6, at 4.9 as
@@ -462,7 +398,12 @@ static_assert(kMaxNormWidth <= 512 * 8 * kVecOf<float> && kMaxNormWidth <= 512 *
 
 int launch_column_sums(const float *part, int nparts, int width, float *out, void *stream) {
     return launch_early(column_sums_kernel, dim3((unsigned)((width + kSumCols - 1) / kSumCols)), kSumCols * kSumRows, 0, 1, stream,
-                        part, nparts, width, out);
+                        part, nparts, width, out, width, (float *)nullptr);
+}
+
+int launch_column_sums2(const float *part, int nparts, int width, float *out, float *out2, void *stream) {
+    return launch_early(column_sums_kernel, dim3((unsigned)((2 * width + kSumCols - 1) / kSumCols)), kSumCols * kSumRows, 0, 1,
+                        stream, part, nparts, 2 * width, out, width, out2);
 }
 
 int launch_rmsnorm_fwd(const cpdr_ctx *c, int64_t rows, int width, const void *x, const void *residual,

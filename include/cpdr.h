@@ -416,6 +416,94 @@ cpdr_status cpdr_rmsnorm_bwd(const cpdr_ctx *ctx, int64_t rows, int32_t width, c
                              size_t workspace_bytes, void *stream);
 
 /*
+ * Layer norm with the residual's addition.  Per row of `width` elements, with
+ * s = x + residual (s = x when residual is NULL) and m = mean(s),
+ *     y_i = (s_i - m) weight_i / sqrt(mean((s - m)^2) + eps) + bias_i.
+ * As cpdr_rmsnorm_fwd in all else: types, sum_out, the 8-bit output with its
+ * scales, the in-place forms, sizes and |s|; weight [width] and bias [width]
+ * fp32, bias or NULL.  With eps = 0 a row without variance has no value.
+ */
+cpdr_status cpdr_layernorm_fwd(const cpdr_ctx *ctx, int64_t rows, int32_t width, const void *x, const void *residual,
+                               const float *weight, const float *bias, float eps, void *sum_out, void *y, void *y8,
+                               float *scale, void *stream);
+
+/*
+ * Its backward, from s (sum_out, or x where there was no residual), dy and,
+ * unless NULL, the gradient dsum that reaches s past the norm: with
+ * rstd = 1/sqrt(mean((s - m)^2) + eps), xh = (s - m) rstd and u = weight dy,
+ *     ds_i = rstd (u_i - mean(u) - xh_i mean(u xh)) + dsum_i,
+ *     dweight_i = sum over rows of dy_i xh_i,   dbias_i = sum over rows of dy_i.
+ * ds is the gradient of x and of residual alike; it may be dy or dsum (in
+ * place).  dy, dsum, ds [rows, width] in the input dtype; dweight and dbias
+ * [width] fp32, dbias or NULL.  workspace: cpdr_layernorm_bwd_workspace_bytes()
+ * bytes, 16-byte aligned.
+ */
+cpdr_status cpdr_layernorm_bwd_workspace_bytes(const cpdr_ctx *ctx, int64_t rows, int32_t width, size_t *bytes);
+cpdr_status cpdr_layernorm_bwd(const cpdr_ctx *ctx, int64_t rows, int32_t width, const void *s, const float *weight,
+                               float eps, const void *dy, const void *dsum, void *ds, float *dweight, float *dbias,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Embedding lookup with scaling:  y_i = scale table[tokens_i].
+ * tokens [n] int32 (4-byte aligned); table [vocab, width] and y [n, width] in
+ * the context's input dtype; a row whose token lies outside 0 .. vocab - 1
+ * (padding, -1) is zero.  scale is finite; y is rounded once.
+ * 0 <= n <= 2^30; 1 <= vocab <= 2^30; width % 8 == 0, at most 2^20.
+ */
+cpdr_status cpdr_embed_fwd(const cpdr_ctx *ctx, const int32_t *tokens, int64_t n, const void *table, int32_t vocab,
+                           int32_t width, float scale, void *y, void *stream);
+
+/*
+ * Its gradient:  dtable_v = scale times the sum over the rows with tokens_i = v
+ * of dy_i.  The whole of dtable [vocab, width] is written, zeros where v does
+ * not occur; rows whose token lies outside the table add nothing.  dy [n,
+ * width] and dtable in the input dtype; sums in fp32, rounded once.  A token's
+ * rows are added in the order of the batch, in groups that depend on the
+ * tokens alone.  workspace: cpdr_embed_bwd_workspace_bytes() bytes, 16-byte
+ * aligned.
+ */
+cpdr_status cpdr_embed_bwd_workspace_bytes(const cpdr_ctx *ctx, int64_t n, int32_t vocab, int32_t width, size_t *bytes);
+cpdr_status cpdr_embed_bwd(const cpdr_ctx *ctx, const int32_t *tokens, int64_t n, int32_t vocab, int32_t width,
+                           float scale, const void *dy, void *dtable, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/*
+ * The gated delta rule token by token, its serving form, over a pool of state
+ * slots: row i of q [n, Hq, dk], k [n, H, dk], v [n, H, dv], beta [n, H], gate
+ * ([n, H] or [n, H, dk]) and o [n, Hq, dv] is the next token of the sequence
+ * whose states are slot slots[i] (int32, device; NULL: slot i) of state
+ * [num_slots, H, dk, dv] fp32 ([.., dv, dk] with CPDR_FLAG_STATE_V_FIRST): what
+ * cpdr_fwd leaves in final_state, and goes on from.  Per state head,
+ *     S <- (I - beta k k^T) Diag(alpha) S + beta k v^T,   o = scale S^T q,
+ * alpha = exp(gate) (-infinity: the state is dropped).  Heads, dims, gate kind,
+ * input dtype, scale and state layout are the context's; its sequences and
+ * segments play no part.  state_out gets the new states of the slots that
+ * occur; it may be state itself (in place), and its other slots are left as
+ * they were.  Rows whose slot is outside 0 .. num_slots - 1 (padding, -1) do
+ * nothing: their o is left as it was.  Rows of the same slot are consecutive
+ * tokens of its sequence, in row order; its states stay on the chip between
+ * them.  0 <= n <= 65535.  States and sums are fp32, o is rounded once.
+ */
+cpdr_status cpdr_delta_step(const cpdr_ctx *ctx, const void *q, const void *k, const void *v, const void *beta,
+                            const float *gate, const float *state, float *state_out, const int32_t *slots, int32_t n,
+                            int32_t num_slots, void *o, void *stream);
+
+/*
+ * The causal conv1d token by token, over a pool of windows: row i of x and y
+ * [n, channels] is the next token of the sequence whose last W - 1 inputs,
+ * oldest first (zeros before its start), are slot slots[i] of state
+ * [num_slots, W - 1, channels] in the input dtype,
+ *     y = act( bias + sum_{i<W-1} weight[c, i] state[i, c] + weight[c, W-1] x[c] ),
+ * and the window moves on by one.  weight, bias, activation and W =
+ * desc.conv_width as for cpdr_conv1d_fwd; slots, state_out, n and rows without
+ * a slot as for cpdr_delta_step.  With W = 1 there is no state: state and
+ * state_out may be NULL.  channels % 8 == 0, at most 2^24.
+ */
+cpdr_status cpdr_conv1d_step(const cpdr_ctx *ctx, const void *x, const float *weight, const float *bias,
+                             const void *state, void *state_out, const int32_t *slots, int32_t n, int32_t num_slots,
+                             int32_t channels, int32_t activation, void *y, void *stream);
+
+/*
  * Matrix product with bias, activation and residual in its epilogue:
  *     z = x w^T + bias,   y = act(z) + residual,
  * x [rows, K], w [N, K], y and residual [rows, N], z [rows, N] or NULL (the
