@@ -27,37 +27,94 @@ using namespace vio;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 
+// A block's share of a matrix: `rows` rows from row0 on and `cols` 16-byte
+// vectors of each from col0 on, which the threads walk through row by row.
+struct Share {
+    int64_t row0;
+    int rows, col0, cols;
+};
+struct Split {
+    int per_block;   // rows of a block
+    int cols;        // vectors of a block
+};
+constexpr int kColVecs = 1024;   // vectors of a row in one block, at most
+
+__device__ __forceinline__ Share share_of(const Split &s, int64_t rows, int vecs) {
+    Share h;
+    h.row0 = (int64_t)blockIdx.x * s.per_block;
+    h.rows = (int)min((int64_t)s.per_block, rows - h.row0);
+    h.col0 = blockIdx.y * s.cols;
+    h.cols = min(s.cols, vecs - h.col0);
+    return h;
+}
+
+// This thread's vectors of a share: (row, col) and how far the next one is.
+struct Walk {
+    int row, col, step_row, step_col, cols;
+    __device__ __forceinline__ explicit Walk(const Share &h)
+        : row(threadIdx.x / h.cols), col(threadIdx.x % h.cols), step_row(kThreads / h.cols), step_col(kThreads % h.cols),
+          cols(h.cols) {}
+    __device__ __forceinline__ void next() {
+        row += step_row;
+        col += step_col;
+        if (col >= cols) {
+            col -= cols;
+            row++;
+        }
+    }
+};
+
+constexpr int kAhead = 4;   // vectors of a thread in flight
+
 // ------------------------------------------------------------------ lookup
-// grid (rows, blocks of columns)
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-embed_fwd_kernel(const int32_t *tokens, const T *table, int vocab, int width, float scale, T *y) {
+embed_fwd_kernel(const int32_t *tokens, int64_t n, const T *table, int vocab, int width, float scale, T *y, Split split) {
     constexpr int V = kVecOf<T>;
     next_grid_may_start();
     previous_grid_done();
-    const int64_t row = blockIdx.x;
-    const int col = (blockIdx.y * kThreads + threadIdx.x) * V;
-    if (col >= width) return;
-    const int token = tokens[row];
-    float x[V];
-    widen16((uint32_t)token < (uint32_t)vocab ? load16(table + (int64_t)token * width + col) : make_uint4(0, 0, 0, 0), x);
+    const Share h = share_of(split, n, width / V);
+    Walk w(h);
+    while (w.row < h.rows) {
+        int64_t to[kAhead];
+        uint4 x[kAhead];
 #pragma unroll
-    for (int j = 0; j < V; j++) x[j] *= scale;
-    store16(y + row * width + col, x);
+        for (int u = 0; u < kAhead; u++, w.next()) {
+            to[u] = -1;
+            x[u] = make_uint4(0, 0, 0, 0);
+            if (w.row >= h.rows) continue;
+            const int64_t row = h.row0 + w.row;
+            const int col = (h.col0 + w.col) * V, token = tokens[row];
+            to[u] = row * width + col;
+            if ((uint32_t)token < (uint32_t)vocab) x[u] = load16(table + (int64_t)token * width + col);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; u++) {
+            if (to[u] < 0) continue;
+            float f[V];
+            widen16(x[u], f);
+#pragma unroll
+            for (int j = 0; j < V; j++) f[j] *= scale;
+            store16(y + to[u], f);
+        }
+    }
 }
 
 // ------------------------------------------------------------------ sort
-// One pass orders the pairs (key, position) by kBits bits of the key: blocks
-// count the digits of their tiles, one block turns the counts into places,
-// and every block moves its pairs, each warp its own stretch of the tile.
-constexpr int kBits = 8, kBins = 1 << kBits;
-constexpr int kPerLane = 8, kTile = kThreads * kPerLane;
+// One pass orders the pairs (key, position) by up to kMaxBits bits of the key:
+// blocks count the digits of their tiles, then every block finds the places of
+// its own from all counts and moves its pairs, each warp its own stretch.
+constexpr int kMaxBits = 10, kMaxBins = 1 << kMaxBits;
+constexpr int kPerLane = 8, kSub = kThreads * kPerLane;   // pairs that a block ranks at once
+constexpr int kMaxTiles = 128;
+static_assert(kSub <= 65536, "a few pairs' positions fit 16 bits");
+constexpr int kOwnBins = kMaxBins / kThreads;              // digits that a thread adds up
 
 struct Pass {
     const int32_t *key, *pos;   // pos NULL: the first pass, whose keys are tokens
     int32_t *key_out, *pos_out;
-    int32_t *counts;            // [kBins][tiles]
-    int n, tiles, vocab, shift;
+    int32_t *counts;            // [tiles][bins]
+    int n, tile, tiles, vocab, shift, bits;
 };
 
 // The key of pair i: its token, or vocab (behind all others) where it lies outside the table.
@@ -66,53 +123,29 @@ __device__ __forceinline__ int key_of(const Pass &p, int i) {
     return p.pos ? k : (uint32_t)k < (uint32_t)p.vocab ? k : p.vocab;
 }
 
-// Counts of each warp's digits in `hist`, and of this lane's pairs before it: in[u].
-__device__ __forceinline__ void rank_tile(const Pass &p, int (*hist)[kBins], int (&key)[kPerLane], int (&rank)[kPerLane]) {
+__device__ __forceinline__ void clear(int *x, int n) {
+    for (int i = threadIdx.x; i < n; i += kThreads) x[i] = 0;
+}
+
+// The ranks of kSub keys (-1: none) among those of their warp with the same
+// digit, and in hist[warp][digit] how many there are.
+__device__ __forceinline__ void rank_keys(const int (&key)[kPerLane], int (&rank)[kPerLane], int (*hist)[kMaxBins], int shift, int bits) {
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int i = threadIdx.x; i < kWarps * kBins; i += kThreads) (&hist[0][0])[i] = 0;
-    __syncthreads();
-    const int first = blockIdx.x * kTile + w * 32 * kPerLane + lane;
-#pragma unroll
-    for (int u = 0; u < kPerLane; u++) key[u] = first + 32 * u < p.n ? key_of(p, first + 32 * u) : -1;
 #pragma unroll
     for (int u = 0; u < kPerLane; u++) {
-        const int digit = key[u] < 0 ? -1 : (key[u] >> p.shift) & (kBins - 1);
+        const int digit = key[u] < 0 ? -1 : (key[u] >> shift) & ((1 << bits) - 1);
         const uint32_t same = __match_any_sync(0xffffffffu, digit);
-        const int before = digit < 0 ? 0 : hist[w][digit];
-        rank[u] = before + __popc(same & ((1u << lane) - 1));
+        rank[u] = digit < 0 ? 0 : hist[w][digit] + __popc(same & ((1u << lane) - 1));
         __syncwarp();
         if (digit >= 0 && lane == 31 - __clz(same)) hist[w][digit] = rank[u] + 1;
         __syncwarp();
     }
-    __syncthreads();
 }
 
-__global__ void __launch_bounds__(kThreads) digit_counts_kernel(Pass p) {
-    __shared__ int hist[kWarps][kBins];
-    next_grid_may_start();
-    previous_grid_done();
-    int key[kPerLane], rank[kPerLane];
-    rank_tile(p, hist, key, rank);
-    for (int d = threadIdx.x; d < kBins; d += kThreads) {
-        int sum = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; w++) sum += hist[w][d];
-        p.counts[(int64_t)d * p.tiles + blockIdx.x] = sum;
-    }
-}
-
-constexpr int kScanThreads = 1024;
-
-// counts[i] <- sum of counts before i: one block, each thread a stretch of its own.
-__global__ void __launch_bounds__(kScanThreads) places_kernel(int32_t *counts, int total) {
-    __shared__ int sums[32];
-    next_grid_may_start();
-    previous_grid_done();
-    const int per = (total + kScanThreads - 1) / kScanThreads, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int a = min(total, (int)threadIdx.x * per), b = min(total, a + per);
-    int sum = 0;
-    for (int i = a; i < b; i++) sum += counts[i];
-    int x = sum;
+// v becomes the sum of the values of the threads before this one.
+__device__ __forceinline__ int sum_before(int v, int *sums) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    int x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -120,193 +153,426 @@ __global__ void __launch_bounds__(kScanThreads) places_kernel(int32_t *counts, i
     }
     if (lane == 31) sums[w] = x;
     __syncthreads();
-    if (w == 0) {
-        int s = sums[lane];
+    int before = x - v;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += y;
+    for (int i = 0; i < kWarps; i++)
+        if (i < w) before += sums[i];
+    return before;
+}
+
+__global__ void __launch_bounds__(kThreads) digit_counts_kernel(Pass p) {
+    __shared__ int hist[kMaxBins];
+    next_grid_may_start();
+    clear(hist, 1 << p.bits);
+    __syncthreads();
+    previous_grid_done();
+    const int a = blockIdx.x * p.tile, b = min(p.n, a + p.tile);
+    for (int i0 = a; i0 < b; i0 += kSub) {
+        int key[kPerLane];
+#pragma unroll
+        for (int u = 0; u < kPerLane; u++) {
+            const int i = i0 + u * kThreads + threadIdx.x;
+            key[u] = i < b ? key_of(p, i) : -1;
         }
-        sums[lane] = s;
+#pragma unroll
+        for (int u = 0; u < kPerLane; u++)
+            if (key[u] >= 0) atomicAdd(&hist[(key[u] >> p.shift) & ((1 << p.bits) - 1)], 1);   // a count has no order
     }
     __syncthreads();
-    int before = x - sum + (w ? sums[w - 1] : 0);
-    for (int i = a; i < b; i++) {
-        const int c = counts[i];
-        counts[i] = before;
-        before += c;
-    }
+    for (int d = threadIdx.x; d < 1 << p.bits; d += kThreads) p.counts[((int64_t)blockIdx.x << p.bits) + d] = hist[d];
 }
 
 __global__ void __launch_bounds__(kThreads) move_pairs_kernel(Pass p) {
-    __shared__ int hist[kWarps][kBins];
+    __shared__ int hist[kWarps][kMaxBins];
+    __shared__ int place[kMaxBins];
+    __shared__ int sums[kWarps];
     next_grid_may_start();
     previous_grid_done();
-    int key[kPerLane], rank[kPerLane];
-    rank_tile(p, hist, key, rank);
-    // from counts of each warp to the place of its first pair of each digit
-    for (int d = threadIdx.x; d < kBins; d += kThreads) {
-        int place = p.counts[(int64_t)d * p.tiles + blockIdx.x];
-        for (int w = 0; w < kWarps; w++) {
-            const int c = hist[w][d];
-            hist[w][d] = place;
-            place += c;
+    // where this block's pairs of each digit go: behind all smaller digits and the blocks before
+    const int bins = 1 << p.bits;
+    {
+        int all[kOwnBins], mine[kOwnBins], total = 0;
+#pragma unroll
+        for (int x = 0; x < kOwnBins; x++) {
+            all[x] = mine[x] = 0;
+            const int d = threadIdx.x * kOwnBins + x;
+            if (d < bins) {
+#pragma unroll 8
+                for (int t = 0; t < p.tiles; t++) {
+                    const int c = p.counts[((int64_t)t << p.bits) + d];
+                    all[x] += c;
+                    if (t < (int)blockIdx.x) mine[x] += c;
+                }
+            }
+            total += all[x];
+        }
+        int before = sum_before(total, sums);
+#pragma unroll
+        for (int x = 0; x < kOwnBins; x++) {
+            const int d = threadIdx.x * kOwnBins + x;
+            if (d < bins) place[d] = before + mine[x];
+            before += all[x];
         }
     }
-    __syncthreads();
-    const int w = threadIdx.x >> 5, first = blockIdx.x * kTile + w * 32 * kPerLane + (threadIdx.x & 31);
+    const int a = blockIdx.x * p.tile, b = min(p.n, a + p.tile);
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int i0 = a; i0 < b; i0 += kSub) {
+        int key[kPerLane], rank[kPerLane];
+        const int first = i0 + w * 32 * kPerLane + lane;
+#pragma unroll
+        for (int u = 0; u < kPerLane; u++) key[u] = first + 32 * u < b ? key_of(p, first + 32 * u) : -1;
+        clear(&hist[0][0], kWarps * kMaxBins);
+        __syncthreads();
+        rank_keys(key, rank, hist, p.shift, p.bits);
+        __syncthreads();
+        for (int d = threadIdx.x; d < bins; d += kThreads) {
+            int at = place[d];
+#pragma unroll
+            for (int x = 0; x < kWarps; x++) {
+                const int c = hist[x][d];
+                hist[x][d] = at;
+                at += c;
+            }
+            place[d] = at;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kPerLane; u++) {
+            const int i = first + 32 * u;
+            if (i >= b) continue;
+            const int at = hist[w][(key[u] >> p.shift) & (bins - 1)] + rank[u];
+            p.key_out[at] = key[u];
+            p.pos_out[at] = p.pos ? p.pos[i] : i;
+        }
+        __syncthreads();
+    }
+}
+
+// All passes over at most kSub pairs, by one block.
+__global__ void __launch_bounds__(kThreads) sort_few_kernel(Pass p, int passes) {
+    __shared__ int hist[kWarps][kMaxBins];
+    __shared__ int sums[kWarps];
+    __shared__ int keys[kSub];
+    __shared__ uint16_t places[kSub];   // positions: below kSub
+    next_grid_may_start();
+    previous_grid_done();
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, first = w * 32 * kPerLane + lane, bins = 1 << p.bits;
+    int key[kPerLane], pos[kPerLane], rank[kPerLane];
 #pragma unroll
     for (int u = 0; u < kPerLane; u++) {
-        const int i = first + 32 * u;
-        if (i >= p.n) continue;
-        const int at = hist[w][(key[u] >> p.shift) & (kBins - 1)] + rank[u];
-        p.key_out[at] = key[u];
-        p.pos_out[at] = p.pos ? p.pos[i] : i;
+        pos[u] = first + 32 * u;
+        key[u] = pos[u] < p.n ? key_of(p, pos[u]) : -1;
+    }
+    for (int i = 0; i < passes; i++) {
+        const int shift = i * p.bits;
+        clear(&hist[0][0], kWarps * kMaxBins);
+        __syncthreads();
+        rank_keys(key, rank, hist, shift, p.bits);
+        __syncthreads();
+        int total = 0;
+#pragma unroll
+        for (int x = 0; x < kOwnBins; x++)
+#pragma unroll
+            for (int y = 0; y < kWarps; y++) total += hist[y][threadIdx.x * kOwnBins + x];
+        int at = sum_before(total, sums);
+#pragma unroll
+        for (int x = 0; x < kOwnBins; x++)
+#pragma unroll
+            for (int y = 0; y < kWarps; y++) {
+                int &c = hist[y][threadIdx.x * kOwnBins + x];
+                const int here = c;
+                c = at;
+                at += here;
+            }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kPerLane; u++)
+            if (key[u] >= 0) {
+                const int to = hist[w][(key[u] >> shift) & (bins - 1)] + rank[u];
+                keys[to] = key[u];
+                places[to] = (uint16_t)pos[u];
+            }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kPerLane; u++) {
+            const int j = first + 32 * u;
+            key[u] = j < p.n ? keys[j] : -1;
+            pos[u] = j < p.n ? places[j] : 0;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kPerLane; u++) {
+        const int j = first + 32 * u;
+        if (j < p.n) {
+            p.key_out[j] = key[u];
+            p.pos_out[j] = pos[u];
+        }
     }
 }
 
 // ------------------------------------------------------------------ sums
-constexpr int kRun = 64;   // sorted pairs that are summed ahead where they hold one token
+constexpr int kRun = 64;   // sorted pairs, or sums of such, that are summed ahead where they hold one token
 
 struct Sums {
     const int32_t *key, *pos;   // sorted
     const void *dy;
     void *dtable;
-    float *part;                // [n / kRun, width]
+    float *part, *part2;        // sums of whole runs of kRun pairs, and of kRun such runs: [.., width]
     int n, vocab, width;
     float scale;
+    Split split;
 };
+
+template <int V>
+__device__ __forceinline__ void add(float (&acc)[V], const uint4 &raw) {
+    float x[V];
+    widen16(raw, x);
+#pragma unroll
+    for (int j = 0; j < V; j++) acc[j] += x[j];
+}
 
 // acc += rows pos[a .. b) of dy, from column col on
 template <typename T, int V>
 __device__ __forceinline__ void add_rows(const Sums &p, int a, int b, int col, float (&acc)[V]) {
-    const T *dy = (const T *)p.dy;
-    for (int i = a; i < b; i++) {
-        float x[V];
-        widen16(load16(dy + (int64_t)p.pos[i] * p.width + col), x);
+    const T *dy = (const T *)p.dy + col;
+    for (; a < b; a += kAhead) {
+        uint4 x[kAhead];
 #pragma unroll
-        for (int j = 0; j < V; j++) acc[j] += x[j];
+        for (int u = 0; u < kAhead; u++)
+            x[u] = a + u < b ? load16(dy + (int64_t)p.pos[a + u] * p.width) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int u = 0; u < kAhead; u++) add<V>(acc, x[u]);
     }
 }
 
-// grid (whole runs of kRun pairs, blocks of columns)
-template <typename T>
+// acc += rows a .. b - 1 of part, from column col on
+template <int V>
+__device__ __forceinline__ void add_sums(const float *part, int width, int a, int b, int col, float (&acc)[V]) {
+    part += (int64_t)a * width + col;
+    for (; a < b; a += kAhead, part += (int64_t)kAhead * width) {
+        float4 x[kAhead][V / 4];
+#pragma unroll
+        for (int u = 0; u < kAhead; u++)
+#pragma unroll
+            for (int j = 0; j < V / 4; j++)
+                x[u][j] = a + u < b ? *reinterpret_cast<const float4 *>(part + (int64_t)u * width + 4 * j)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int u = 0; u < kAhead; u++)
+#pragma unroll
+            for (int j = 0; j < V / 4; j++) {
+                acc[4 * j] += x[u][j].x;
+                acc[4 * j + 1] += x[u][j].y;
+                acc[4 * j + 2] += x[u][j].z;
+                acc[4 * j + 3] += x[u][j].w;
+            }
+    }
+}
+
+// SECOND: of kRun runs' sums.  grid (whole runs, blocks of columns)
+template <typename T, bool SECOND>
 __global__ void __launch_bounds__(kThreads) run_sums_kernel(Sums p) {
-    constexpr int V = kVecOf<T>;
+    constexpr int V = kVecOf<T>, LEN = SECOND ? kRun * kRun : kRun;
     next_grid_may_start();
     previous_grid_done();
-    const int a = blockIdx.x * kRun, col = (blockIdx.y * kThreads + threadIdx.x) * V;
+    const int a = blockIdx.x * LEN, col = (blockIdx.y * kThreads + threadIdx.x) * V;
     const int k = p.key[a];
-    if (k != p.key[a + kRun - 1] || k >= p.vocab || col >= p.width) return;
+    if (k != p.key[a + LEN - 1] || k >= p.vocab || col >= p.width) return;
     float acc[V];
 #pragma unroll
     for (int j = 0; j < V; j++) acc[j] = 0.f;
-    add_rows<T>(p, a, a + kRun, col, acc);
+    if (SECOND) add_sums<V>(p.part, p.width, a / kRun, a / kRun + kRun, col, acc);
+    else add_rows<T, V>(p, a, a + LEN, col, acc);
+    float *to = (SECOND ? p.part2 : p.part) + (int64_t)blockIdx.x * p.width + col;
 #pragma unroll
-    for (int j = 0; j < V; j += 4)
-        *reinterpret_cast<float4 *>(p.part + (int64_t)blockIdx.x * p.width + col + j) =
-            make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+    for (int j = 0; j < V; j += 4) *reinterpret_cast<float4 *>(to + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
 }
 
-// The first pair whose key is not below k.
+// The whole warp calls it: the first pair whose key is not below k.
 __device__ __forceinline__ int lower_bound(const int32_t *key, int n, int k) {
-    int a = 0, b = n;
-    while (a < b) {
-        const int m = (int)(((int64_t)a + b) / 2);
-        if (key[m] < k) a = m + 1;
-        else b = m;
+    const int lane = threadIdx.x & 31;
+    int a = 0, len = n;   // it lies in a .. a + len
+    while (len > 32) {
+        const int step = len / 33, at = a + (lane + 1) * step;   // the last one: a + 32 (len / 33) < a + len
+        const int below = __popc(__ballot_sync(0xffffffffu, key[at] < k));
+        const int end = below < 32 ? a + (below + 1) * step : a + len;
+        if (below) a += below * step + 1;
+        len = end - a;
     }
-    return a;
+    return a + __popc(__ballot_sync(0xffffffffu, lane < len && key[a + (lane < len ? lane : 0)] < k));
 }
 
-constexpr int kTableRows = 16;   // table rows of a block
+constexpr int kTableRows = 256;   // table rows of a block, at most
 
-// grid (blocks of table rows, blocks of columns)
+// acc += the sum of pairs a .. b - 1 of the sorted list, which hold one token
+template <typename T, int V>
+__device__ __forceinline__ void add_pairs(const Sums &p, int a, int b, int col, float (&acc)[V]) {
+    const int c0 = (a + kRun - 1) / kRun, c1 = b / kRun;   // whole runs
+    if (c0 >= c1) {
+        add_rows<T, V>(p, a, b, col, acc);
+        return;
+    }
+    add_rows<T, V>(p, a, c0 * kRun, col, acc);
+    const int d0 = (c0 + kRun - 1) / kRun, d1 = c1 / kRun;
+    if (d0 >= d1) {
+        add_sums<V>(p.part, p.width, c0, c1, col, acc);
+    } else {
+        add_sums<V>(p.part, p.width, c0, d0 * kRun, col, acc);
+        add_sums<V>(p.part2, p.width, d0, d1, col, acc);
+        add_sums<V>(p.part, p.width, d1 * kRun, c1, col, acc);
+    }
+    add_rows<T, V>(p, c1 * kRun, b, col, acc);
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads) table_rows_kernel(Sums p) {
     constexpr int V = kVecOf<T>;
-    __shared__ int start[kTableRows + 1];
+    __shared__ int first[kTableRows], last[kTableRows], ends[2];   // pairs of each row: first .. last - 1
     next_grid_may_start();
     previous_grid_done();
-    const int v0 = blockIdx.x * kTableRows, rows = min(kTableRows, p.vocab - v0);
-    if (threadIdx.x <= rows) start[threadIdx.x] = lower_bound(p.key, p.n, v0 + threadIdx.x);
+    const Share h = share_of(p.split, p.vocab, p.width / V);
+    for (int r = threadIdx.x; r < h.rows; r += kThreads) first[r] = last[r] = 0;
+    if (threadIdx.x < 64) {
+        const int w = threadIdx.x >> 5, e = lower_bound(p.key, p.n, (int)h.row0 + (w ? h.rows : 0));
+        if ((threadIdx.x & 31) == 0) ends[w] = e;
+    }
     __syncthreads();
-    const int col = (blockIdx.y * kThreads + threadIdx.x) * V;
-    if (col >= p.width) return;
-    for (int r = 0; r < rows; r++) {
-        const int a = start[r], b = start[r + 1];
-        // whole runs c0 .. c1 - 1 of this token, if any
-        const int c0 = (a + kRun - 1) / kRun, c1 = b / kRun;
-        float acc[V];
+    const int a = ends[0], b = ends[1];
+    for (int i = a + threadIdx.x; i < b; i += kThreads) {
+        const int k = p.key[i], r = k - (int)h.row0;
+        if (i == a || p.key[i - 1] != k) first[r] = i;
+        if (i == b - 1 || p.key[i + 1] != k) last[r] = i + 1;
+    }
+    __syncthreads();
+    Walk w(h);
+    while (w.row < h.rows) {
+        int row[kAhead], col[kAhead];
+        uint4 x[kAhead];
 #pragma unroll
-        for (int j = 0; j < V; j++) acc[j] = 0.f;
-        if (c0 >= c1) {
-            add_rows<T>(p, a, b, col, acc);
-        } else {
-            add_rows<T>(p, a, c0 * kRun, col, acc);
-            for (int c = c0; c < c1; c++)
-#pragma unroll
-                for (int j = 0; j < V; j += 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(p.part + (int64_t)c * p.width + col + j);
-                    acc[j] += x.x;
-                    acc[j + 1] += x.y;
-                    acc[j + 2] += x.z;
-                    acc[j + 3] += x.w;
-                }
-            add_rows<T>(p, c1 * kRun, b, col, acc);
+        for (int u = 0; u < kAhead; u++, w.next()) {
+            row[u] = w.row;
+            col[u] = (h.col0 + w.col) * V;
+            x[u] = make_uint4(0, 0, 0, 0);
+            if (row[u] < h.rows && last[row[u]] != 0)
+                x[u] = load16((const T *)p.dy + (int64_t)p.pos[first[row[u]]] * p.width + col[u]);
         }
 #pragma unroll
-        for (int j = 0; j < V; j++) acc[j] *= p.scale;
-        store16((T *)p.dtable + (int64_t)(v0 + r) * p.width + col, acc);
+        for (int u = 0; u < kAhead; u++) {
+            if (row[u] >= h.rows) continue;
+            const int i = first[row[u]], e = last[row[u]];
+            float acc[V];
+            widen16(x[u], acc);
+            if (e > i + 1) {
+                // whole runs start at the first pair: it is not taken by itself
+                if (e - i >= kRun) {
+#pragma unroll
+                    for (int j = 0; j < V; j++) acc[j] = 0.f;
+                    add_pairs<T, V>(p, i, e, col[u], acc);
+                } else {
+                    add_rows<T, V>(p, i + 1, e, col[u], acc);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < V; j++) acc[j] *= p.scale;
+            store16((T *)p.dtable + (h.row0 + row[u]) * p.width + col[u], acc);
+        }
     }
 }
 
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
-int passes_of(int vocab) {   // keys are 0 .. vocab
+int bits_of(int vocab) {   // keys are 0 .. vocab
     int bits = 1;
     while (bits < 31 && (vocab >> bits) != 0) bits++;
-    return (bits + kBits - 1) / kBits;
+    return bits;
+}
+
+// Pairs of a block of the sort: one ranking's, or more where that makes more than kMaxTiles blocks.
+int tile_of(int64_t n) {
+    const int64_t most = (int64_t)kSub * kMaxTiles;
+    return (int)(kSub * ((n + most - 1) / most));
 }
 
 // The workspace: two lists of keys and positions, the counts, the runs' sums.
 struct Space {
-    size_t list, counts, part, bytes;
+    size_t list, counts, part, part2, bytes;
 };
 Space space(int64_t n, int width) {
     Space s{};
     s.list = round256((size_t)n * 4);
     s.counts = 4 * s.list;
-    s.part = s.counts + round256((size_t)((n + kTile - 1) / kTile) * kBins * 4);
-    s.bytes = s.part + (size_t)(n / kRun) * (size_t)width * 4;
+    s.part = s.counts + (n > kSub ? (size_t)kMaxTiles * kMaxBins * 4 : 0);
+    s.part2 = s.part + (size_t)(n / kRun) * (size_t)width * 4;
+    s.bytes = s.part2 + (size_t)(n / (kRun * kRun)) * (size_t)width * 4;
     return s;
 }
 
+// Rows and vectors of a block: about `most` vectors, fewer where that leaves multiprocessors without a block.
+Split split_of(int64_t rows, int vecs, int most, int max_rows, int sms) {
+    Split s;
+    s.cols = vecs <= kColVecs ? vecs : kColVecs;
+    const int64_t full = std::max(1, std::min(max_rows, most / s.cols));
+    const int64_t blocks_of_a_row = (vecs + s.cols - 1) / s.cols;
+    s.per_block = (int)std::max<int64_t>(1, std::min(full, rows * blocks_of_a_row / (4 * sms)));
+    return s;
+}
+dim3 grid_of(const Split &s, int64_t rows, int vecs) {
+    return dim3((unsigned)((rows + s.per_block - 1) / s.per_block), (unsigned)((vecs + s.cols - 1) / s.cols));
+}
+
+constexpr int kBlockVecs = 4096;   // vectors of a block: 16 of each thread
+
 template <typename T>
 int backward(const int32_t *tokens, int n, int vocab, int width, float scale, const void *dy, void *dtable, char *ws,
-             void *stream) {
+             int sms, void *stream) {
+    constexpr int V = kVecOf<T>;
     const Space s = space(n, width);
     int32_t *key[2] = {(int32_t *)ws, (int32_t *)(ws + s.list)};
     int32_t *pos[2] = {(int32_t *)(ws + 2 * s.list), (int32_t *)(ws + 3 * s.list)};
-    Pass p{tokens, nullptr, nullptr, nullptr, (int32_t *)(ws + s.counts), n, (n + kTile - 1) / kTile, vocab, 0};
-    const int passes = n ? passes_of(vocab) : 0;
-    for (int i = 0; i < passes; i++, p.shift += kBits) {
-        p.key_out = key[i & 1];
-        p.pos_out = pos[i & 1];
-        int rc = launch_early(digit_counts_kernel, dim3((unsigned)p.tiles), kThreads, 0, 1, stream, p);
-        if (!rc) rc = launch_early(places_kernel, dim3(1), kScanThreads, 0, 1, stream, p.counts, p.tiles * kBins);
-        if (!rc) rc = launch_early(move_pairs_kernel, dim3((unsigned)p.tiles), kThreads, 0, 1, stream, p);
-        if (rc) return rc;
-        p.key = p.key_out;
-        p.pos = p.pos_out;
+    const int bits = bits_of(vocab), passes = (bits + kMaxBits - 1) / kMaxBits;
+    Pass p{};
+    p.key = tokens;
+    p.key_out = key[0];
+    p.pos_out = pos[0];
+    p.counts = (int32_t *)(ws + s.counts);
+    p.n = n;
+    p.tile = tile_of(n);
+    p.vocab = vocab;
+    p.bits = (bits + passes - 1) / passes;
+    int rc = 0;
+    if (n > 0 && n <= kSub) {
+        rc = launch_early(sort_few_kernel, dim3(1), kThreads, 0, 1, stream, p, passes);
+        p.key = key[0];
+        p.pos = pos[0];
+    } else if (n > 0) {
+        p.tiles = (n + p.tile - 1) / p.tile;
+        for (int i = 0; i < passes && !rc; i++, p.shift += p.bits) {
+            p.key_out = key[i & 1];
+            p.pos_out = pos[i & 1];
+            rc = launch_early(digit_counts_kernel, dim3((unsigned)p.tiles), kThreads, 0, 1, stream, p);
+            if (!rc) rc = launch_early(move_pairs_kernel, dim3((unsigned)p.tiles), kThreads, 0, 1, stream, p);
+            p.key = p.key_out;
+            p.pos = p.pos_out;
+        }
     }
-    const Sums q{p.key, p.pos, dy, dtable, (float *)(ws + s.part), n, vocab, width, scale};
-    const unsigned cols = (unsigned)((width + kThreads * kVecOf<T> - 1) / (kThreads * kVecOf<T>));
-    if (n >= kRun) {
-        const int rc = launch_early(run_sums_kernel<T>, dim3((unsigned)(n / kRun), cols), kThreads, 0, 1, stream, q);
-        if (rc) return rc;
-    }
-    return launch_early(table_rows_kernel<T>, dim3((unsigned)((vocab + kTableRows - 1) / kTableRows), cols), kThreads, 0, 1, stream, q);
+    if (rc) return rc;
+    Sums q{p.key, p.pos, dy, dtable, (float *)(ws + s.part), (float *)(ws + s.part2), n, vocab, width, scale, {}};
+    const unsigned cols = (unsigned)((width + kThreads * V - 1) / (kThreads * V));
+    if (n >= kRun) rc = launch_early(run_sums_kernel<T, false>, dim3((unsigned)(n / kRun), cols), kThreads, 0, 1, stream, q);
+    if (!rc && n >= kRun * kRun)
+        rc = launch_early(run_sums_kernel<T, true>, dim3((unsigned)(n / (kRun * kRun)), cols), kThreads, 0, 1, stream, q);
+    if (rc) return rc;
+    q.split = split_of(vocab, width / V, kBlockVecs, kTableRows, sms);
+    return launch_early(table_rows_kernel<T>, grid_of(q.split, vocab, width / V), kThreads, 0, 1, stream, q);
+}
+
+template <typename T>
+int forward(const int32_t *tokens, int64_t n, const void *table, int vocab, int width, float scale, void *y, int sms,
+            void *stream) {
+    constexpr int V = kVecOf<T>;
+    const Split s = split_of(n, width / V, kBlockVecs, kBlockVecs, sms);
+    return launch_early(embed_fwd_kernel<T>, grid_of(s, n, width / V), kThreads, 0, 1, stream, tokens, n, (const T *)table, vocab,
+                        width, scale, (T *)y, s);
 }
 
 }  // namespace
@@ -314,23 +580,20 @@ int backward(const int32_t *tokens, int n, int vocab, int width, float scale, co
 int launch_embed_fwd(const cpdr_ctx *c, const int32_t *tokens, int64_t n, const void *table, int vocab, int width,
                      float scale, void *y, void *stream) {
     if (n == 0) return 0;
-    if (c->plan.in_dtype == CPDR_DTYPE_F32) {
-        const dim3 grid((unsigned)n, (unsigned)((width + kThreads * 4 - 1) / (kThreads * 4)));
-        return launch_early(embed_fwd_kernel<float>, grid, kThreads, 0, 1, stream, tokens, (const float *)table, vocab, width,
-                            scale, (float *)y);
-    }
-    const dim3 grid((unsigned)n, (unsigned)((width + kThreads * 8 - 1) / (kThreads * 8)));
-    return launch_early(embed_fwd_kernel<__nv_bfloat16>, grid, kThreads, 0, 1, stream, tokens, (const __nv_bfloat16 *)table,
-                        vocab, width, scale, (__nv_bfloat16 *)y);
+    const int sms = device_sms(c->device);
+    return c->plan.in_dtype == CPDR_DTYPE_F32
+               ? forward<float>(tokens, n, table, vocab, width, scale, y, sms, stream)
+               : forward<__nv_bfloat16>(tokens, n, table, vocab, width, scale, y, sms, stream);
 }
 
 size_t embed_bwd_workspace(int64_t n, int width) { return space(n, width).bytes; }
 
 int launch_embed_bwd(const cpdr_ctx *c, const int32_t *tokens, int64_t n, int vocab, int width, float scale,
                      const void *dy, void *dtable, void *ws, void *stream) {
-    if (c->plan.in_dtype == CPDR_DTYPE_F32)
-        return backward<float>(tokens, (int)n, vocab, width, scale, dy, dtable, (char *)ws, stream);
-    return backward<__nv_bfloat16>(tokens, (int)n, vocab, width, scale, dy, dtable, (char *)ws, stream);
+    const int sms = device_sms(c->device);
+    return c->plan.in_dtype == CPDR_DTYPE_F32
+               ? backward<float>(tokens, (int)n, vocab, width, scale, dy, dtable, (char *)ws, sms, stream)
+               : backward<__nv_bfloat16>(tokens, (int)n, vocab, width, scale, dy, dtable, (char *)ws, sms, stream);
 }
 
 }  // namespace cpdr
