@@ -7,14 +7,12 @@
 // The gradient sorts the positions by token (stable, least significant digit
 // first), so that a token's rows of dy stand together in the order of the
 // batch: sums run in a fixed order, without atomics, and every table row is
-// written once.  A token may stand in any share of the batch, so rows of the
-// sorted list are first summed in 64s wherever a 64 holds one token only; a
-// table row then adds fewer than 64 rows of dy at either end and the sums of
-// the 64s between.
+// written once.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "cpdr_internal.hpp"
 #include "launch.cuh"
@@ -102,68 +100,86 @@ embed_fwd_kernel(const int32_t *tokens, int64_t n, const T *table, int vocab, in
 
 // ------------------------------------------------------------------ sort
 // One pass orders the pairs (key, position) by up to kMaxBits bits of the key:
-// blocks count the digits of their tiles, then every block finds the places of
-// its own from all counts and moves its pairs, each warp its own stretch.
+// from the counts of every tile's digits each block finds the places of its own
+// pairs and moves them, each warp its own stretch; it counts the next pass's
+// digits of the tiles that they go to.
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
 constexpr int kMaxBits = 10, kMaxBins = 1 << kMaxBits;
-constexpr int kPerLane = 8, kSub = kThreads * kPerLane;   // pairs that a block ranks at once
-constexpr int kMaxTiles = 128;
-static_assert(kSub <= 65536, "a few pairs' positions fit 16 bits");
-constexpr int kOwnBins = kMaxBins / kThreads;              // digits that a thread adds up
+constexpr int kPerLane = 8, kSub = kSortThreads * kPerLane;   // pairs that a block ranks at once
+constexpr int kMaxTiles = 128, kMaxPasses = (31 + kMaxBits - 1) / kMaxBits;
+constexpr int kOwnBins = kMaxBins / kSortThreads;              // digits of a thread
+static_assert(kSub <= 65536 && 32 * kPerLane <= 65536, "a few pairs' positions and a warp's counts fit 16 bits");
 
 struct Pass {
-    const int32_t *key, *pos;   // pos NULL: the first pass, whose keys are tokens
-    int32_t *key_out, *pos_out;
-    int32_t *counts;            // [tiles][bins]
-    int n, tile, tiles, vocab, shift, bits;
+    const int32_t *tokens;
+    const int2 *in;    // pairs (key, position); NULL: the first pass, which takes the tokens
+    int2 *out;
+    int32_t *counts;   // [passes][tiles][bins]
+    int n, tile, tiles, vocab, pass, passes, bits;
+    __device__ __forceinline__ int32_t *counts_of(int which) const { return counts + ((int64_t)which * tiles << bits); }
+    // The key of position i: its token, or vocab (behind all others) where it lies outside the table.
+    __device__ __forceinline__ int key_of(int i) const {
+        const int k = tokens[i];
+        return (uint32_t)k < (uint32_t)vocab ? k : vocab;
+    }
 };
 
-// The key of pair i: its token, or vocab (behind all others) where it lies outside the table.
-__device__ __forceinline__ int key_of(const Pass &p, int i) {
-    const int k = p.key[i];
-    return p.pos ? k : (uint32_t)k < (uint32_t)p.vocab ? k : p.vocab;
-}
-
-__device__ __forceinline__ void clear(int *x, int n) {
-    for (int i = threadIdx.x; i < n; i += kThreads) x[i] = 0;
-}
-
 // The ranks of kSub keys (-1: none) among those of their warp with the same
-// digit, and in hist[warp][digit] how many there are.
-__device__ __forceinline__ void rank_keys(const int (&key)[kPerLane], int (&rank)[kPerLane], int (*hist)[kMaxBins], int shift, int bits) {
+// digit, and in hist[warp][digit] how many there are.  The whole block calls it.
+__device__ __forceinline__ void rank_keys(const int (&key)[kPerLane], int (&rank)[kPerLane], uint16_t (*hist)[kMaxBins],
+                                          int shift, int bits) {
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int d = lane; d < 1 << bits; d += 32) hist[w][d] = 0;
+    __syncwarp();
 #pragma unroll
     for (int u = 0; u < kPerLane; u++) {
         const int digit = key[u] < 0 ? -1 : (key[u] >> shift) & ((1 << bits) - 1);
         const uint32_t same = __match_any_sync(0xffffffffu, digit);
         rank[u] = digit < 0 ? 0 : hist[w][digit] + __popc(same & ((1u << lane) - 1));
         __syncwarp();
-        if (digit >= 0 && lane == 31 - __clz(same)) hist[w][digit] = rank[u] + 1;
+        if (digit >= 0 && lane == 31 - __clz(same)) hist[w][digit] = (uint16_t)(rank[u] + 1);
         __syncwarp();
     }
+    __syncthreads();
 }
 
-// v becomes the sum of the values of the threads before this one.
-__device__ __forceinline__ int sum_before(int v, int *sums) {
+// place[d] = the sum of count[x] of the digits x before d; the whole block calls it.
+__device__ __forceinline__ void places_of(const int *count, int *place, int bins, int *sums) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    int x = v;
+    int c[kOwnBins], v = 0;
+#pragma unroll
+    for (int x = 0; x < kOwnBins; x++) {
+        const int d = threadIdx.x * kOwnBins + x;
+        c[x] = d < bins ? count[d] : 0;
+        v += c[x];
+    }
+    int s = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        const int y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
     }
-    if (lane == 31) sums[w] = x;
+    if (lane == 31) sums[w] = s;
     __syncthreads();
-    int before = x - v;
+    s -= v;
 #pragma unroll
-    for (int i = 0; i < kWarps; i++)
-        if (i < w) before += sums[i];
-    return before;
+    for (int i = 0; i < kSortWarps; i++)
+        if (i < w) s += sums[i];
+#pragma unroll
+    for (int x = 0; x < kOwnBins; x++) {
+        const int d = threadIdx.x * kOwnBins + x;
+        if (d < bins) place[d] = s;
+        s += c[x];
+    }
+    __syncthreads();
 }
 
-__global__ void __launch_bounds__(kThreads) digit_counts_kernel(Pass p) {
+// The first pass's counts, and zeros for the others'.
+__global__ void __launch_bounds__(kSortThreads) digit_counts_kernel(Pass p) {
     __shared__ int hist[kMaxBins];
     next_grid_may_start();
-    clear(hist, 1 << p.bits);
+    const int bins = 1 << p.bits;
+    for (int d = threadIdx.x; d < bins; d += kSortThreads) hist[d] = 0;
     __syncthreads();
     previous_grid_done();
     const int a = blockIdx.x * p.tile, b = min(p.n, a + p.tile);
@@ -171,89 +187,107 @@ __global__ void __launch_bounds__(kThreads) digit_counts_kernel(Pass p) {
         int key[kPerLane];
 #pragma unroll
         for (int u = 0; u < kPerLane; u++) {
-            const int i = i0 + u * kThreads + threadIdx.x;
-            key[u] = i < b ? key_of(p, i) : -1;
+            const int i = i0 + u * kSortThreads + threadIdx.x;
+            key[u] = i < b ? p.key_of(i) : -1;
         }
 #pragma unroll
         for (int u = 0; u < kPerLane; u++)
-            if (key[u] >= 0) atomicAdd(&hist[(key[u] >> p.shift) & ((1 << p.bits) - 1)], 1);   // a count has no order
+            if (key[u] >= 0) atomicAdd(&hist[key[u] & (bins - 1)], 1);   // a count has no order
     }
     __syncthreads();
-    for (int d = threadIdx.x; d < 1 << p.bits; d += kThreads) p.counts[((int64_t)blockIdx.x << p.bits) + d] = hist[d];
+    for (int d = threadIdx.x; d < bins; d += kSortThreads) {
+        const int64_t at = ((int64_t)blockIdx.x << p.bits) + d;
+        p.counts[at] = hist[d];
+        for (int i = 1; i < p.passes; i++) p.counts_of(i)[at] = 0;
+    }
 }
 
-__global__ void __launch_bounds__(kThreads) move_pairs_kernel(Pass p) {
-    __shared__ int hist[kWarps][kMaxBins];
-    __shared__ int place[kMaxBins];
-    __shared__ int sums[kWarps];
+__global__ void __launch_bounds__(kSortThreads) move_pairs_kernel(Pass p) {
+    __shared__ uint16_t hist[kSortWarps][kMaxBins];
+    __shared__ int place[kMaxBins], total[kMaxBins], sums[kSortWarps];
     next_grid_may_start();
     previous_grid_done();
-    // where this block's pairs of each digit go: behind all smaller digits and the blocks before
     const int bins = 1 << p.bits;
-    {
-        int all[kOwnBins], mine[kOwnBins], total = 0;
+    const int a = blockIdx.x * p.tile, b = min(p.n, a + p.tile), shift = p.pass * p.bits;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t *counts = p.counts_of(p.pass);
+    int32_t *next_counts = p.pass + 1 < p.passes ? p.counts_of(p.pass + 1) : nullptr;
+    // where this block's pairs of each digit go: behind all smaller digits and the blocks before
+    int mine[kOwnBins];
 #pragma unroll
-        for (int x = 0; x < kOwnBins; x++) {
-            all[x] = mine[x] = 0;
-            const int d = threadIdx.x * kOwnBins + x;
-            if (d < bins) {
-#pragma unroll 8
-                for (int t = 0; t < p.tiles; t++) {
-                    const int c = p.counts[((int64_t)t << p.bits) + d];
-                    all[x] += c;
-                    if (t < (int)blockIdx.x) mine[x] += c;
-                }
+    for (int x = 0; x < kOwnBins; x++) {
+        const int d = x * kSortThreads + threadIdx.x;
+        int all = 0;
+        mine[x] = 0;
+        if (d < bins) {
+#pragma unroll 16
+            for (int t = 0; t < p.tiles; t++) {
+                const int c = counts[((int64_t)t << p.bits) + d];
+                all += c;
+                if (t < (int)blockIdx.x) mine[x] += c;
             }
-            total += all[x];
-        }
-        int before = sum_before(total, sums);
-#pragma unroll
-        for (int x = 0; x < kOwnBins; x++) {
-            const int d = threadIdx.x * kOwnBins + x;
-            if (d < bins) place[d] = before + mine[x];
-            before += all[x];
+            total[d] = all;
         }
     }
-    const int a = blockIdx.x * p.tile, b = min(p.n, a + p.tile);
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __syncthreads();
+    places_of(total, place, bins, sums);
+#pragma unroll
+    for (int x = 0; x < kOwnBins; x++) {
+        const int d = x * kSortThreads + threadIdx.x;
+        if (d < bins) place[d] += mine[x];
+    }
     for (int i0 = a; i0 < b; i0 += kSub) {
-        int key[kPerLane], rank[kPerLane];
+        int key[kPerLane], pos[kPerLane], rank[kPerLane];
         const int first = i0 + w * 32 * kPerLane + lane;
 #pragma unroll
-        for (int u = 0; u < kPerLane; u++) key[u] = first + 32 * u < b ? key_of(p, first + 32 * u) : -1;
-        clear(&hist[0][0], kWarps * kMaxBins);
-        __syncthreads();
-        rank_keys(key, rank, hist, p.shift, p.bits);
-        __syncthreads();
-        for (int d = threadIdx.x; d < bins; d += kThreads) {
-            int at = place[d];
-#pragma unroll
-            for (int x = 0; x < kWarps; x++) {
-                const int c = hist[x][d];
-                hist[x][d] = at;
-                at += c;
+        for (int u = 0; u < kPerLane; u++) {
+            const int i = first + 32 * u;
+            key[u] = -1;
+            pos[u] = i;
+            if (i >= b) continue;
+            if (p.in) {
+                const int2 x = p.in[i];
+                key[u] = x.x;
+                pos[u] = x.y;
+            } else {
+                key[u] = p.key_of(i);
             }
-            place[d] = at;
+        }
+        rank_keys(key, rank, hist, shift, p.bits);
+        // hist becomes how many pairs of the digit the warps before have
+        for (int d = threadIdx.x; d < bins; d += kSortThreads) {
+            int before = 0;
+#pragma unroll
+            for (int x = 0; x < kSortWarps; x++) {
+                const int c = hist[x][d];
+                hist[x][d] = (uint16_t)before;
+                before += c;
+            }
+            total[d] = before;
         }
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < kPerLane; u++) {
-            const int i = first + 32 * u;
-            if (i >= b) continue;
-            const int at = hist[w][(key[u] >> p.shift) & (bins - 1)] + rank[u];
-            p.key_out[at] = key[u];
-            p.pos_out[at] = p.pos ? p.pos[i] : i;
+            if (key[u] < 0) continue;
+            const int digit = (key[u] >> shift) & (bins - 1), at = place[digit] + hist[w][digit] + rank[u];
+            p.out[at] = make_int2(key[u], pos[u]);
+            if (next_counts) atomicAdd(&next_counts[((int64_t)(at / p.tile) << p.bits) + ((key[u] >> (shift + p.bits)) & (bins - 1))], 1);
         }
+        if (i0 + kSub >= b) break;
+        __syncthreads();
+        for (int d = threadIdx.x; d < bins; d += kSortThreads) place[d] += total[d];
         __syncthreads();
     }
 }
 
 // All passes over at most kSub pairs, by one block.
-__global__ void __launch_bounds__(kThreads) sort_few_kernel(Pass p, int passes) {
-    __shared__ int hist[kWarps][kMaxBins];
-    __shared__ int sums[kWarps];
-    __shared__ int keys[kSub];
-    __shared__ uint16_t places[kSub];   // positions: below kSub
+__global__ void __launch_bounds__(kSortThreads) sort_few_kernel(Pass p) {
+    __shared__ __align__(16) uint16_t hist[kSortWarps][kMaxBins];
+    __shared__ int place[kMaxBins], sums[kSortWarps];
+    // the pairs change places in the counts' memory
+    static_assert(sizeof(hist) >= kSub * (sizeof(int) + sizeof(uint16_t)), "the pairs fit it");
+    int *keys = (int *)&hist[0][0];
+    uint16_t *places = (uint16_t *)(keys + kSub);
     next_grid_may_start();
     previous_grid_done();
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, first = w * 32 * kPerLane + lane, bins = 1 << p.bits;
@@ -261,36 +295,35 @@ __global__ void __launch_bounds__(kThreads) sort_few_kernel(Pass p, int passes) 
 #pragma unroll
     for (int u = 0; u < kPerLane; u++) {
         pos[u] = first + 32 * u;
-        key[u] = pos[u] < p.n ? key_of(p, pos[u]) : -1;
+        key[u] = pos[u] < p.n ? p.key_of(pos[u]) : -1;
     }
-    for (int i = 0; i < passes; i++) {
+    for (int i = 0; i < p.passes; i++) {
         const int shift = i * p.bits;
-        clear(&hist[0][0], kWarps * kMaxBins);
-        __syncthreads();
         rank_keys(key, rank, hist, shift, p.bits);
-        __syncthreads();
-        int total = 0;
+        for (int d = threadIdx.x; d < bins; d += kSortThreads) {
+            int before = 0;
 #pragma unroll
-        for (int x = 0; x < kOwnBins; x++)
-#pragma unroll
-            for (int y = 0; y < kWarps; y++) total += hist[y][threadIdx.x * kOwnBins + x];
-        int at = sum_before(total, sums);
-#pragma unroll
-        for (int x = 0; x < kOwnBins; x++)
-#pragma unroll
-            for (int y = 0; y < kWarps; y++) {
-                int &c = hist[y][threadIdx.x * kOwnBins + x];
-                const int here = c;
-                c = at;
-                at += here;
+            for (int x = 0; x < kSortWarps; x++) {
+                const int c = hist[x][d];
+                hist[x][d] = (uint16_t)before;
+                before += c;
             }
+            place[d] = before;
+        }
+        __syncthreads();
+        places_of(place, place, bins, sums);
+#pragma unroll
+        for (int u = 0; u < kPerLane; u++) {
+            if (key[u] < 0) continue;
+            const int digit = (key[u] >> shift) & (bins - 1);
+            rank[u] += place[digit] + hist[w][digit];
+        }
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < kPerLane; u++)
             if (key[u] >= 0) {
-                const int to = hist[w][(key[u] >> shift) & (bins - 1)] + rank[u];
-                keys[to] = key[u];
-                places[to] = (uint16_t)pos[u];
+                keys[rank[u]] = key[u];
+                places[rank[u]] = (uint16_t)pos[u];
             }
         __syncthreads();
 #pragma unroll
@@ -299,183 +332,247 @@ __global__ void __launch_bounds__(kThreads) sort_few_kernel(Pass p, int passes) 
             key[u] = j < p.n ? keys[j] : -1;
             pos[u] = j < p.n ? places[j] : 0;
         }
+        __syncthreads();
     }
 #pragma unroll
     for (int u = 0; u < kPerLane; u++) {
         const int j = first + 32 * u;
-        if (j < p.n) {
-            p.key_out[j] = key[u];
-            p.pos_out[j] = pos[u];
-        }
+        if (j < p.n) p.out[j] = make_int2(key[u], pos[u]);
     }
 }
 
 // ------------------------------------------------------------------ sums
-constexpr int kRun = 64;   // sorted pairs, or sums of such, that are summed ahead where they hold one token
+// The sorted list is cut into segments, so that a token in every place costs no
+// more than one in few.  A segment's runs of one token are summed; a run that
+// lies in it whole is a table row, the others (its first and its last run, when
+// the token goes on beyond the segment) go to the segment's two rows of `part`,
+// which a second kernel adds up.  Table rows that do not occur are filled by
+// blocks of their own, among the segments'.
+constexpr int kSegment = 32;
+constexpr int kMaxGroups = 32;   // segments of a block, at most
 
 struct Sums {
-    const int32_t *key, *pos;   // sorted
+    const int2 *pair;           // (key, position), sorted
     const void *dy;
     void *dtable;
-    float *part, *part2;        // sums of whole runs of kRun pairs, and of kRun such runs: [.., width]
+    float *part;                // [segments][2][width]: the run that comes from before, the one that goes on
     int n, vocab, width;
     float scale;
-    Split split;
+    int cols, groups;           // segments' blocks: vectors of a row, segments of a block
+    int seg_blocks, zero_blocks, col_blocks;
+    Split split;                // of the table, for the blocks that fill it
 };
 
 template <int V>
-__device__ __forceinline__ void add(float (&acc)[V], const uint4 &raw) {
-    float x[V];
-    widen16(raw, x);
+__device__ __forceinline__ void store_floats(float *to, const float (&x)[V]) {
 #pragma unroll
-    for (int j = 0; j < V; j++) acc[j] += x[j];
-}
-
-// acc += rows pos[a .. b) of dy, from column col on
-template <typename T, int V>
-__device__ __forceinline__ void add_rows(const Sums &p, int a, int b, int col, float (&acc)[V]) {
-    const T *dy = (const T *)p.dy + col;
-    for (; a < b; a += kAhead) {
-        uint4 x[kAhead];
-#pragma unroll
-        for (int u = 0; u < kAhead; u++)
-            x[u] = a + u < b ? load16(dy + (int64_t)p.pos[a + u] * p.width) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int u = 0; u < kAhead; u++) add<V>(acc, x[u]);
-    }
-}
-
-// acc += rows a .. b - 1 of part, from column col on
-template <int V>
-__device__ __forceinline__ void add_sums(const float *part, int width, int a, int b, int col, float (&acc)[V]) {
-    part += (int64_t)a * width + col;
-    for (; a < b; a += kAhead, part += (int64_t)kAhead * width) {
-        float4 x[kAhead][V / 4];
-#pragma unroll
-        for (int u = 0; u < kAhead; u++)
-#pragma unroll
-            for (int j = 0; j < V / 4; j++)
-                x[u][j] = a + u < b ? *reinterpret_cast<const float4 *>(part + (int64_t)u * width + 4 * j)
-                                    : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int u = 0; u < kAhead; u++)
-#pragma unroll
-            for (int j = 0; j < V / 4; j++) {
-                acc[4 * j] += x[u][j].x;
-                acc[4 * j + 1] += x[u][j].y;
-                acc[4 * j + 2] += x[u][j].z;
-                acc[4 * j + 3] += x[u][j].w;
-            }
-    }
-}
-
-// SECOND: of kRun runs' sums.  grid (whole runs, blocks of columns)
-template <typename T, bool SECOND>
-__global__ void __launch_bounds__(kThreads) run_sums_kernel(Sums p) {
-    constexpr int V = kVecOf<T>, LEN = SECOND ? kRun * kRun : kRun;
-    next_grid_may_start();
-    previous_grid_done();
-    const int a = blockIdx.x * LEN, col = (blockIdx.y * kThreads + threadIdx.x) * V;
-    const int k = p.key[a];
-    if (k != p.key[a + LEN - 1] || k >= p.vocab || col >= p.width) return;
-    float acc[V];
-#pragma unroll
-    for (int j = 0; j < V; j++) acc[j] = 0.f;
-    if (SECOND) add_sums<V>(p.part, p.width, a / kRun, a / kRun + kRun, col, acc);
-    else add_rows<T, V>(p, a, a + LEN, col, acc);
-    float *to = (SECOND ? p.part2 : p.part) + (int64_t)blockIdx.x * p.width + col;
-#pragma unroll
-    for (int j = 0; j < V; j += 4) *reinterpret_cast<float4 *>(to + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+    for (int j = 0; j < V; j += 4) *reinterpret_cast<float4 *>(to + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
 }
 
 // The whole warp calls it: the first pair whose key is not below k.
-__device__ __forceinline__ int lower_bound(const int32_t *key, int n, int k) {
+__device__ __forceinline__ int lower_bound(const int2 *pair, int n, int k) {
     const int lane = threadIdx.x & 31;
     int a = 0, len = n;   // it lies in a .. a + len
     while (len > 32) {
         const int step = len / 33, at = a + (lane + 1) * step;   // the last one: a + 32 (len / 33) < a + len
-        const int below = __popc(__ballot_sync(0xffffffffu, key[at] < k));
+        const int below = __popc(__ballot_sync(0xffffffffu, pair[at].x < k));
         const int end = below < 32 ? a + (below + 1) * step : a + len;
         if (below) a += below * step + 1;
         len = end - a;
     }
-    return a + __popc(__ballot_sync(0xffffffffu, lane < len && key[a + (lane < len ? lane : 0)] < k));
+    return a + __popc(__ballot_sync(0xffffffffu, lane < len && pair[a + lane].x < k));
 }
 
-constexpr int kTableRows = 256;   // table rows of a block, at most
+constexpr int kTableRows = 512;   // table rows of a block, at most
 
-// acc += the sum of pairs a .. b - 1 of the sorted list, which hold one token
-template <typename T, int V>
-__device__ __forceinline__ void add_pairs(const Sums &p, int a, int b, int col, float (&acc)[V]) {
-    const int c0 = (a + kRun - 1) / kRun, c1 = b / kRun;   // whole runs
-    if (c0 >= c1) {
-        add_rows<T, V>(p, a, b, col, acc);
-        return;
-    }
-    add_rows<T, V>(p, a, c0 * kRun, col, acc);
-    const int d0 = (c0 + kRun - 1) / kRun, d1 = c1 / kRun;
-    if (d0 >= d1) {
-        add_sums<V>(p.part, p.width, c0, c1, col, acc);
-    } else {
-        add_sums<V>(p.part, p.width, c0, d0 * kRun, col, acc);
-        add_sums<V>(p.part2, p.width, d0, d1, col, acc);
-        add_sums<V>(p.part, p.width, d1 * kRun, c1, col, acc);
-    }
-    add_rows<T, V>(p, c1 * kRun, b, col, acc);
-}
-
+// zeros in the rows of a share of the table that do not occur
 template <typename T>
-__global__ void __launch_bounds__(kThreads) table_rows_kernel(Sums p) {
-    constexpr int V = kVecOf<T>;
-    __shared__ int first[kTableRows], last[kTableRows], ends[2];   // pairs of each row: first .. last - 1
-    next_grid_may_start();
-    previous_grid_done();
-    const Share h = share_of(p.split, p.vocab, p.width / V);
-    for (int r = threadIdx.x; r < h.rows; r += kThreads) first[r] = last[r] = 0;
+__device__ __forceinline__ void fill_rows(const Sums &p, const Share &h, uint32_t *occurs, int *ends) {
+    for (int r = threadIdx.x; r < kTableRows / 32; r += kThreads) occurs[r] = 0;
     if (threadIdx.x < 64) {
-        const int w = threadIdx.x >> 5, e = lower_bound(p.key, p.n, (int)h.row0 + (w ? h.rows : 0));
+        const int w = threadIdx.x >> 5, e = lower_bound(p.pair, p.n, (int)h.row0 + (w ? h.rows : 0));
         if ((threadIdx.x & 31) == 0) ends[w] = e;
     }
     __syncthreads();
-    const int a = ends[0], b = ends[1];
-    for (int i = a + threadIdx.x; i < b; i += kThreads) {
-        const int k = p.key[i], r = k - (int)h.row0;
-        if (i == a || p.key[i - 1] != k) first[r] = i;
-        if (i == b - 1 || p.key[i + 1] != k) last[r] = i + 1;
+    for (int i = ends[0] + threadIdx.x; i < ends[1]; i += kThreads) {
+        const int k = p.pair[i].x, r = k - (int)h.row0;
+        if (i == ends[0] || p.pair[i - 1].x != k) atomicOr(&occurs[r >> 5], 1u << (r & 31));
     }
     __syncthreads();
-    Walk w(h);
-    while (w.row < h.rows) {
-        int row[kAhead], col[kAhead];
+    T *to = (T *)p.dtable + h.row0 * p.width + h.col0 * kVecOf<T>;
+    for (Walk w(h); w.row < h.rows; w.next())
+        if (!(occurs[w.row >> 5] >> (w.row & 31) & 1))
+            *reinterpret_cast<uint4 *>(to + (int64_t)w.row * p.width + w.col * kVecOf<T>) = make_uint4(0, 0, 0, 0);
+}
+
+// grid: the segments' and the filling blocks in turn
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 5) segment_sums_kernel(Sums p) {
+    constexpr int V = kVecOf<T>;
+    __shared__ int2 pairs[kMaxGroups * kSegment];
+    __shared__ int ends[2];
+    next_grid_may_start();
+    previous_grid_done();
+    // the roles alternate as long as there are blocks of both
+    const int both_of = 2 * min(p.seg_blocks, p.zero_blocks), i = blockIdx.x;
+    const bool fills = i < both_of ? i & 1 : p.seg_blocks < p.zero_blocks;
+    const int at = i < both_of ? i >> 1 : i - both_of / 2;
+    if (fills) {
+        const int per_row = (p.width / V + p.split.cols - 1) / p.split.cols;
+        Share h;
+        h.row0 = (int64_t)(at / per_row) * p.split.per_block;
+        h.rows = (int)min((int64_t)p.split.per_block, p.vocab - h.row0);
+        h.col0 = at % per_row * p.split.cols;
+        h.cols = min(p.split.cols, p.width / V - h.col0);
+        fill_rows<T>(p, h, (uint32_t *)pairs, ends);
+        return;
+    }
+    const int seg0 = at / p.col_blocks * p.groups;
+    const int group = threadIdx.x / p.cols, col = (at % p.col_blocks * p.cols + threadIdx.x % p.cols) * V;
+    for (int x = threadIdx.x; x < p.groups * kSegment; x += kThreads) {
+        const int j = seg0 * kSegment + x;
+        pairs[x] = j < p.n ? p.pair[j] : make_int2(p.vocab, 0);
+    }
+    __syncthreads();
+    const int seg = seg0 + group, a = seg * kSegment, b = min(p.n, a + kSegment);
+    if (group >= p.groups || a >= p.n || col >= p.width) return;
+    const int2 *pair = pairs + group * kSegment;
+    const bool from_before = a > 0 && p.pair[a - 1].x == pair[0].x, goes_on = b < p.n && p.pair[b].x == pair[b - 1 - a].x;
+    const T *dy = (const T *)p.dy + col;
+    float *part = p.part + (int64_t)seg * 2 * p.width + col;
+    float acc[V];
+#pragma unroll
+    for (int j = 0; j < V; j++) acc[j] = 0.f;
+    bool first = true;   // the segment's first run
+    // pairs that are padding (or lie behind the list) load dy's first row, which nothing takes
+#pragma unroll 1
+    for (int j = 0; j < kSegment; j += kAhead) {
         uint4 x[kAhead];
 #pragma unroll
-        for (int u = 0; u < kAhead; u++, w.next()) {
-            row[u] = w.row;
-            col[u] = (h.col0 + w.col) * V;
-            x[u] = make_uint4(0, 0, 0, 0);
-            if (row[u] < h.rows && last[row[u]] != 0)
-                x[u] = load16((const T *)p.dy + (int64_t)p.pos[first[row[u]]] * p.width + col[u]);
+        for (int u = 0; u < kAhead; u++) {
+            const int2 q = pair[j + u];
+            x[u] = load16(dy + (int64_t)(q.x < p.vocab ? q.y : 0) * p.width);
         }
 #pragma unroll
         for (int u = 0; u < kAhead; u++) {
-            if (row[u] >= h.rows) continue;
-            const int i = first[row[u]], e = last[row[u]];
-            float acc[V];
-            widen16(x[u], acc);
-            if (e > i + 1) {
-                // whole runs start at the first pair: it is not taken by itself
-                if (e - i >= kRun) {
+            const int k = pair[j + u].x;
+            if (k >= p.vocab) return;   // nothing but padding behind it
+            float f[V];
+            widen16(x[u], f);
 #pragma unroll
-                    for (int j = 0; j < V; j++) acc[j] = 0.f;
-                    add_pairs<T, V>(p, i, e, col[u], acc);
-                } else {
-                    add_rows<T, V>(p, i + 1, e, col[u], acc);
-                }
+            for (int e = 0; e < V; e++) acc[e] += f[e];
+            const bool ends_here = a + j + u == b - 1;
+            if (!ends_here && pair[j + u + 1].x == k) continue;
+            // the run is over, or the segment
+            if (first && from_before) {
+                store_floats(part, acc);
+            } else if (ends_here && goes_on) {
+                store_floats(part + p.width, acc);
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; e++) acc[e] *= p.scale;
+                store16((T *)p.dtable + (int64_t)k * p.width + col, acc);
             }
+            first = false;
 #pragma unroll
-            for (int j = 0; j < V; j++) acc[j] *= p.scale;
-            store16((T *)p.dtable + (h.row0 + row[u]) * p.width + col[u], acc);
+            for (int e = 0; e < V; e++) acc[e] = 0.f;
         }
+    }
+}
+
+// Four floats; volatile, so that a batch of loads stays ahead of the sums that
+// take them (left to itself the compiler saves the registers: two loads in flight).
+__device__ __forceinline__ float4 load_now(const float *p) {
+    float4 v;
+    asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ void add4(float4 &a, const float4 &b) {
+    a.x += b.x;
+    a.y += b.y;
+    a.z += b.z;
+    a.w += b.w;
+}
+
+// acc += the incoming runs of segments a .. b - 1, from column col on
+__device__ __forceinline__ void add_parts(const Sums &p, int a, int b, int col, float4 &acc) {
+    const int64_t row = 2 * (int64_t)p.width;
+    const float *part = p.part + a * row + col;
+    auto some = [&](auto count) {
+        constexpr int N = decltype(count)::value;
+        float4 x[N];
+#pragma unroll
+        for (int u = 0; u < N; u++) x[u] = load_now(part + u * row);
+#pragma unroll
+        for (int u = 0; u < N; u++) add4(acc, x[u]);
+        part += N * row;
+    };
+#pragma unroll 1
+    for (; a + 16 <= b; a += 16) some(std::integral_constant<int, 16>());
+#pragma unroll 1
+    for (; a + 4 <= b; a += 4) some(std::integral_constant<int, 4>());
+#pragma unroll 1
+    for (; a < b; a++) some(std::integral_constant<int, 1>());
+}
+
+__device__ __forceinline__ void store_four(float *p, const float4 &v) { *reinterpret_cast<float4 *>(p) = v; }
+__device__ __forceinline__ void store_four(__nv_bfloat16 *p, const float4 &v) {
+    store2(p, make_float2(v.x, v.y));
+    store2(p + 2, make_float2(v.z, v.w));
+}
+
+constexpr int kLong = 64;   // segments of a run that one warp adds up alone, at most
+
+// The tokens that go on beyond the segment they begin in: a warp for each
+// segment, 128 columns; the block's warps share a long run.
+// grid (blocks of kWarps segments, blocks of columns)
+template <typename T>
+__global__ void __launch_bounds__(kThreads) joined_runs_kernel(Sums p) {
+    __shared__ float4 sh[kWarps][32];
+    __shared__ int len[kWarps];
+    next_grid_may_start();
+    previous_grid_done();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int seg = blockIdx.x * kWarps + w, col = (blockIdx.y * 32 + lane) * 4;
+    const bool live = col < p.width;
+    // segments behind this one that the run goes on into
+    int more = 0, k = p.vocab;
+    const int64_t b = (int64_t)(seg + 1) * kSegment;
+    if (b < p.n) {
+        k = p.pair[b - 1].x;
+        const int a = (int)b - kSegment;
+        if (k < p.vocab && p.pair[b].x == k && (a == 0 || p.pair[a - 1].x != k || p.pair[a].x != k))
+            more = (lower_bound(p.pair, p.n, k + 1) - 1) / kSegment - seg;
+    }
+    float4 acc;
+    auto begin = [&](int s) { acc = live ? load_now(p.part + (2 * (int64_t)s + 1) * p.width + col) : make_float4(0.f, 0.f, 0.f, 0.f); };
+    auto finish = [&](int key) {
+        if (live)
+            store_four((T *)p.dtable + (int64_t)key * p.width + col,
+                       make_float4(acc.x * p.scale, acc.y * p.scale, acc.z * p.scale, acc.w * p.scale));
+    };
+    if (more > 0 && more <= kLong) {
+        begin(seg);
+        if (live) add_parts(p, seg + 1, seg + 1 + more, col, acc);
+        finish(k);
+    }
+    if (lane == 0) len[w] = more > kLong ? more : 0;
+    __syncthreads();
+    for (int x = 0; x < kWarps; x++) {
+        const int m = len[x];
+        if (!m) continue;
+        const int s = blockIdx.x * kWarps + x, per = (m + kWarps - 1) / kWarps;
+        if (w == 0) begin(s);
+        else acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (live) add_parts(p, s + 1 + min(m, w * per), s + 1 + min(m, (w + 1) * per), col, acc);
+        sh[w][lane] = acc;
+        __syncthreads();
+        if (w == 0) {
+#pragma unroll
+            for (int y = 1; y < kWarps; y++) add4(acc, sh[y][lane]);
+            finish(p.pair[(int64_t)(s + 1) * kSegment - 1].x);
+        }
+        __syncthreads();
     }
 }
 
@@ -490,20 +587,21 @@ int bits_of(int vocab) {   // keys are 0 .. vocab
 // Pairs of a block of the sort: one ranking's, or more where that makes more than kMaxTiles blocks.
 int tile_of(int64_t n) {
     const int64_t most = (int64_t)kSub * kMaxTiles;
-    return (int)(kSub * ((n + most - 1) / most));
+    return (int)(kSub * std::max<int64_t>(1, (n + most - 1) / most));
 }
 
-// The workspace: two lists of keys and positions, the counts, the runs' sums.
+int64_t segments_of(int64_t n) { return (n + kSegment - 1) / kSegment; }
+
+// The workspace: two lists of pairs, the passes' counts, the segments' sums.
 struct Space {
-    size_t list, counts, part, part2, bytes;
+    size_t list, counts, part, bytes;
 };
 Space space(int64_t n, int width) {
     Space s{};
-    s.list = round256((size_t)n * 4);
-    s.counts = 4 * s.list;
-    s.part = s.counts + (n > kSub ? (size_t)kMaxTiles * kMaxBins * 4 : 0);
-    s.part2 = s.part + (size_t)(n / kRun) * (size_t)width * 4;
-    s.bytes = s.part2 + (size_t)(n / (kRun * kRun)) * (size_t)width * 4;
+    s.list = round256((size_t)n * sizeof(int2));
+    s.counts = (n > kSub ? 2 : 1) * s.list;
+    s.part = s.counts + (n > kSub ? (size_t)kMaxPasses * kMaxTiles * kMaxBins * 4 : 0);
+    s.bytes = s.part + (size_t)segments_of(n) * 2 * (size_t)width * 4;
     return s;
 }
 
@@ -527,43 +625,46 @@ int backward(const int32_t *tokens, int n, int vocab, int width, float scale, co
              int sms, void *stream) {
     constexpr int V = kVecOf<T>;
     const Space s = space(n, width);
-    int32_t *key[2] = {(int32_t *)ws, (int32_t *)(ws + s.list)};
-    int32_t *pos[2] = {(int32_t *)(ws + 2 * s.list), (int32_t *)(ws + 3 * s.list)};
-    const int bits = bits_of(vocab), passes = (bits + kMaxBits - 1) / kMaxBits;
+    int2 *list[2] = {(int2 *)ws, (int2 *)(ws + s.list)};
+    const int bits = bits_of(vocab);
     Pass p{};
-    p.key = tokens;
-    p.key_out = key[0];
-    p.pos_out = pos[0];
+    p.tokens = tokens;
+    p.out = list[0];
     p.counts = (int32_t *)(ws + s.counts);
     p.n = n;
     p.tile = tile_of(n);
+    p.tiles = (n + p.tile - 1) / p.tile;
     p.vocab = vocab;
-    p.bits = (bits + passes - 1) / passes;
+    p.passes = (bits + kMaxBits - 1) / kMaxBits;
+    p.bits = (bits + p.passes - 1) / p.passes;
     int rc = 0;
     if (n > 0 && n <= kSub) {
-        rc = launch_early(sort_few_kernel, dim3(1), kThreads, 0, 1, stream, p, passes);
-        p.key = key[0];
-        p.pos = pos[0];
+        rc = launch_early(sort_few_kernel, dim3(1), kSortThreads, 0, 1, stream, p);
     } else if (n > 0) {
-        p.tiles = (n + p.tile - 1) / p.tile;
-        for (int i = 0; i < passes && !rc; i++, p.shift += p.bits) {
-            p.key_out = key[i & 1];
-            p.pos_out = pos[i & 1];
-            rc = launch_early(digit_counts_kernel, dim3((unsigned)p.tiles), kThreads, 0, 1, stream, p);
-            if (!rc) rc = launch_early(move_pairs_kernel, dim3((unsigned)p.tiles), kThreads, 0, 1, stream, p);
-            p.key = p.key_out;
-            p.pos = p.pos_out;
+        rc = launch_early(digit_counts_kernel, dim3((unsigned)p.tiles), kSortThreads, 0, 1, stream, p);
+        for (; p.pass < p.passes && !rc; p.pass++) {
+            p.out = list[p.pass & 1];
+            rc = launch_early(move_pairs_kernel, dim3((unsigned)p.tiles), kSortThreads, 0, 1, stream, p);
+            p.in = p.out;
         }
     }
     if (rc) return rc;
-    Sums q{p.key, p.pos, dy, dtable, (float *)(ws + s.part), (float *)(ws + s.part2), n, vocab, width, scale, {}};
-    const unsigned cols = (unsigned)((width + kThreads * V - 1) / (kThreads * V));
-    if (n >= kRun) rc = launch_early(run_sums_kernel<T, false>, dim3((unsigned)(n / kRun), cols), kThreads, 0, 1, stream, q);
-    if (!rc && n >= kRun * kRun)
-        rc = launch_early(run_sums_kernel<T, true>, dim3((unsigned)(n / (kRun * kRun)), cols), kThreads, 0, 1, stream, q);
-    if (rc) return rc;
-    q.split = split_of(vocab, width / V, kBlockVecs, kTableRows, sms);
-    return launch_early(table_rows_kernel<T>, grid_of(q.split, vocab, width / V), kThreads, 0, 1, stream, q);
+    const int vecs = width / V;
+    Sums q{p.out, dy, dtable, (float *)(ws + s.part), n, vocab, width, scale};
+    q.cols = std::min(vecs, kThreads);
+    q.groups = std::min(kThreads / q.cols, kMaxGroups);
+    q.col_blocks = (vecs + q.cols - 1) / q.cols;
+    const int64_t segments = segments_of(n), seg_blocks = (segments + q.groups - 1) / q.groups * q.col_blocks;
+    q.split = split_of(vocab, vecs, kBlockVecs, kTableRows, sms);
+    const dim3 fill = grid_of(q.split, vocab, vecs);
+    const int64_t zero_blocks = (int64_t)fill.x * fill.y;
+    if (seg_blocks + zero_blocks > 0x7fffffff) return (int)cudaErrorInvalidValue;
+    q.seg_blocks = (int)seg_blocks;
+    q.zero_blocks = (int)zero_blocks;
+    rc = launch_early(segment_sums_kernel<T>, dim3((unsigned)(seg_blocks + zero_blocks)), kThreads, 0, 1, stream, q);
+    if (rc || segments < 2) return rc;
+    return launch_early(joined_runs_kernel<T>, dim3((unsigned)((segments + kWarps - 1) / kWarps), (unsigned)((width + 127) / 128)),
+                        kThreads, 0, 1, stream, q);
 }
 
 template <typename T>
