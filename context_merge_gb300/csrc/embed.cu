@@ -93,7 +93,10 @@ embed_fwd_kernel(const int32_t *tokens, int64_t n, const T *table, int vocab, in
             widen16(x[u], f);
 #pragma unroll
             for (int j = 0; j < V; j++) f[j] *= scale;
-            store16(y + to[u], f);
+            // y is read by another kernel: it leaves the L2 to the table's rows (262144 x 2048: 221 -> 216 us)
+            float4 r;
+            store16(reinterpret_cast<T *>(&r), f);
+            __stcs(reinterpret_cast<float4 *>(y + to[u]), r);
         }
     }
 }
@@ -212,6 +215,25 @@ __global__ void __launch_bounds__(kSortThreads) move_pairs_kernel(Pass p) {
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t *counts = p.counts_of(p.pass);
     int32_t *next_counts = p.pass + 1 < p.passes ? p.counts_of(p.pass + 1) : nullptr;
+    int key[kPerLane], pos[kPerLane], rank[kPerLane];
+    const int mine0 = w * 32 * kPerLane + lane;
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int u = 0; u < kPerLane; u++) {
+            const int i = i0 + mine0 + 32 * u;
+            key[u] = -1;
+            pos[u] = i;
+            if (i >= b) continue;
+            if (p.in) {
+                const int2 x = p.in[i];
+                key[u] = x.x;
+                pos[u] = x.y;
+            } else {
+                key[u] = p.key_of(i);
+            }
+        }
+    };
+    load(a);
     // where this block's pairs of each digit go: behind all smaller digits and the blocks before
     int mine[kOwnBins];
 #pragma unroll
@@ -237,22 +259,6 @@ __global__ void __launch_bounds__(kSortThreads) move_pairs_kernel(Pass p) {
         if (d < bins) place[d] += mine[x];
     }
     for (int i0 = a; i0 < b; i0 += kSub) {
-        int key[kPerLane], pos[kPerLane], rank[kPerLane];
-        const int first = i0 + w * 32 * kPerLane + lane;
-#pragma unroll
-        for (int u = 0; u < kPerLane; u++) {
-            const int i = first + 32 * u;
-            key[u] = -1;
-            pos[u] = i;
-            if (i >= b) continue;
-            if (p.in) {
-                const int2 x = p.in[i];
-                key[u] = x.x;
-                pos[u] = x.y;
-            } else {
-                key[u] = p.key_of(i);
-            }
-        }
         rank_keys(key, rank, hist, shift, p.bits);
         // hist becomes how many pairs of the digit the warps before have
         for (int d = threadIdx.x; d < bins; d += kSortThreads) {
@@ -277,6 +283,7 @@ __global__ void __launch_bounds__(kSortThreads) move_pairs_kernel(Pass p) {
         __syncthreads();
         for (int d = threadIdx.x; d < bins; d += kSortThreads) place[d] += total[d];
         __syncthreads();
+        load(i0 + kSub);
     }
 }
 
@@ -343,22 +350,23 @@ __global__ void __launch_bounds__(kSortThreads) sort_few_kernel(Pass p) {
 
 // ------------------------------------------------------------------ sums
 // The sorted list is cut into segments, so that a token in every place costs no
-// more than one in few.  A segment's runs of one token are summed; a run that
-// lies in it whole is a table row, the others (its first and its last run, when
-// the token goes on beyond the segment) go to the segment's two rows of `part`,
-// which a second kernel adds up.  Table rows that do not occur are filled by
-// blocks of their own, among the segments'.
-constexpr int kSegment = 32;
+// more than one in few.  A segment sums the runs of one token that begin in it,
+// to their ends, which may lie up to kBeyond pairs behind it.  A run that goes
+// on further is long: each of its segments puts its part of the sum into `part`,
+// and a second kernel adds those up.  Table rows that do not occur are
+// filled by blocks of their own, among the segments'.
+constexpr int kSegment = 32;   // a warp's lanes
+constexpr int kBeyond = 256;
 constexpr int kMaxGroups = 32;   // segments of a block, at most
 
 struct Sums {
     const int2 *pair;           // (key, position), sorted
     const void *dy;
     void *dtable;
-    float *part;                // [segments][2][width]: the run that comes from before, the one that goes on
+    float *part;                // [segments][2][width]: a long run that comes from before, one that begins here
     int n, vocab, width;
     float scale;
-    int cols, groups;           // segments' blocks: vectors of a row, segments of a block
+    int cols, groups;           // segments' blocks: vectors of a row (two for each thread), segments of a block
     int seg_blocks, zero_blocks, col_blocks;
     Split split;                // of the table, for the blocks that fill it
 };
@@ -394,9 +402,23 @@ __device__ __forceinline__ void fill_rows(const Sums &p, const Share &h, uint32_
         if ((threadIdx.x & 31) == 0) ends[w] = e;
     }
     __syncthreads();
-    for (int i = ends[0] + threadIdx.x; i < ends[1]; i += kThreads) {
-        const int k = p.pair[i].x, r = k - (int)h.row0;
-        if (i == ends[0] || p.pair[i - 1].x != k) atomicOr(&occurs[r >> 5], 1u << (r & 31));
+    const int a = ends[0], b = ends[1];
+    if (b - a <= 4 * kThreads) {
+        for (int i = a + threadIdx.x; i < b; i += kThreads) {
+            const int k = p.pair[i].x, r = k - (int)h.row0;
+            if (i == a || p.pair[i - 1].x != k) atomicOr(&occurs[r >> 5], 1u << (r & 31));
+        }
+    } else {   // frequent tokens: a search for each row instead of a look at every pair
+        for (int r = threadIdx.x; r < h.rows; r += kThreads) {
+            const int k = (int)h.row0 + r;
+            int lo = a, hi = b;
+            while (lo < hi) {
+                const int m = lo + (hi - lo) / 2;
+                if (p.pair[m].x < k) lo = m + 1;
+                else hi = m;
+            }
+            if (lo < b && p.pair[lo].x == k) atomicOr(&occurs[r >> 5], 1u << (r & 31));
+        }
     }
     __syncthreads();
     T *to = (T *)p.dtable + h.row0 * p.width + h.col0 * kVecOf<T>;
@@ -405,11 +427,78 @@ __device__ __forceinline__ void fill_rows(const Sums &p, const Share &h, uint32_
             *reinterpret_cast<uint4 *>(to + (int64_t)w.row * p.width + w.col * kVecOf<T>) = make_uint4(0, 0, 0, 0);
 }
 
+// What a segment sums: pairs begin .. end - 1.
+struct Plan {
+    int begin, end;
+    uint32_t ends;        // bit i: a run ends with the segment's pair i
+    bool from_before;     // the first run is a long one, begun before
+    bool goes_on;         // the last run is a long one, begun here
+};
+
+// The whole warp calls it; `pair` holds the segment's pairs.
+__device__ __forceinline__ Plan plan_of(const Sums &p, const int2 *pair, int seg) {
+    const int a = seg * kSegment, lane = threadIdx.x & 31;
+    Plan s{a, a, 0, false, false};
+    if (a >= p.n) return s;
+    const int b = min(p.n, a + kSegment), len = b - a;
+    const int key = pair[lane].x, first = pair[0].x, last = pair[len - 1].x;   // behind the list: vocab
+    const uint32_t alike = __ballot_sync(0xffffffffu, lane < len && key == first);
+    s.ends = __ballot_sync(0xffffffffu, lane + 1 < len && key != pair[lane + 1 < len ? lane + 1 : lane].x);
+    const int tokens = __popc(__ballot_sync(0xffffffffu, key < p.vocab));   // padding stands last
+    s.end = a + tokens;
+    const int before = a ? p.pair[a - 1].x : -1, behind = b < p.n ? p.pair[b].x : -1;
+    if (before == first && first < p.vocab) {
+        // where it began, and whether it is long
+        const int w0 = a - kBeyond - kSegment;
+        bool is_long = w0 >= 0 && p.pair[w0 >= 0 ? w0 : 0].x == first;
+        if (!is_long) {
+            const int from = max(0, w0), start = from + lower_bound(p.pair + from, a - from, first);
+            const int64_t limit = (int64_t)(start / kSegment + 1) * kSegment + kBeyond;
+            is_long = limit < p.n && p.pair[limit].x == first;
+        }
+        s.from_before = is_long;
+        if (!is_long) s.begin = a + __popc(alike);
+    }
+    if (behind == last && last < p.vocab && s.begin < b && !(s.from_before && last == first)) {
+        const int64_t limit = (int64_t)b + kBeyond;
+        s.goes_on = limit < p.n && p.pair[limit].x == last;
+        if (!s.goes_on) s.end = b + lower_bound(p.pair + b, (int)min((int64_t)kBeyond, (int64_t)p.n - b), last + 1);
+    }
+    return s;
+}
+
+// Rows of dy on their way to a thread's places in shared memory, two vectors
+// of each: 5 blocks of an SM have 160 KB in flight.
+constexpr int kStages = 4;
+
+__device__ __forceinline__ void fetch16(void *to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void fetch_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void fetch_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The values of a vector, in pairs.
+__device__ __forceinline__ void pairs_of(const uint4 &r, float2 (&v)[2], float) {
+    v[0] = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
+    v[1] = make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
+}
+__device__ __forceinline__ void pairs_of(const uint4 &r, float2 (&v)[4], __nv_bfloat16) {
+    v[0] = widen(Raw2<__nv_bfloat16>{r.x});
+    v[1] = widen(Raw2<__nv_bfloat16>{r.y});
+    v[2] = widen(Raw2<__nv_bfloat16>{r.z});
+    v[3] = widen(Raw2<__nv_bfloat16>{r.w});
+}
+
 // grid: the segments' and the filling blocks in turn
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 5) segment_sums_kernel(Sums p) {
-    constexpr int V = kVecOf<T>;
+    constexpr int V = kVecOf<T>, H = V / 2;
+    __shared__ uint4 stage[kStages][2][kThreads];   // each thread reads what it fetched itself
     __shared__ int2 pairs[kMaxGroups * kSegment];
+    __shared__ Plan plans[kMaxGroups];
     __shared__ int ends[2];
     next_grid_may_start();
     previous_grid_done();
@@ -428,56 +517,86 @@ __global__ void __launch_bounds__(kThreads, 5) segment_sums_kernel(Sums p) {
         return;
     }
     const int seg0 = at / p.col_blocks * p.groups;
-    const int group = threadIdx.x / p.cols, col = (at % p.col_blocks * p.cols + threadIdx.x % p.cols) * V;
     for (int x = threadIdx.x; x < p.groups * kSegment; x += kThreads) {
         const int j = seg0 * kSegment + x;
         pairs[x] = j < p.n ? p.pair[j] : make_int2(p.vocab, 0);
     }
     __syncthreads();
-    const int seg = seg0 + group, a = seg * kSegment, b = min(p.n, a + kSegment);
-    if (group >= p.groups || a >= p.n || col >= p.width) return;
+    for (int g = threadIdx.x >> 5; g < p.groups; g += kWarps) {
+        const Plan s = plan_of(p, pairs + g * kSegment, seg0 + g);
+        if ((threadIdx.x & 31) == 0) plans[g] = s;
+    }
+    __syncthreads();
+    const int half = (p.cols + 1) / 2, group = threadIdx.x / half, mine = threadIdx.x % half;
+    if (group >= p.groups) return;
+    const int vec = at % p.col_blocks * p.cols + mine, vecs = p.width / V;
+    if (vec >= vecs) return;
+    const bool two = mine + half < p.cols && vec + half < vecs;   // the second vector is there
+    const Plan s = plans[group];
+    const int a = (seg0 + group) * kSegment;
     const int2 *pair = pairs + group * kSegment;
-    const bool from_before = a > 0 && p.pair[a - 1].x == pair[0].x, goes_on = b < p.n && p.pair[b].x == pair[b - 1 - a].x;
-    const T *dy = (const T *)p.dy + col;
-    float *part = p.part + (int64_t)seg * 2 * p.width + col;
-    float acc[V];
-#pragma unroll
-    for (int j = 0; j < V; j++) acc[j] = 0.f;
-    bool first = true;   // the segment's first run
-    // pairs that are padding (or lie behind the list) load dy's first row, which nothing takes
-#pragma unroll 1
-    for (int j = 0; j < kSegment; j += kAhead) {
-        uint4 x[kAhead];
-#pragma unroll
-        for (int u = 0; u < kAhead; u++) {
-            const int2 q = pair[j + u];
-            x[u] = load16(dy + (int64_t)(q.x < p.vocab ? q.y : 0) * p.width);
+    const int col[2] = {vec * V, (two ? vec + half : vec) * V};
+    const T *dy = (const T *)p.dy;
+    auto fetch = [&](int j, int slot) {
+        if (j < s.end) {
+            const T *row = dy + (int64_t)(j < a + kSegment ? pair[j - a].y : p.pair[j].y) * p.width;
+            fetch16(&stage[slot][0][threadIdx.x], row + col[0]);
+            if (two) fetch16(&stage[slot][1][threadIdx.x], row + col[1]);
         }
+        fetch_group();
+    };
+    float2 acc[2][H];
+    auto clear = [&]() {
 #pragma unroll
-        for (int u = 0; u < kAhead; u++) {
-            const int k = pair[j + u].x;
-            if (k >= p.vocab) return;   // nothing but padding behind it
+        for (int c = 0; c < 2; c++)
+#pragma unroll
+            for (int e = 0; e < H; e++) acc[c][e] = make_float2(0.f, 0.f);
+    };
+    clear();
+    bool first = true;   // the segment's first run
+    // a run is over, with pair j
+    auto finish = [&](int j) {
+        const bool before = first && s.from_before, on = s.goes_on && j == s.end - 1;
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+            if (c && !two) continue;
             float f[V];
-            widen16(x[u], f);
+            const float scale = before || on ? 1.f : p.scale;
 #pragma unroll
-            for (int e = 0; e < V; e++) acc[e] += f[e];
-            const bool ends_here = a + j + u == b - 1;
-            if (!ends_here && pair[j + u + 1].x == k) continue;
-            // the run is over, or the segment
-            if (first && from_before) {
-                store_floats(part, acc);
-            } else if (ends_here && goes_on) {
-                store_floats(part + p.width, acc);
-            } else {
-#pragma unroll
-                for (int e = 0; e < V; e++) acc[e] *= p.scale;
-                store16((T *)p.dtable + (int64_t)k * p.width + col, acc);
+            for (int e = 0; e < H; e++) {
+                f[2 * e] = acc[c][e].x * scale;
+                f[2 * e + 1] = acc[c][e].y * scale;
             }
-            first = false;
+            if (before || on)
+                store_floats(p.part + ((int64_t)(seg0 + group) * 2 + !before) * p.width + col[c], f);
+            else
+                store16((T *)p.dtable + (int64_t)pair[min(j - a, kSegment - 1)].x * p.width + col[c], f);
+        }
+        first = false;
+        clear();
+    };
 #pragma unroll
-            for (int e = 0; e < V; e++) acc[e] = 0.f;
+    for (int u = 0; u < kStages; u++) fetch(s.begin + u, u);
+#pragma unroll 1
+    for (int j0 = s.begin; j0 < s.end; j0 += kStages) {
+#pragma unroll
+        for (int u = 0; u < kStages; u++) {
+            const int j = j0 + u;
+            if (j >= s.end) break;
+            fetch_wait<kStages - 1>();
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                if (c && !two) continue;
+                float2 f[H];
+                pairs_of(stage[u][c][threadIdx.x], f, T());
+#pragma unroll
+                for (int e = 0; e < H; e++) acc[c][e] = add2(acc[c][e], f[e]);
+            }
+            fetch(j + kStages, u);
+            if (j == s.end - 1 || (j < a + kSegment && (s.ends >> (j - a) & 1))) finish(j);
         }
     }
+    fetch_wait<0>();
 }
 
 // Four floats; volatile, so that a batch of loads stays ahead of the sums that
@@ -508,9 +627,7 @@ __device__ __forceinline__ void add_parts(const Sums &p, int a, int b, int col, 
         part += N * row;
     };
 #pragma unroll 1
-    for (; a + 16 <= b; a += 16) some(std::integral_constant<int, 16>());
-#pragma unroll 1
-    for (; a + 4 <= b; a += 4) some(std::integral_constant<int, 4>());
+    for (; a + 8 <= b; a += 8) some(std::integral_constant<int, 8>());
 #pragma unroll 1
     for (; a < b; a++) some(std::integral_constant<int, 1>());
 }
@@ -521,56 +638,47 @@ __device__ __forceinline__ void store_four(__nv_bfloat16 *p, const float4 &v) {
     store2(p + 2, make_float2(v.z, v.w));
 }
 
-constexpr int kLong = 64;   // segments of a run that one warp adds up alone, at most
+constexpr int kJoined = 64;   // segments that a block looks for long runs in
 
-// The tokens that go on beyond the segment they begin in: a warp for each
-// segment, 128 columns; the block's warps share a long run.
-// grid (blocks of kWarps segments, blocks of columns)
+// The long runs: the block's warps share the segments of each that begins in
+// the block's.  grid (blocks of kJoined segments, blocks of 128 columns)
 template <typename T>
-__global__ void __launch_bounds__(kThreads) joined_runs_kernel(Sums p) {
+__global__ void __launch_bounds__(kThreads) long_runs_kernel(Sums p) {
     __shared__ float4 sh[kWarps][32];
-    __shared__ int len[kWarps];
+    __shared__ int key_of[kJoined];   // of a long run that begins in the segment, or vocab
     next_grid_may_start();
     previous_grid_done();
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int seg = blockIdx.x * kWarps + w, col = (blockIdx.y * 32 + lane) * 4;
-    const bool live = col < p.width;
-    // segments behind this one that the run goes on into
-    int more = 0, k = p.vocab;
-    const int64_t b = (int64_t)(seg + 1) * kSegment;
-    if (b < p.n) {
-        k = p.pair[b - 1].x;
-        const int a = (int)b - kSegment;
-        if (k < p.vocab && p.pair[b].x == k && (a == 0 || p.pair[a - 1].x != k || p.pair[a].x != k))
-            more = (lower_bound(p.pair, p.n, k + 1) - 1) / kSegment - seg;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, col = (blockIdx.y * 32 + lane) * 4;
+    bool any = false;
+    if (threadIdx.x < kJoined) {
+        const int seg = blockIdx.x * kJoined + threadIdx.x;
+        const int64_t b = (int64_t)(seg + 1) * kSegment, a = b - kSegment;
+        int k = p.vocab;
+        if (b + kBeyond < p.n) {
+            const int first = p.pair[a].x, before = a ? p.pair[a - 1].x : -1, last = p.pair[b - 1].x, end = p.pair[b + kBeyond].x;
+            if (end == last && last < p.vocab && (first != last || before != last)) k = last;
+        }
+        key_of[threadIdx.x] = k;
+        any = k < p.vocab;
     }
-    float4 acc;
-    auto begin = [&](int s) { acc = live ? load_now(p.part + (2 * (int64_t)s + 1) * p.width + col) : make_float4(0.f, 0.f, 0.f, 0.f); };
-    auto finish = [&](int key) {
-        if (live)
-            store_four((T *)p.dtable + (int64_t)key * p.width + col,
-                       make_float4(acc.x * p.scale, acc.y * p.scale, acc.z * p.scale, acc.w * p.scale));
-    };
-    if (more > 0 && more <= kLong) {
-        begin(seg);
-        if (live) add_parts(p, seg + 1, seg + 1 + more, col, acc);
-        finish(k);
-    }
-    if (lane == 0) len[w] = more > kLong ? more : 0;
-    __syncthreads();
-    for (int x = 0; x < kWarps; x++) {
-        const int m = len[x];
-        if (!m) continue;
-        const int s = blockIdx.x * kWarps + x, per = (m + kWarps - 1) / kWarps;
-        if (w == 0) begin(s);
-        else acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (live) add_parts(p, s + 1 + min(m, w * per), s + 1 + min(m, (w + 1) * per), col, acc);
+    if (!__syncthreads_or(any)) return;
+    for (int x = 0; x < kJoined; x++) {
+        const int k = key_of[x];
+        if (k >= p.vocab) continue;
+        const int s = blockIdx.x * kJoined + x, m = (lower_bound(p.pair, p.n, k + 1) - 1) / kSegment - s;
+        const int per = (m + kWarps - 1) / kWarps;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (col < p.width) {
+            if (w == 0) acc = load_now(p.part + (2 * (int64_t)s + 1) * p.width + col);
+            add_parts(p, s + 1 + min(m, w * per), s + 1 + min(m, (w + 1) * per), col, acc);
+        }
         sh[w][lane] = acc;
         __syncthreads();
-        if (w == 0) {
+        if (w == 0 && col < p.width) {
 #pragma unroll
             for (int y = 1; y < kWarps; y++) add4(acc, sh[y][lane]);
-            finish(p.pair[(int64_t)(s + 1) * kSegment - 1].x);
+            store_four((T *)p.dtable + (int64_t)k * p.width + col,
+                       make_float4(acc.x * p.scale, acc.y * p.scale, acc.z * p.scale, acc.w * p.scale));
         }
         __syncthreads();
     }
@@ -651,8 +759,8 @@ int backward(const int32_t *tokens, int n, int vocab, int width, float scale, co
     if (rc) return rc;
     const int vecs = width / V;
     Sums q{p.out, dy, dtable, (float *)(ws + s.part), n, vocab, width, scale};
-    q.cols = std::min(vecs, kThreads);
-    q.groups = std::min(kThreads / q.cols, kMaxGroups);
+    q.cols = std::min(vecs, 2 * kThreads);
+    q.groups = std::min(kThreads / ((q.cols + 1) / 2), kMaxGroups);
     q.col_blocks = (vecs + q.cols - 1) / q.cols;
     const int64_t segments = segments_of(n), seg_blocks = (segments + q.groups - 1) / q.groups * q.col_blocks;
     q.split = split_of(vocab, vecs, kBlockVecs, kTableRows, sms);
@@ -662,8 +770,8 @@ int backward(const int32_t *tokens, int n, int vocab, int width, float scale, co
     q.seg_blocks = (int)seg_blocks;
     q.zero_blocks = (int)zero_blocks;
     rc = launch_early(segment_sums_kernel<T>, dim3((unsigned)(seg_blocks + zero_blocks)), kThreads, 0, 1, stream, q);
-    if (rc || segments < 2) return rc;
-    return launch_early(joined_runs_kernel<T>, dim3((unsigned)((segments + kWarps - 1) / kWarps), (unsigned)((width + 127) / 128)),
+    if (rc || n <= kSegment + kBeyond) return rc;   // no run can be long
+    return launch_early(long_runs_kernel<T>, dim3((unsigned)((segments + kJoined - 1) / kJoined), (unsigned)((width + 127) / 128)),
                         kThreads, 0, 1, stream, q);
 }
 
