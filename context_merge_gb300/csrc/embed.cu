@@ -118,6 +118,7 @@ struct Pass {
     const int2 *in;    // pairs (key, position); NULL: the first pass, which takes the tokens
     int2 *out;
     int32_t *counts;   // [passes][tiles][bins]
+    int *longs;        // set to 0 for the sums
     int n, tile, tiles, vocab, pass, passes, bits;
     __device__ __forceinline__ int32_t *counts_of(int which) const { return counts + ((int64_t)which * tiles << bits); }
     // The key of position i: its token, or vocab (behind all others) where it lies outside the table.
@@ -127,15 +128,17 @@ struct Pass {
     }
 };
 
-// The ranks of kSub keys (-1: none) among those of their warp with the same
-// digit, and in hist[warp][digit] how many there are.  The whole block calls it.
+// The ranks of keys (-1: none; `rounds` of them a lane) among those of their warp
+// with the same digit, and in hist[warp][digit] how many there are.  The whole
+// block calls it.
 __device__ __forceinline__ void rank_keys(const int (&key)[kPerLane], int (&rank)[kPerLane], uint16_t (*hist)[kMaxBins],
-                                          int shift, int bits) {
+                                          int rounds, int shift, int bits) {
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int d = lane; d < 1 << bits; d += 32) hist[w][d] = 0;
     __syncwarp();
 #pragma unroll
     for (int u = 0; u < kPerLane; u++) {
+        if (u >= rounds) break;
         const int digit = key[u] < 0 ? -1 : (key[u] >> shift) & ((1 << bits) - 1);
         const uint32_t same = __match_any_sync(0xffffffffu, digit);
         rank[u] = digit < 0 ? 0 : hist[w][digit] + __popc(same & ((1u << lane) - 1));
@@ -203,6 +206,7 @@ __global__ void __launch_bounds__(kSortThreads) digit_counts_kernel(Pass p) {
         p.counts[at] = hist[d];
         for (int i = 1; i < p.passes; i++) p.counts_of(i)[at] = 0;
     }
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.longs = 0;
 }
 
 __global__ void __launch_bounds__(kSortThreads) move_pairs_kernel(Pass p) {
@@ -259,7 +263,7 @@ __global__ void __launch_bounds__(kSortThreads) move_pairs_kernel(Pass p) {
         if (d < bins) place[d] += mine[x];
     }
     for (int i0 = a; i0 < b; i0 += kSub) {
-        rank_keys(key, rank, hist, shift, p.bits);
+        rank_keys(key, rank, hist, kPerLane, shift, p.bits);
         // hist becomes how many pairs of the digit the warps before have
         for (int d = threadIdx.x; d < bins; d += kSortThreads) {
             int before = 0;
@@ -297,16 +301,18 @@ __global__ void __launch_bounds__(kSortThreads) sort_few_kernel(Pass p) {
     uint16_t *places = (uint16_t *)(keys + kSub);
     next_grid_may_start();
     previous_grid_done();
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, first = w * 32 * kPerLane + lane, bins = 1 << p.bits;
+    // every warp has a stretch of the list, of `rounds` pairs a lane
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, bins = 1 << p.bits;
+    const int rounds = (p.n + kSortThreads - 1) / kSortThreads, first = w * 32 * rounds + lane;
     int key[kPerLane], pos[kPerLane], rank[kPerLane];
 #pragma unroll
     for (int u = 0; u < kPerLane; u++) {
         pos[u] = first + 32 * u;
-        key[u] = pos[u] < p.n ? p.key_of(pos[u]) : -1;
+        key[u] = u < rounds && pos[u] < p.n ? p.key_of(pos[u]) : -1;
     }
     for (int i = 0; i < p.passes; i++) {
         const int shift = i * p.bits;
-        rank_keys(key, rank, hist, shift, p.bits);
+        rank_keys(key, rank, hist, rounds, shift, p.bits);
         for (int d = threadIdx.x; d < bins; d += kSortThreads) {
             int before = 0;
 #pragma unroll
@@ -336,15 +342,17 @@ __global__ void __launch_bounds__(kSortThreads) sort_few_kernel(Pass p) {
 #pragma unroll
         for (int u = 0; u < kPerLane; u++) {
             const int j = first + 32 * u;
-            key[u] = j < p.n ? keys[j] : -1;
-            pos[u] = j < p.n ? places[j] : 0;
+            const bool mine = u < rounds && j < p.n;
+            key[u] = mine ? keys[j] : -1;
+            pos[u] = mine ? places[j] : 0;
         }
         __syncthreads();
     }
 #pragma unroll
     for (int u = 0; u < kPerLane; u++) {
         const int j = first + 32 * u;
-        if (j < p.n) p.out[j] = make_int2(key[u], pos[u]);
+        if (u < rounds && j < p.n) p.out[j] = make_int2(key[u], pos[u]);
+        if (j == 0) *p.longs = 0;
     }
 }
 
@@ -356,13 +364,14 @@ __global__ void __launch_bounds__(kSortThreads) sort_few_kernel(Pass p) {
 // and a second kernel adds those up.  Table rows that do not occur are
 // filled by blocks of their own, among the segments'.
 constexpr int kSegment = 32;   // a warp's lanes
-constexpr int kBeyond = 256;
+constexpr int kBeyond = 128;
 constexpr int kMaxGroups = 32;   // segments of a block, at most
 
 struct Sums {
     const int2 *pair;           // (key, position), sorted
     const void *dy;
     void *dtable;
+    int *longs;                 // how many long runs there are, and the segments that they begin in
     float *part;                // [segments][2][width]: a long run that comes from before, one that begins here
     int n, vocab, width;
     float scale;
@@ -524,7 +533,11 @@ __global__ void __launch_bounds__(kThreads, 5) segment_sums_kernel(Sums p) {
     __syncthreads();
     for (int g = threadIdx.x >> 5; g < p.groups; g += kWarps) {
         const Plan s = plan_of(p, pairs + g * kSegment, seg0 + g);
-        if ((threadIdx.x & 31) == 0) plans[g] = s;
+        if ((threadIdx.x & 31) == 0) {
+            plans[g] = s;
+            // the list's order does not matter: every run is added up by itself
+            if (s.goes_on && at % p.col_blocks == 0) p.longs[1 + atomicAdd(p.longs, 1)] = seg0 + g;
+        }
     }
     __syncthreads();
     const int half = (p.cols + 1) / 2, group = threadIdx.x / half, mine = threadIdx.x % half;
@@ -638,34 +651,18 @@ __device__ __forceinline__ void store_four(__nv_bfloat16 *p, const float4 &v) {
     store2(p + 2, make_float2(v.z, v.w));
 }
 
-constexpr int kJoined = 64;   // segments that a block looks for long runs in
-
-// The long runs: the block's warps share the segments of each that begins in
-// the block's.  grid (blocks of kJoined segments, blocks of 128 columns)
+// The long runs, 128 columns at a time: the block's warps share a run's segments.
+// grid: blocks that take the listed runs in turn
 template <typename T>
 __global__ void __launch_bounds__(kThreads) long_runs_kernel(Sums p) {
     __shared__ float4 sh[kWarps][32];
-    __shared__ int key_of[kJoined];   // of a long run that begins in the segment, or vocab
     next_grid_may_start();
     previous_grid_done();
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, col = (blockIdx.y * 32 + lane) * 4;
-    bool any = false;
-    if (threadIdx.x < kJoined) {
-        const int seg = blockIdx.x * kJoined + threadIdx.x;
-        const int64_t b = (int64_t)(seg + 1) * kSegment, a = b - kSegment;
-        int k = p.vocab;
-        if (b + kBeyond < p.n) {
-            const int first = p.pair[a].x, before = a ? p.pair[a - 1].x : -1, last = p.pair[b - 1].x, end = p.pair[b + kBeyond].x;
-            if (end == last && last < p.vocab && (first != last || before != last)) k = last;
-        }
-        key_of[threadIdx.x] = k;
-        any = k < p.vocab;
-    }
-    if (!__syncthreads_or(any)) return;
-    for (int x = 0; x < kJoined; x++) {
-        const int k = key_of[x];
-        if (k >= p.vocab) continue;
-        const int s = blockIdx.x * kJoined + x, m = (lower_bound(p.pair, p.n, k + 1) - 1) / kSegment - s;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, col_blocks = (p.width + 127) / 128;
+    const int64_t items = (int64_t)*p.longs * col_blocks;
+    for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+        const int s = p.longs[1 + i / col_blocks], col = ((int)(i % col_blocks) * 32 + lane) * 4;
+        const int k = p.pair[(int64_t)(s + 1) * kSegment - 1].x, m = (lower_bound(p.pair, p.n, k + 1) - 1) / kSegment - s;
         const int per = (m + kWarps - 1) / kWarps;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         if (col < p.width) {
@@ -702,13 +699,14 @@ int64_t segments_of(int64_t n) { return (n + kSegment - 1) / kSegment; }
 
 // The workspace: two lists of pairs, the passes' counts, the segments' sums.
 struct Space {
-    size_t list, counts, part, bytes;
+    size_t list, counts, longs, part, bytes;
 };
 Space space(int64_t n, int width) {
     Space s{};
     s.list = round256((size_t)n * sizeof(int2));
     s.counts = (n > kSub ? 2 : 1) * s.list;
-    s.part = s.counts + (n > kSub ? (size_t)kMaxPasses * kMaxTiles * kMaxBins * 4 : 0);
+    s.longs = s.counts + (n > kSub ? (size_t)kMaxPasses * kMaxTiles * kMaxBins * 4 : 0);
+    s.part = s.longs + round256((size_t)(1 + n / (kBeyond + 1)) * 4);
     s.bytes = s.part + (size_t)segments_of(n) * 2 * (size_t)width * 4;
     return s;
 }
@@ -739,6 +737,7 @@ int backward(const int32_t *tokens, int n, int vocab, int width, float scale, co
     p.tokens = tokens;
     p.out = list[0];
     p.counts = (int32_t *)(ws + s.counts);
+    p.longs = (int *)(ws + s.longs);
     p.n = n;
     p.tile = tile_of(n);
     p.tiles = (n + p.tile - 1) / p.tile;
@@ -758,7 +757,7 @@ int backward(const int32_t *tokens, int n, int vocab, int width, float scale, co
     }
     if (rc) return rc;
     const int vecs = width / V;
-    Sums q{p.out, dy, dtable, (float *)(ws + s.part), n, vocab, width, scale};
+    Sums q{p.out, dy, dtable, p.longs, (float *)(ws + s.part), n, vocab, width, scale};
     q.cols = std::min(vecs, 2 * kThreads);
     q.groups = std::min(kThreads / ((q.cols + 1) / 2), kMaxGroups);
     q.col_blocks = (vecs + q.cols - 1) / q.cols;
@@ -771,8 +770,9 @@ int backward(const int32_t *tokens, int n, int vocab, int width, float scale, co
     q.zero_blocks = (int)zero_blocks;
     rc = launch_early(segment_sums_kernel<T>, dim3((unsigned)(seg_blocks + zero_blocks)), kThreads, 0, 1, stream, q);
     if (rc || n <= kSegment + kBeyond) return rc;   // no run can be long
-    return launch_early(long_runs_kernel<T>, dim3((unsigned)((segments + kJoined - 1) / kJoined), (unsigned)((width + 127) / 128)),
-                        kThreads, 0, 1, stream, q);
+    // no more blocks than the longest possible list has items, and a wave of them
+    const int64_t most = n / (kBeyond + 1) * ((width + 127) / 128);
+    return launch_early(long_runs_kernel<T>, dim3((unsigned)std::min<int64_t>(most, 6 * sms)), kThreads, 0, 1, stream, q);
 }
 
 template <typename T>

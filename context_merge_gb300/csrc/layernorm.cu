@@ -97,91 +97,106 @@ struct FwdParams {
     float eps, inv_width;
 };
 
-// grid: row blocks of kBlock / TPR rows
+// Blocks of an SM that the forward's registers leave room for.
+template <typename T, int TPR, int NV>
+constexpr int fwd_per_sm() {
+    constexpr int regs = kVecOf<T> == 8 ? (NV == 1 ? 48 : NV == 2 ? 64 : NV == 3 ? 80 : 128)
+                                        : (NV <= 2 ? 48 : NV == 3 ? 56 : NV == 4 ? 64 : 128);
+    constexpr int n = 65536 / (regs * kBlock<TPR>);
+    return n < 1 ? 1 : n;
+}
+
+// persistent: each group of TPR threads takes every (gridDim.x * groups)-th row,
+// whose loads go out before the reductions of the row before it.
 template <typename T, int TPR, int NV, bool E4M3>
-__global__ void __launch_bounds__(kBlock<TPR>) layernorm_fwd_kernel(FwdParams p) {
-    constexpr int V = kVecOf<T>, W = kBlock<TPR> / 32;
+__global__ void __launch_bounds__(kBlock<TPR>, fwd_per_sm<T, TPR, NV>()) layernorm_fwd_kernel(FwdParams p) {
+    constexpr int V = kVecOf<T>, W = kBlock<TPR> / 32, G = kBlock<TPR> / TPR;
     __shared__ float sh1[W][1], sh2[W][2], sh3[W];
     next_grid_may_start();
     previous_grid_done();
-    const int64_t row = (int64_t)blockIdx.x * (kBlock<TPR> / TPR) + threadIdx.x / TPR;
     const int t = threadIdx.x % TPR;
-    const bool live = row < p.rows;
-    const int64_t o = row * p.width;
-    const T *x = (const T *)p.x + o;
-    const T *res = p.res ? (const T *)p.res + o : nullptr;
+    const int64_t stride = (int64_t)gridDim.x * G;
+    int64_t row = (int64_t)blockIdx.x * G + threadIdx.x / TPR;
     uint4 xr[NV], rr[NV];
-#pragma unroll
-    for (int i = 0; i < NV; i++) {
-        const int col = (i * TPR + t) * V;
-        xr[i] = rr[i] = make_uint4(0, 0, 0, 0);
-        if (live && col < p.width) {
-            xr[i] = load16(x + col);
-            if (res) rr[i] = load16(res + col);
-        }
-    }
-    float s[NV][V];
-    float sum[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < NV; i++) {
-        const int col = (i * TPR + t) * V;
-        widen16(xr[i], s[i]);
-        if (res) {
-            float r[V];
-            widen16(rr[i], r);
-#pragma unroll
-            for (int j = 0; j < V; j++) s[i][j] += r[j];
-        }
-        if (live && col < p.width && p.s) store16((T *)p.s + o + col, s[i]);
-#pragma unroll
-        for (int j = 0; j < V; j++) sum[0] += s[i][j];
-    }
-    row_sums<TPR>(sum, sh1);
-    const float mean = sum[0] * p.inv_width;
-    float st[2] = {0.f, 0.f};   // differences to the mean, and their squares
-#pragma unroll
-    for (int i = 0; i < NV; i++) {
-        if ((i * TPR + t) * V < p.width) {
-#pragma unroll
-            for (int j = 0; j < V; j++) {
-                s[i][j] -= mean;
-                st[0] += s[i][j];
-                st[1] = fmaf(s[i][j], s[i][j], st[1]);
-            }
-        }
-    }
-    row_sums<TPR>(st, sh2);
-    const float off = st[0] * p.inv_width;
-    const float rstd = rsqrtf(max_nan(fmaf(-off, off, st[1] * p.inv_width), 0.f) + p.eps);
-    float big = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; i++) {
-        const int col = (i * TPR + t) * V;
-        if (col >= p.width) continue;
-        float w[V], b[V];
-        load_floats(p.w + col, w);
-#pragma unroll
-        for (int j = 0; j < V; j++) b[j] = 0.f;
-        if (p.b) load_floats(p.b + col, b);
-#pragma unroll
-        for (int j = 0; j < V; j++) {
-            s[i][j] = fmaf((s[i][j] - off) * rstd, w[j], b[j]);
-            if (E4M3) big = max_nan(big, fabsf(s[i][j]));
-        }
-        if (live && p.y) store16((T *)p.y + o + col, s[i]);
-    }
-    if (E4M3) {
-        const float scale = max_nan(row_max<TPR>(big, sh3) / kE4m3Max, 1.17549435e-38f);
-        if (!live) return;
-        const float inv = 1.f / scale;
-        if (t == 0) p.scale[row] = scale;
+    auto load = [&](int64_t at) {
+        const T *x = (const T *)p.x + at * p.width, *res = p.res ? (const T *)p.res + at * p.width : nullptr;
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             const int col = (i * TPR + t) * V;
-            if (col < p.width) store_e4m3(p.y8 + o + col, s[i], inv);
+            xr[i] = rr[i] = make_uint4(0, 0, 0, 0);
+            if (at < p.rows && col < p.width) {
+                xr[i] = load16(x + col);
+                if (res) rr[i] = load16(res + col);
+            }
         }
+    };
+    load(row);
+    // every group of the block makes the same number of turns (the barriers)
+    for (int64_t base = (int64_t)blockIdx.x * G; base < p.rows; base += stride, row += stride) {
+        const bool live = row < p.rows;
+        const int64_t o = row * p.width;
+        float s[NV][V];
+        float sum[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int col = (i * TPR + t) * V;
+            widen16(xr[i], s[i]);
+            if (p.res) {
+                float r[V];
+                widen16(rr[i], r);
+#pragma unroll
+                for (int j = 0; j < V; j++) s[i][j] += r[j];
+            }
+            if (live && col < p.width && p.s) store16((T *)p.s + o + col, s[i]);
+#pragma unroll
+            for (int j = 0; j < V; j++) sum[0] += s[i][j];
+        }
+        load(row + stride);
+        row_sums<TPR>(sum, sh1);
+        const float mean = sum[0] * p.inv_width;
+        float st[2] = {0.f, 0.f};   // differences to the mean, and their squares
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            if ((i * TPR + t) * V < p.width) {
+#pragma unroll
+                for (int j = 0; j < V; j++) {
+                    s[i][j] -= mean;
+                    st[0] += s[i][j];
+                    st[1] = fmaf(s[i][j], s[i][j], st[1]);
+                }
+            }
+        }
+        row_sums<TPR>(st, sh2);
+        const float off = st[0] * p.inv_width;
+        const float rstd = rsqrtf(max_nan(fmaf(-off, off, st[1] * p.inv_width), 0.f) + p.eps);
+        float big = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int col = (i * TPR + t) * V;
+            if (col >= p.width) continue;
+            float w[V], b[V];
+            load_floats(p.w + col, w);
+#pragma unroll
+            for (int j = 0; j < V; j++) b[j] = 0.f;
+            if (p.b) load_floats(p.b + col, b);
+#pragma unroll
+            for (int j = 0; j < V; j++) {
+                s[i][j] = fmaf((s[i][j] - off) * rstd, w[j], b[j]);
+                if (E4M3) big = max_nan(big, fabsf(s[i][j]));
+            }
+            if (live && p.y) store16((T *)p.y + o + col, s[i]);
+        }
+        if (E4M3) {
+            const float scale = max_nan(row_max<TPR>(big, sh3) / kE4m3Max, 1.17549435e-38f);
+            const float inv = 1.f / scale;
+            if (live && t == 0) p.scale[row] = scale;
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                const int col = (i * TPR + t) * V;
+                if (live && col < p.width) store_e4m3(p.y8 + o + col, s[i], inv);
+            }
+        }    }
     }
-}
 
 struct BwdParams {
     const void *s, *dy, *dsum;
@@ -193,15 +208,24 @@ struct BwdParams {
     float eps, inv_width;
 };
 
-template <int TPR>
-constexpr int kBwdPerSm = kBlock<TPR> > 256 ? 1 : 2;
+// Blocks of an SM that the backward's registers leave room for.
+template <typename T, int TPR, int NV>
+constexpr int bwd_per_sm() {
+    constexpr int regs = kVecOf<T> == 8 ? (NV == 1 ? 80 : 128) : (NV == 1 ? 64 : NV == 2 ? 80 : NV == 3 ? 104 : 128);
+    constexpr int n = 65536 / (regs * kBlock<TPR>);
+    return n < 1 ? 1 : n;
+}
+// The next row's loads go out before this one's reductions where registers allow.
+template <typename T, int NV>
+constexpr bool kBwdAhead = kVecOf<T> == 8 ? NV == 1 : NV <= 2;
 
 // persistent: each group of TPR threads takes every (gridDim.x * groups)-th
 // row and sums its rows' dw and db terms in registers; the block's sums go to its row of `part`.
 template <typename T, int TPR, int NV>
-__global__ void __launch_bounds__(kBlock<TPR>, kBwdPerSm<TPR>) layernorm_bwd_kernel(BwdParams p) {
+__global__ void __launch_bounds__(kBlock<TPR>, bwd_per_sm<T, TPR, NV>()) layernorm_bwd_kernel(BwdParams p) {
     constexpr int V = kVecOf<T>, W = kBlock<TPR> / 32;
     constexpr int G = kBlock<TPR> / TPR, ROW = TPR * NV * V;
+    constexpr bool AHEAD = kBwdAhead<T, NV>;
     __shared__ float sh1[W][2], sh2[W][3];
     extern __shared__ __align__(16) float row_sh[];   // ROW weights; at the end the groups' sums
     next_grid_may_start();
@@ -209,34 +233,41 @@ __global__ void __launch_bounds__(kBlock<TPR>, kBwdPerSm<TPR>) layernorm_bwd_ker
     const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
     const int64_t stride = (int64_t)gridDim.x * G;
     const T *sp = (const T *)p.s, *dyp = (const T *)p.dy, *dsp = (const T *)p.dsum;
-    for (int i = threadIdx.x; i < ROW; i += kBlock<TPR>) row_sh[i] = i < p.width ? p.w[i] : 0.f;
-    float dw[NV][V], db[NV][V];
-#pragma unroll
-    for (int i = 0; i < NV; i++)
-#pragma unroll
-        for (int j = 0; j < V; j++) dw[i][j] = db[i][j] = 0.f;
-    __syncthreads();
+    struct Raw {
+        uint4 s[NV], d[NV], u[NV];
+    } cur, next;
     int64_t row = (int64_t)blockIdx.x * G + grp;
-    // every group of the block makes the same number of turns (the barriers)
-    for (int64_t base = (int64_t)blockIdx.x * G; base < p.rows; base += stride, row += stride) {
-        uint4 sr[NV], dr[NV], ur[NV];
+    auto load = [&](Raw &r, int64_t at) {
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             const int col = (i * TPR + t) * V;
-            sr[i] = dr[i] = ur[i] = make_uint4(0, 0, 0, 0);
-            if (row < p.rows && col < p.width) {
-                const int64_t o = row * p.width + col;
-                sr[i] = load16(sp + o);
-                dr[i] = load16(dyp + o);
-                if (dsp) ur[i] = load16(dsp + o);
+            r.s[i] = r.d[i] = r.u[i] = make_uint4(0, 0, 0, 0);
+            if (at < p.rows && col < p.width) {
+                const int64_t o = at * p.width + col;
+                r.s[i] = load16(sp + o);
+                r.d[i] = load16(dyp + o);
+                if (dsp) r.u[i] = load16(dsp + o);
             }
         }
+    };
+    if (AHEAD) load(cur, row);
+    for (int i = threadIdx.x; i < ROW; i += kBlock<TPR>) row_sh[i] = i < p.width ? p.w[i] : 0.f;
+    float2 dw[NV][V / 2], db[NV][V / 2];
+#pragma unroll
+    for (int i = 0; i < NV; i++)
+#pragma unroll
+        for (int j = 0; j < V / 2; j++) dw[i][j] = db[i][j] = make_float2(0.f, 0.f);
+    __syncthreads();
+    // every group of the block makes the same number of turns (the barriers)
+    for (int64_t base = (int64_t)blockIdx.x * G; base < p.rows; base += stride, row += stride) {
+        if (AHEAD) load(next, row + stride);
+        else load(cur, row);
         float one[2] = {0.f, 0.f};   // sums of s and u
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             float s[V], d[V], w[V];
-            widen16(sr[i], s);
-            widen16(dr[i], d);
+            widen16(cur.s[i], s);
+            widen16(cur.d[i], d);
             load_floats(row_sh + (i * TPR + t) * V, w);
 #pragma unroll
             for (int j = 0; j < V; j++) {
@@ -251,8 +282,8 @@ __global__ void __launch_bounds__(kBlock<TPR>, kBwdPerSm<TPR>) layernorm_bwd_ker
         for (int i = 0; i < NV; i++) {
             if ((i * TPR + t) * V >= p.width) continue;
             float s[V], d[V], w[V];
-            widen16(sr[i], s);
-            widen16(dr[i], d);
+            widen16(cur.s[i], s);
+            widen16(cur.d[i], d);
             load_floats(row_sh + (i * TPR + t) * V, w);
 #pragma unroll
             for (int j = 0; j < V; j++) {
@@ -272,29 +303,36 @@ __global__ void __launch_bounds__(kBlock<TPR>, kBwdPerSm<TPR>) layernorm_bwd_ker
         for (int i = 0; i < NV; i++) {
             const int col = (i * TPR + t) * V;
             float s[V], d[V], u[V], w[V], ds[V];
-            widen16(sr[i], s);
-            widen16(dr[i], d);
-            widen16(ur[i], u);
+            widen16(cur.s[i], s);
+            widen16(cur.d[i], d);
+            widen16(cur.u[i], u);
             load_floats(row_sh + (i * TPR + t) * V, w);
 #pragma unroll
-            for (int j = 0; j < V; j++) {
-                const float xh = ((s[j] - mean) - off) * rstd;
-                dw[i][j] = fmaf(d[j], xh, dw[i][j]);
-                db[i][j] += d[j];
-                ds[j] = fmaf(rstd, fmaf(w[j], d[j], -mu) - xh * dot, u[j]);
+            for (int j = 0; j < V; j += 2) {
+                const float2 xh = make_float2(((s[j] - mean) - off) * rstd, ((s[j + 1] - mean) - off) * rstd);
+                const float2 dd = make_float2(d[j], d[j + 1]);
+                dw[i][j / 2] = fma2(dd, xh, dw[i][j / 2]);
+                db[i][j / 2] = add2(db[i][j / 2], dd);
+                ds[j] = fmaf(rstd, fmaf(w[j], d[j], -mu) - xh.x * dot, u[j]);
+                ds[j + 1] = fmaf(rstd, fmaf(w[j + 1], d[j + 1], -mu) - xh.y * dot, u[j + 1]);
             }
             if (row < p.rows && col < p.width) store16((T *)p.ds + row * p.width + col, ds);
         }
+        if (AHEAD) cur = next;
     }
     float *part = p.part + (int64_t)blockIdx.x * 2 * p.width;
 #pragma unroll
     for (int which = 0; which < 2; which++) {
+        auto value = [&](int i, int j) {
+            const float2 v = which ? db[i][j / 2] : dw[i][j / 2];
+            return j & 1 ? v.y : v.x;
+        };
         if (G > 1) {
             __syncthreads();   // the weights, or the sums before, have been read
 #pragma unroll
             for (int i = 0; i < NV; i++)
 #pragma unroll
-                for (int j = 0; j < V; j++) row_sh[grp * ROW + (i * TPR + t) * V + j] = which ? db[i][j] : dw[i][j];
+                for (int j = 0; j < V; j++) row_sh[grp * ROW + (i * TPR + t) * V + j] = value(i, j);
             __syncthreads();
             for (int col = threadIdx.x; col < p.width; col += kBlock<TPR>) {
                 float v = 0.f;
@@ -307,17 +345,16 @@ __global__ void __launch_bounds__(kBlock<TPR>, kBwdPerSm<TPR>) layernorm_bwd_ker
                 const int col = (i * TPR + t) * V;
 #pragma unroll
                 for (int j = 0; j < V; j++)
-                    if (col < p.width) part[which * p.width + col + j] = which ? db[i][j] : dw[i][j];
+                    if (col < p.width) part[which * p.width + col + j] = value(i, j);
             }
         }
     }
 }
 
 template <typename T, int TPR, int NV>
-int fwd(const FwdParams &p, void *st) {
+int fwd(const FwdParams &p, int sms, void *st) {
     constexpr int per = kBlock<TPR> / TPR;
-    const int64_t grid = (p.rows + per - 1) / per;
-    if (grid > (int64_t)0x7fffffff) return (int)cudaErrorInvalidValue;
+    const int64_t grid = std::min<int64_t>((p.rows + per - 1) / per, (int64_t)sms * fwd_per_sm<T, TPR, NV>());
     return launch_early(p.y8 ? layernorm_fwd_kernel<T, TPR, NV, true> : layernorm_fwd_kernel<T, TPR, NV, false>,
                         dim3((unsigned)grid), kBlock<TPR>, 0, 1, st, p);
 }
@@ -325,16 +362,24 @@ int fwd(const FwdParams &p, void *st) {
 template <typename T, int TPR, int NV>
 int bwd(const BwdParams &p, int grid, float *dw, float *db, void *st) {
     constexpr size_t smem = (size_t)kBlock<TPR> * NV * kVecOf<T> * sizeof(float);
-    static_assert(smem * kBwdPerSm<TPR> <= 220 * 1024, "the blocks of an SM fit its shared memory");
+    static_assert(smem * bwd_per_sm<T, TPR, NV>() <= 220 * 1024, "the blocks of an SM fit its shared memory");
     const int rc = launch_early(layernorm_bwd_kernel<T, TPR, NV>, dim3((unsigned)grid), kBlock<TPR>, smem, 1, st, p);
     if (rc) return rc;
     return launch_column_sums2(p.part, grid, p.width, dw, db, st);
 }
 
-// Threads and vectors of a row of the backward, which holds dw and db.
+// Threads and vectors of a row of the backward, which holds dw and db: one
+// bf16 vector a thread as long as 512 threads do.
 template <typename T, typename F>
 int by_width_bwd(int width, F f) {
     const int vecs = (width + kVecOf<T> - 1) / kVecOf<T>;
+    if constexpr (kVecOf<T> == 8) {
+        if (vecs > 48 && vecs <= 64) return with<64, 1>(f);
+        if (vecs > 96 && vecs <= 128) return with<128, 1>(f);
+        if (vecs > 192 && vecs <= 256) return with<256, 1>(f);
+        if (vecs > 256 && vecs <= 512) return with<512, 1>(f);
+        if (vecs > 512 && vecs <= 1024) return with<512, 2>(f);
+    }
     if (vecs <= 768) return narrow_row<T>(vecs, f);
     if (vecs <= 1024) return with<512, 2>(f);
     if (vecs <= 1536) return with<512, 3>(f);
@@ -352,8 +397,7 @@ Shape bwd_shape(int width) {
     Shape s{};
     by_width_bwd<T>(width, [&](auto tpr, auto nv) {
         constexpr int TPR = decltype(tpr)::value;
-        (void)nv;
-        s = Shape{kBlock<TPR> / TPR, kBwdPerSm<TPR>};
+        s = Shape{kBlock<TPR> / TPR, bwd_per_sm<T, TPR, decltype(nv)::value>()};
         return CPDR_OK;
     });
     return s;
@@ -368,12 +412,13 @@ int launch_layernorm_fwd(const cpdr_ctx *c, int64_t rows, int width, const void 
                          float *scale, void *stream) {
     if (rows == 0) return 0;
     const FwdParams p{x, residual, weight, bias, sum_out, y, (uint8_t *)y8, scale, rows, width, eps, 1.f / (float)width};
+    const int sms = device_sms(c->device);
     if (c->plan.in_dtype == CPDR_DTYPE_F32)
         return by_width<float>(width, [&](auto tpr, auto nv) {
-            return fwd<float, decltype(tpr)::value, decltype(nv)::value>(p, stream);
+            return fwd<float, decltype(tpr)::value, decltype(nv)::value>(p, sms, stream);
         });
     return by_width<__nv_bfloat16>(width, [&](auto tpr, auto nv) {
-        return fwd<__nv_bfloat16, decltype(tpr)::value, decltype(nv)::value>(p, stream);
+        return fwd<__nv_bfloat16, decltype(tpr)::value, decltype(nv)::value>(p, sms, stream);
     });
 }
 
