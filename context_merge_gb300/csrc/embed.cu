@@ -480,15 +480,6 @@ __device__ __forceinline__ Plan plan_of(const Sums &p, const int2 *pair, int seg
 // of each: 5 blocks of an SM have 160 KB in flight.
 constexpr int kStages = 4;
 
-__device__ __forceinline__ void fetch16(void *to, const void *from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
-}
-__device__ __forceinline__ void fetch_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void fetch_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // The values of a vector, in pairs.
 __device__ __forceinline__ void pairs_of(const uint4 &r, float2 (&v)[2], float) {
     v[0] = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));

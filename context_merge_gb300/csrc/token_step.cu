@@ -29,7 +29,14 @@ namespace {
 using namespace vio;
 
 constexpr int kThreads = 128, kWarps = kThreads / 32;
-constexpr int kSlice = 32;   // value dims of a CTA
+constexpr int kSlice = 32;   // value dims of a CTA with [dv, dk] states
+constexpr int kWide = 64;    // and with [dk, dv] states
+// CTAs of an SM that the registers leave room for
+template <int D>
+constexpr int kStepPerSm = D == 128 ? 3 : 4;
+template <typename T>
+constexpr int kVfirstPerSm[5] = {0, sizeof(T) == 2 ? 5 : 4, sizeof(T) == 2 ? 5 : 4, 0, sizeof(T) == 2 ? 4 : 3};
+constexpr int kMaxRows[2] = {2, 4};   // rows of a CTA with [dk, dv] and [dv, dk] states, at most (a warp's lanes)
 
 __device__ __forceinline__ float at(const float *p, int64_t i) { return p[i]; }
 __device__ __forceinline__ float at(const __nv_bfloat16 *p, int64_t i) { return __bfloat162float(p[i]); }
@@ -47,7 +54,7 @@ struct Rows {
         : slots(slots), n(n), slot(slot), last(last), base(row + 1), found(0) {}
     // The row behind row j, n when there is none; the whole warp calls it.
     __device__ __forceinline__ int next(int j) {
-        if (j >= last) return n;
+        if (j >= last) return n;   // n itself among them
         while (!found) {
             if (base > last) return n;   // only if the slots changed meanwhile
             const int i = base + (threadIdx.x & 31);
@@ -98,60 +105,20 @@ struct Params {
     void *o;
     int n, num_slots, H, G;
     float scale;
+    int rows;   // of a CTA
 };
 
-// This CTA's row has a slot, and the row before has another one.
-__device__ __forceinline__ bool slot_of(const Params &p, int row, int &slot) {
+// The rows of a CTA that may be the first of their slot: they have one, and the
+// row before has another.  Bit i: row `row0` + i; `slot` is lane i's.
+__device__ __forceinline__ uint32_t first_rows(const Params &p, int row0, int &slot) {
+    const int lane = threadIdx.x & 31, row = row0 + lane;
+    const bool mine = lane < p.rows && row < p.n;
     slot = row;
-    if (!p.slots) return true;
-    slot = p.slots[row];
-    const int before = row ? p.slots[row - 1] : -1;
-    return slot >= 0 && slot < p.num_slots && slot != before;
+    if (!p.slots) return __ballot_sync(0xffffffffu, mine);
+    slot = mine ? p.slots[row] : -1;
+    const int before = mine && row ? p.slots[row - 1] : -1;
+    return __ballot_sync(0xffffffffu, slot >= 0 && slot < p.num_slots && slot != before);
 }
-
-// A token as the [dk, dv] kernel reads it: k, q and the gate's factors as pairs of the
-// same value, for packed arithmetic.
-template <int D, bool KDA, int GP>
-struct Token {
-    alignas(16) float2 k[D], q[GP][D], a[KDA ? D : 1];
-    alignas(16) float v[kSlice];   // read four at a time
-    float beta;
-};
-// What one thread fetches of it.
-template <typename T, int D, bool KDA, int GP>
-struct Fetch {
-    T kq[GP + 1], v, beta;
-    float a;
-    __device__ __forceinline__ void load(const Params &p, int row, int h, int v0) {
-        const int t = threadIdx.x;
-        const int64_t hk = (int64_t)row * p.H + h, hq = hk * p.G;
-        if (t < D) {
-            kq[GP] = ((const T *)p.k)[hk * D + t];
-#pragma unroll
-            for (int g = 0; g < GP; g++) kq[g] = g < p.G ? ((const T *)p.q)[(hq + g) * D + t] : T(0.f);
-            if (KDA) a = p.g[hk * D + t];
-        }
-        if (t < kSlice) v = ((const T *)p.v)[hk * D + v0 + t];
-        if (t == kThreads - 1) {
-            beta = ((const T *)p.beta)[hk];
-            if (!KDA) a = p.g[hk];
-        }
-    }
-    __device__ __forceinline__ void store(Token<D, KDA, GP> &s) const {
-        const int t = threadIdx.x;
-        if (t < D) {
-            s.k[t] = both((float)kq[GP]);
-#pragma unroll
-            for (int g = 0; g < GP; g++) s.q[g][t] = both((float)kq[g]);
-            if (KDA) s.a[t] = both(expf(a));
-        }
-        if (t < kSlice) s.v[t] = (float)v;
-        if (t == kThreads - 1) {
-            s.beta = (float)beta;
-            if (!KDA) s.a[0] = both(expf(a));
-        }
-    }
-};
 
 // Four columns of a row.
 struct Quad {
@@ -163,154 +130,6 @@ __device__ __forceinline__ void fma(Quad &c, float2 a, const Quad &b) {
     c.y = fma2(a, b.y, c.y);
 }
 
-// [dk, dv] states.  A thread holds four columns of the slice (lane % 8) and
-// every 16th row: sums over rows go over four lanes of a warp and the four warps.
-// A token's vectors are fetched by one thread per dim while the token before
-// runs.  GP: query heads of the first round, which shares its reduction with P^T k.
-constexpr int kStepPerSm[5] = {0, 5, 4, 0, 3};   // CTAs of an SM, by GP
-template <typename T, int D, bool KDA, int GP>
-__global__ void __launch_bounds__(kThreads, kStepPerSm[GP]) delta_step_kernel(Params p) {
-    constexpr int N = D / (4 * kWarps);           // rows of a thread
-    constexpr int R = 4 * (1 + GP) + GP;          // sums of a thread: P^T k, P^T q, q . k
-    constexpr int RP = (R + 3) / 4 * 4;
-    __shared__ int shared_last[kWarps][1];
-    __shared__ Token<D, KDA, GP> tok[2];
-    __shared__ __align__(16) float red[2][kWarps][8][RP];
-    next_grid_may_start();
-    previous_grid_done();
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int h = blockIdx.x / (D / kSlice), v0 = blockIdx.x % (D / kSlice) * kSlice, c0 = (lane & 7) * 4;
-    const int row = blockIdx.y;
-    Fetch<T, D, KDA, GP> f;
-    f.load(p, row, h, v0);
-    int slot[1], last[1];
-    if (!slot_of(p, row, slot[0])) return;
-    const int64_t so = ((int64_t)slot[0] * p.H + h) * D * D + v0 + c0;
-    const int k0 = w * 4 + (lane >> 3);           // rows k0 + 16 i
-    Quad S[N];
-#pragma unroll
-    for (int i = 0; i < N; i++) {
-        const float4 x = *reinterpret_cast<const float4 *>(p.state + so + (k0 + 16 * i) * D);
-        S[i] = Quad{make_float2(x.x, x.y), make_float2(x.z, x.w)};
-    }
-    f.store(tok[0]);
-    last[0] = row;
-    if (p.slots) last_rows<1>(p.slots, p.n, slot, row, last, shared_last);
-    else __syncthreads();
-    if (last[0] == kEarlier) return;
-    Rows rows(p.slots, p.n, slot[0], row, last[0]);
-    int par = 0, turn = 0;
-    for (int j = row; j < p.n; turn ^= 1) {
-        const int next = rows.next(j);
-        if (next < p.n) f.load(p, next, h, v0);
-        const Token<D, KDA, GP> &t = tok[turn];
-        const int64_t hq = ((int64_t)j * p.H + h) * p.G;
-        Quad a{}, b[GP];
-        float qk[GP];
-#pragma unroll
-        for (int g = 0; g < GP; g++) {
-            b[g] = Quad{};
-            qk[g] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-            const float2 k = t.k[k0 + 16 * i];
-            S[i] = mul(t.a[KDA ? k0 + 16 * i : 0], S[i]);
-            fma(a, k, S[i]);
-#pragma unroll
-            for (int g = 0; g < GP; g++) {
-                const float2 q = t.q[g][k0 + 16 * i];
-                fma(b[g], q, S[i]);
-                qk[g] = fmaf(q.x, k.x, qk[g]);
-            }
-        }
-        float r[RP] = {};
-        auto lay = [&](int i, const Quad &x) {
-            r[i] = x.x.x;
-            r[i + 1] = x.x.y;
-            r[i + 2] = x.y.x;
-            r[i + 3] = x.y.y;
-        };
-        auto sum = [&](int count) {
-#pragma unroll
-            for (int i = 0; i < RP; i++) {
-                if (i >= count) continue;
-                r[i] += __shfl_xor_sync(0xffffffffu, r[i], 8);
-                r[i] += __shfl_xor_sync(0xffffffffu, r[i], 16);
-            }
-            if (lane < 8) {
-#pragma unroll
-                for (int i = 0; i < RP; i += 4)
-                    *reinterpret_cast<float4 *>(&red[par][w][lane][i]) = make_float4(r[i], r[i + 1], r[i + 2], r[i + 3]);
-            }
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < RP; i += 4) {
-                float4 s = *reinterpret_cast<const float4 *>(&red[par][0][lane & 7][i]);
-#pragma unroll
-                for (int x = 1; x < kWarps; x++) {
-                    const float4 y = *reinterpret_cast<const float4 *>(&red[par][x][lane & 7][i]);
-                    s = make_float4(s.x + y.x, s.y + y.y, s.z + y.z, s.w + y.w);
-                }
-                r[i] = s.x;
-                r[i + 1] = s.y;
-                r[i + 2] = s.z;
-                r[i + 3] = s.w;
-            }
-            par ^= 1;   // the next sum writes the other half: its barrier is behind these reads
-        };
-        lay(0, a);
-#pragma unroll
-        for (int g = 0; g < GP; g++) {
-            lay(4 + 4 * g, b[g]);
-            r[4 + 4 * GP + g] = qk[g];
-        }
-        if (next < p.n) f.store(tok[turn ^ 1]);   // read behind the sum's barrier
-        sum(R);
-        const float4 v = *reinterpret_cast<const float4 *>(&t.v[c0]);
-        const float d[4] = {t.beta * (v.x - r[0]), t.beta * (v.y - r[1]), t.beta * (v.z - r[2]), t.beta * (v.w - r[3])};
-        const Quad dq{make_float2(d[0], d[1]), make_float2(d[2], d[3])};
-#pragma unroll
-        for (int i = 0; i < N; i++) fma(S[i], t.k[k0 + 16 * i], dq);
-        T *o = (T *)p.o + hq * D + v0 + c0;
-        if (threadIdx.x < 8) {
-#pragma unroll
-            for (int g = 0; g < GP; g++)
-                if (g < p.G) {
-#pragma unroll
-                    for (int c = 0; c < 4; c++) put(o, g * D + c, p.scale * fmaf(r[4 + 4 * GP + g], d[c], r[4 + 4 * g + c]));
-                }
-        }
-        // the query heads behind the first GP read S' itself
-        for (int g0 = GP; g0 < p.G; g0 += GP) {
-#pragma unroll
-            for (int g = 0; g < GP; g++) {
-                b[g] = Quad{};
-                if (g0 + g < p.G) {
-#pragma unroll
-                    for (int i = 0; i < N; i++)
-                        fma(b[g], both(at((const T *)p.q, (hq + g0 + g) * D + k0 + 16 * i)), S[i]);
-                }
-                lay(4 * g, b[g]);
-            }
-            sum(4 * GP);
-            if (threadIdx.x < 8) {
-#pragma unroll
-                for (int g = 0; g < GP; g++)
-                    if (g0 + g < p.G) {
-#pragma unroll
-                        for (int c = 0; c < 4; c++) put(o, (int64_t)(g0 + g) * D + c, p.scale * r[4 * g + c]);
-                    }
-            }
-        }
-        __syncthreads();   // the token has been read before its place is filled again
-        j = next;
-    }
-#pragma unroll
-    for (int i = 0; i < N; i++)
-        *reinterpret_cast<float4 *>(p.state_out + so + (k0 + 16 * i) * D) = make_float4(S[i].x.x, S[i].x.y, S[i].y.x, S[i].y.y);
-}
-
 // Four neighbouring values as loaded.
 template <typename T>
 struct Raw4;
@@ -318,12 +137,14 @@ template <>
 struct Raw4<float> {
     float4 r;
     __device__ __forceinline__ void load(const float *p) { r = *reinterpret_cast<const float4 *>(p); }
+    __device__ __forceinline__ void store(float *p) const { *reinterpret_cast<float4 *>(p) = r; }
     __device__ __forceinline__ Quad wide() const { return Quad{make_float2(r.x, r.y), make_float2(r.z, r.w)}; }
 };
 template <>
 struct Raw4<__nv_bfloat16> {
     uint2 r;
     __device__ __forceinline__ void load(const __nv_bfloat16 *p) { r = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *reinterpret_cast<uint2 *>(p) = r; }
     __device__ __forceinline__ Quad wide() const {
         return Quad{widen(Raw2<__nv_bfloat16>{r.x}), widen(Raw2<__nv_bfloat16>{r.y})};
     }
@@ -356,19 +177,17 @@ __device__ __forceinline__ float spread_sum(float (&x)[N]) {
 
 // [dv, dk] states: a row of S^T (one value dim) lies along D / 4 lanes, four
 // key dims each; a warp holds 8 value dims and needs no other warp.
-constexpr int kVfirstPerSm[5] = {0, 5, 5, 0, 4};
 template <typename T, int D, bool KDA, int GP>
-__global__ void __launch_bounds__(kThreads, kVfirstPerSm[GP]) delta_step_vfirst_kernel(Params p) {
+__global__ void __launch_bounds__(kThreads, kVfirstPerSm<T>[GP]) delta_step_vfirst_kernel(Params p) {
     constexpr int L = D / 4, PER = 32 / L;        // lanes of a value dim, value dims of one load
     constexpr int N = 8 / PER;                    // value dims of a thread
-    __shared__ int shared_last[kWarps][1];
+    __shared__ int shared_last[2][kWarps][1];
     next_grid_may_start();
     previous_grid_done();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int h = blockIdx.x / (D / kSlice);
     const int v0 = blockIdx.x % (D / kSlice) * kSlice + w * 8 + lane / L, k0 = lane % L * 4;   // value dims v0 + PER i
     const int own = lane % L / (L / N);           // the value dim whose sums end up here
-    const int row = blockIdx.y;
     // one token as loaded, fetched while the one before runs
     struct Raw {
         Raw4<T> k, q[GP];
@@ -385,84 +204,252 @@ __global__ void __launch_bounds__(kThreads, kVfirstPerSm[GP]) delta_step_vfirst_
         if (KDA) f.a = *reinterpret_cast<const float4 *>(p.g + hk * D + k0);
         else f.a.x = p.g[hk];
     };
-    load(row);
-    int slot[1], last[1];
-    if (!slot_of(p, row, slot[0])) return;
-    const int64_t so = (((int64_t)slot[0] * p.H + h) * D + v0) * D + k0;
-    Quad S[N];
-#pragma unroll
-    for (int i = 0; i < N; i++) {
-        const float4 x = *reinterpret_cast<const float4 *>(p.state + so + PER * i * D);
-        S[i] = Quad{make_float2(x.x, x.y), make_float2(x.z, x.w)};
-    }
-    last[0] = row;
-    if (p.slots) last_rows<1>(p.slots, p.n, slot, row, last, shared_last);
-    if (last[0] == kEarlier) return;
-    Rows rows(p.slots, p.n, slot[0], row, last[0]);
-    for (int j = row; j < p.n;) {
-        const int64_t hq = ((int64_t)j * p.H + h) * p.G;
-        const Quad k = f.k.wide();
-        Quad q[GP], a;
-#pragma unroll
-        for (int g = 0; g < GP; g++) q[g] = f.q[g].wide();
-        if (KDA) {
-            a.x = make_float2(expf(f.a.x), expf(f.a.y));
-            a.y = make_float2(expf(f.a.z), expf(f.a.w));
-        } else {
-            a.x = a.y = both(expf(f.a.x));
-        }
-        const float v = (float)f.v, beta = (float)f.beta;
-        const int next = rows.next(j);
-        if (next < p.n) load(next);
-        float x[N], y[GP][N], qk[GP];
+    int slots, par = 0;
+    for (uint32_t firsts = first_rows(p, blockIdx.y * p.rows, slots); firsts; firsts &= firsts - 1, par ^= 1) {
+        const int at_bit = __ffs(firsts) - 1, row = blockIdx.y * p.rows + at_bit;
+        const int slot[1] = {__shfl_sync(0xffffffffu, slots, at_bit)};
+        load(row);
+        const int64_t so = (((int64_t)slot[0] * p.H + h) * D + v0) * D + k0;
+        Quad S[N];
 #pragma unroll
         for (int i = 0; i < N; i++) {
-            S[i] = Quad{mul2(a.x, S[i].x), mul2(a.y, S[i].y)};
-            x[i] = dot(k, S[i]);
+            const float4 x = *reinterpret_cast<const float4 *>(p.state + so + PER * i * D);
+            S[i] = Quad{make_float2(x.x, x.y), make_float2(x.z, x.w)};
+        }
+        int last[1] = {row};
+        if (p.slots) last_rows<1>(p.slots, p.n, slot, row, last, shared_last[par]);
+        if (last[0] == kEarlier) continue;
+        Rows rows(p.slots, p.n, slot[0], row, last[0]);
+        for (int j = row; j < p.n;) {
+            const int64_t hq = ((int64_t)j * p.H + h) * p.G;
+            const Quad k = f.k.wide();
+            Quad q[GP], a;
 #pragma unroll
-            for (int g = 0; g < GP; g++) y[g][i] = dot(q[g], S[i]);
+            for (int g = 0; g < GP; g++) q[g] = f.q[g].wide();
+            if (KDA) {
+                a.x = make_float2(expf(f.a.x), expf(f.a.y));
+                a.y = make_float2(expf(f.a.z), expf(f.a.w));
+            } else {
+                a.x = a.y = both(expf(f.a.x));
+            }
+            const float v = (float)f.v, beta = (float)f.beta;
+            const int next = rows.next(j);
+            if (next < p.n) load(next);
+            float x[N], y[GP][N], qk[GP];
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                S[i] = Quad{mul2(a.x, S[i].x), mul2(a.y, S[i].y)};
+                x[i] = dot(k, S[i]);
+#pragma unroll
+                for (int g = 0; g < GP; g++) y[g][i] = dot(q[g], S[i]);
+            }
+#pragma unroll
+            for (int g = 0; g < GP; g++) qk[g] = dot(q[g], k);
+#pragma unroll
+            for (int o = L / 2; o > 0; o /= 2)
+#pragma unroll
+                for (int g = 0; g < GP; g++) qk[g] += __shfl_xor_sync(0xffffffffu, qk[g], o);
+            const float d = beta * (v - spread_sum<N, L>(x));
+            T *out = (T *)p.o + hq * D + v0 + PER * own;
+            const bool writes = lane % (L / N) == 0;
+#pragma unroll
+            for (int g = 0; g < GP; g++) {
+                const float o = p.scale * fmaf(qk[g], d, spread_sum<N, L>(y[g]));
+                if (writes && g < p.G) put(out, g * D, o);
+            }
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                const float2 e = both(__shfl_sync(0xffffffffu, d, lane / L * L + i * (L / N)));
+                S[i].x = fma2(k.x, e, S[i].x);
+                S[i].y = fma2(k.y, e, S[i].y);
+            }
+            // the query heads behind the first GP read S' itself
+            for (int g = GP; g < p.G; g++) {
+                Raw4<T> r;
+                r.load((const T *)p.q + (hq + g) * D + k0);
+                const Quad qx = r.wide();
+#pragma unroll
+                for (int i = 0; i < N; i++) x[i] = dot(qx, S[i]);
+                const float o = p.scale * spread_sum<N, L>(x);
+                if (writes) put(out, (int64_t)g * D, o);
+            }
+            j = next;
         }
 #pragma unroll
-        for (int g = 0; g < GP; g++) qk[g] = dot(q[g], k);
+        for (int i = 0; i < N; i++)
+            *reinterpret_cast<float4 *>(p.state_out + so + PER * i * D) = make_float4(S[i].x.x, S[i].x.y, S[i].y.x, S[i].y.y);
+    }
+}
+
+// [dk, dv] states: a warp holds 16 value dims of all key dims and needs no other
+// warp.  A lane has four of the value dims and D / 8 neighbouring key dims, so
+// that a load takes 64 bytes of each of 8 rows, and sums over the key dims go
+// over the 8 lanes of the same value dims.  A token's k, q and gate factors
+// come from the warp's own place in shared memory, each as a pair of the
+// same value for packed arithmetic, the groups of key dims 16 bytes off each
+// other's banks.
+template <int D, bool KDA, int GP>
+struct Token {
+    static constexpr int N = D / 8, ROW = N + 2;
+    alignas(16) float2 k[8 * ROW];
+    alignas(16) float2 q[GP][8 * ROW];
+    alignas(16) float2 a[KDA ? 8 * ROW : 2];
+};
+template <typename T, int D, bool KDA, int GP>
+__global__ void __launch_bounds__(kThreads, kStepPerSm<D>) delta_step_kernel(Params p) {
+    using Tok = Token<D, KDA, GP>;
+    constexpr int N = Tok::N;                     // key dims of a lane
+    __shared__ int shared_last[2][kWarps][1];
+    __shared__ Tok toks[kWarps];
+    next_grid_may_start();
+    previous_grid_done();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int h = blockIdx.x / (D / kWide), v0 = blockIdx.x % (D / kWide) * kWide + w * 16 + (lane & 3) * 4;
+    const int k0 = (lane >> 2) * N;               // key dims k0 + i
+    const int own = lane >> 3 & 3;                // after spread(): the value dim of the four whose sums end up here
+    const int d0 = lane * 4;                      // the dims that this lane fetches of k, q and the gate
+    const bool fetches = d0 < D;
+    Tok &t = toks[w];
+    const int place = d0 + d0 / N * 2, mine = (lane >> 2) * Tok::ROW;
+    // one token as loaded, fetched while the one before runs
+    struct Raw {
+        Raw4<T> k, q[GP], v;
+        T beta;
+        float4 a;
+    } f;
+    auto load = [&](int j) {
+        const int64_t hk = (int64_t)j * p.H + h, hq = hk * p.G;
+        if (fetches) {
+            f.k.load((const T *)p.k + hk * D + d0);
 #pragma unroll
-        for (int o = L / 2; o > 0; o /= 2)
-#pragma unroll
-            for (int g = 0; g < GP; g++) qk[g] += __shfl_xor_sync(0xffffffffu, qk[g], o);
-        const float d = beta * (v - spread_sum<N, L>(x));
-        T *out = (T *)p.o + hq * D + v0 + PER * own;
-        const bool writes = lane % (L / N) == 0;
-#pragma unroll
-        for (int g = 0; g < GP; g++) {
-            const float o = p.scale * fmaf(qk[g], d, spread_sum<N, L>(y[g]));
-            if (writes && g < p.G) put(out, g * D, o);
+            for (int g = 0; g < GP; g++) f.q[g].load((const T *)p.q + (hq + (g < p.G ? g : 0)) * D + d0);
+            if (KDA) f.a = *reinterpret_cast<const float4 *>(p.g + hk * D + d0);
         }
+        if (!KDA) f.a.x = p.g[hk];
+        f.v.load((const T *)p.v + hk * D + v0);
+        f.beta = ((const T *)p.beta)[hk];
+    };
+    auto lay = [&](float2 *to, const Quad &x) {   // each of the four twice
+        if (!fetches) return;
+        *reinterpret_cast<float4 *>(to + place) = make_float4(x.x.x, x.x.x, x.x.y, x.x.y);
+        *reinterpret_cast<float4 *>(to + place + 2) = make_float4(x.y.x, x.y.x, x.y.y, x.y.y);
+    };
+    auto pair_at = [&](const float2 *from, int i) {   // two neighbouring key dims' pairs
+        const float4 x = *reinterpret_cast<const float4 *>(from + mine + i);
+        return Quad{make_float2(x.x, x.y), make_float2(x.z, x.w)};
+    };
+    // the four value dims' sums over the key dims: each lane ends up with that of dim `own`
+    auto spread = [&](const Quad &x) {
+        const bool up = lane & 16, odd = lane & 8;
+        float2 keep = up ? x.y : x.x, give = up ? x.x : x.y;
+        keep.x += __shfl_xor_sync(0xffffffffu, give.x, 16);
+        keep.y += __shfl_xor_sync(0xffffffffu, give.y, 16);
+        float r = (odd ? keep.y : keep.x) + __shfl_xor_sync(0xffffffffu, odd ? keep.x : keep.y, 8);
+        return r + __shfl_xor_sync(0xffffffffu, r, 4);
+    };
+    int slots, par = 0;
+    for (uint32_t firsts = first_rows(p, blockIdx.y * p.rows, slots); firsts; firsts &= firsts - 1, par ^= 1) {
+        const int at_bit = __ffs(firsts) - 1, row = blockIdx.y * p.rows + at_bit;
+        const int slot[1] = {__shfl_sync(0xffffffffu, slots, at_bit)};
+        load(row);
+        const int64_t so = (((int64_t)slot[0] * p.H + h) * D + k0) * D + v0;
+        Quad S[N];
 #pragma unroll
         for (int i = 0; i < N; i++) {
-            const float2 e = both(__shfl_sync(0xffffffffu, d, lane / L * L + i * (L / N)));
-            S[i].x = fma2(k.x, e, S[i].x);
-            S[i].y = fma2(k.y, e, S[i].y);
+            const float4 x = *reinterpret_cast<const float4 *>(p.state + so + i * D);
+            S[i] = Quad{make_float2(x.x, x.y), make_float2(x.z, x.w)};
         }
-        // the query heads behind the first GP read S' itself
-        for (int g = GP; g < p.G; g++) {
-            Raw4<T> r;
-            r.load((const T *)p.q + (hq + g) * D + k0);
-            const Quad qx = r.wide();
+        int last[1] = {row};
+        if (p.slots) last_rows<1>(p.slots, p.n, slot, row, last, shared_last[par]);
+        if (last[0] == kEarlier) continue;
+        Rows rows(p.slots, p.n, slot[0], row, last[0]);
+        for (int j = row; j < p.n;) {
+            const int64_t hq = ((int64_t)j * p.H + h) * p.G;
+            T *out = (T *)p.o + hq * D + v0 + own;
+            const Quad k = f.k.wide(), v = f.v.wide();
+            float qk[GP];
+            __syncwarp();   // the token before has been read
+            lay(t.k, k);
 #pragma unroll
-            for (int i = 0; i < N; i++) x[i] = dot(qx, S[i]);
-            const float o = p.scale * spread_sum<N, L>(x);
-            if (writes) put(out, (int64_t)g * D, o);
+            for (int g = 0; g < GP; g++) {
+                const Quad q = f.q[g].wide();
+                lay(t.q[g], q);
+                qk[g] = fetches ? dot(q, k) : 0.f;
+            }
+            float2 a = both(0.f);
+            if (KDA) lay(t.a, Quad{make_float2(expf(f.a.x), expf(f.a.y)), make_float2(expf(f.a.z), expf(f.a.w))});
+            else a = both(expf(f.a.x));
+            const float beta = (float)f.beta;
+            const int next = rows.next(j);
+            if (next < p.n) load(next);
+            __syncwarp();
+            Quad x{}, y[GP] = {};
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                const Quad kk = pair_at(t.k, i);
+                Quad aa{a, a};
+                if (KDA) aa = pair_at(t.a, i);
+                S[i] = mul(aa.x, S[i]);
+                S[i + 1] = mul(aa.y, S[i + 1]);
+                fma(x, kk.x, S[i]);
+                fma(x, kk.y, S[i + 1]);
+#pragma unroll
+                for (int g = 0; g < GP; g++) {
+                    const Quad qq = pair_at(t.q[g], i);
+                    fma(y[g], qq.x, S[i]);
+                    fma(y[g], qq.y, S[i + 1]);
+                }
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o /= 2)
+#pragma unroll
+                for (int g = 0; g < GP; g++) qk[g] += __shfl_xor_sync(0xffffffffu, qk[g], o);
+            const float2 vv = own & 2 ? v.y : v.x;
+            const float d = beta * ((own & 1 ? vv.y : vv.x) - spread(x));
+            const bool writes = (lane & 4) == 0;
+#pragma unroll
+            for (int g = 0; g < GP; g++) {
+                const float o = p.scale * fmaf(qk[g], d, spread(y[g]));
+                if (writes && g < p.G) put(out, g * D, o);
+            }
+            Quad dd;
+            dd.x = make_float2(__shfl_sync(0xffffffffu, d, lane & 3), __shfl_sync(0xffffffffu, d, 8 + (lane & 3)));
+            dd.y = make_float2(__shfl_sync(0xffffffffu, d, 16 + (lane & 3)), __shfl_sync(0xffffffffu, d, 24 + (lane & 3)));
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                const Quad kk = pair_at(t.k, i);
+                fma(S[i], kk.x, dd);
+                fma(S[i + 1], kk.y, dd);
+            }
+            // the query heads behind the first GP read S' itself
+            for (int g = GP; g < p.G; g++) {
+                Raw4<T> r;
+                if (fetches) r.load((const T *)p.q + (hq + g) * D + d0);
+                __syncwarp();
+                if (fetches) lay(t.q[0], r.wide());
+                __syncwarp();
+                Quad z{};
+#pragma unroll
+                for (int i = 0; i < N; i += 2) {
+                    const Quad qq = pair_at(t.q[0], i);
+                    fma(z, qq.x, S[i]);
+                    fma(z, qq.y, S[i + 1]);
+                }
+                const float o = p.scale * spread(z);
+                if (writes) put(out, (int64_t)g * D, o);
+            }
+            j = next;
         }
-        j = next;
+#pragma unroll
+        for (int i = 0; i < N; i++)
+            *reinterpret_cast<float4 *>(p.state_out + so + i * D) = make_float4(S[i].x.x, S[i].x.y, S[i].y.x, S[i].y.y);
     }
-#pragma unroll
-    for (int i = 0; i < N; i++)
-        *reinterpret_cast<float4 *>(p.state_out + so + PER * i * D) = make_float4(S[i].x.x, S[i].x.y, S[i].y.x, S[i].y.y);
 }
 
 // The causal conv's tokens: y = act(b + sum_i w_i x_i) over a slot's W - 1 kept
 // inputs (oldest first) and the row's own, which then is the newest one kept.  A
-// thread owns one 16-byte vector of channels; its weights stay in registers
-// for the rows of its block.
+// thread owns four channels, whose weights stay in registers for the rows of its
+// CTA; the loads of kConvRows rows are in flight at once.
 struct ConvParams {
     const void *x;
     const float *weight, *bias;
@@ -470,9 +457,10 @@ struct ConvParams {
     void *state_out;
     const int32_t *slots;
     void *y;
-    int n, num_slots, channels, groups;   // groups of kConvRows rows for a block
+    int n, num_slots, channels, groups;   // groups of kConvRows rows of a CTA
 };
-constexpr int kConvRows = 2;   // rows whose loads a thread has in flight
+template <typename T>
+constexpr int kConvRows = sizeof(T) == 2 ? 4 : 2;
 
 // as in the conv over sequences: the fast divide returns 0 once the denominator
 // passes 2^126, where the exact quotient is below 1e-36
@@ -481,49 +469,45 @@ __device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.f + __ex
 // grid (channel blocks, blocks of rows)
 template <typename T, int W, bool SILU>
 __global__ void __launch_bounds__(kThreads) conv1d_step_kernel(ConvParams p) {
-    constexpr int V = kVecOf<T>, NW = W > 1 ? W - 1 : 1, R = kConvRows;
+    constexpr int NW = W > 1 ? W - 1 : 1, R = kConvRows<T>;
     __shared__ int shared_last[2][kWarps][R];
     next_grid_may_start();
     previous_grid_done();
-    const int c = (blockIdx.x * kThreads + threadIdx.x) * V;
-    const bool live = c < p.channels;   // the block stays whole for the rows' search
+    const int c = (blockIdx.x * kThreads + threadIdx.x) * 4;
+    const bool live = c < p.channels;   // the CTA stays whole for the rows' search
     const T *state = (const T *)p.state + c;
     const int64_t C = p.channels;
-    float w[W * V], b[V];   // w[V' W + i]: as they lie
+    Quad w[W], b{};
     if (live) {
+        float f[4 * W];   // as they lie: the four channels' W weights
 #pragma unroll
-        for (int i = 0; i < W * V; i += 4) {
+        for (int i = 0; i < 4 * W; i += 4) {
             const float4 x = *reinterpret_cast<const float4 *>(p.weight + (int64_t)c * W + i);
-            w[i] = x.x;
-            w[i + 1] = x.y;
-            w[i + 2] = x.z;
-            w[i + 3] = x.w;
+            f[i] = x.x;
+            f[i + 1] = x.y;
+            f[i + 2] = x.z;
+            f[i + 3] = x.w;
         }
 #pragma unroll
-        for (int j = 0; j < V; j += 4) {
-            const float4 x = p.bias ? *reinterpret_cast<const float4 *>(p.bias + c + j) : make_float4(0.f, 0.f, 0.f, 0.f);
-            b[j] = x.x;
-            b[j + 1] = x.y;
-            b[j + 2] = x.z;
-            b[j + 3] = x.w;
+        for (int i = 0; i < W; i++) w[i] = Quad{make_float2(f[i], f[W + i]), make_float2(f[2 * W + i], f[3 * W + i])};
+        if (p.bias) {
+            const float4 x = *reinterpret_cast<const float4 *>(p.bias + c);
+            b = Quad{make_float2(x.x, x.y), make_float2(x.z, x.w)};
         }
     }
     // y of row j, and the window moved on
-    auto token = [&](int j, uint4 (&win)[NW], const uint4 &x) {
-        float z[V], t[V];
-#pragma unroll
-        for (int e = 0; e < V; e++) z[e] = b[e];
+    auto token = [&](int j, Raw4<T> (&win)[NW], const Raw4<T> &x) {
+        Quad z = b;
 #pragma unroll
         for (int i = 0; i < W; i++) {
-            widen16(i < W - 1 ? win[i < W - 1 ? i : 0] : x, t);
-#pragma unroll
-            for (int e = 0; e < V; e++) z[e] = fmaf(w[e * W + i], t[e], z[e]);
+            const Quad t = i < W - 1 ? win[i < W - 1 ? i : 0].wide() : x.wide();
+            z.x = fma2(w[i].x, t.x, z.x);
+            z.y = fma2(w[i].y, t.y, z.y);
         }
-        if (SILU) {
-#pragma unroll
-            for (int e = 0; e < V; e++) z[e] = silu(z[e]);
-        }
-        store16((T *)p.y + j * C + c, z);
+        if (SILU) z = Quad{make_float2(silu(z.x.x), silu(z.x.y)), make_float2(silu(z.y.x), silu(z.y.y))};
+        T *y = (T *)p.y + j * C + c;
+        store2(y, z.x);
+        store2(y + 2, z.y);
 #pragma unroll
         for (int i = 0; i + 1 < W - 1; i++) win[i] = win[i + 1];
         if (W > 1) win[NW - 1] = x;
@@ -533,32 +517,39 @@ __global__ void __launch_bounds__(kThreads) conv1d_step_kernel(ConvParams p) {
         if (row >= p.n) break;
         int slot[R], last[R];
         bool used[R];
-        uint4 win[R][NW], x[R];
+        Raw4<T> win[R][NW], x[R];
 #pragma unroll
         for (int r = 0; r < R; r++) {
             last[r] = row + r;
             slot[r] = row + r >= p.n ? -1 : p.slots ? p.slots[row + r] : row + r;
             used[r] = slot[r] >= 0 && slot[r] < p.num_slots;
-            x[r] = make_uint4(0, 0, 0, 0);
-            if (live && used[r]) {
-                x[r] = load16((const T *)p.x + (row + r) * C + c);
+        }
 #pragma unroll
-                for (int u = 0; u < W - 1; u++) win[r][u] = load16(state + ((int64_t)slot[r] * (W - 1) + u) * C);
+        for (int r = 0; r < R; r++) {
+            if (live && used[r]) {
+                x[r].load((const T *)p.x + (row + r) * C + c);
+#pragma unroll
+                for (int u = 0; u < W - 1; u++) win[r][u].load(state + ((int64_t)slot[r] * (W - 1) + u) * C);
             }
         }
         if (p.slots) last_rows<R>(p.slots, p.n, slot, row, last, shared_last[i & 1]);
 #pragma unroll
         for (int r = 0; r < R; r++) {
             if (!used[r] || last[r] == kEarlier) continue;
-            Rows rows(p.slots, p.n, slot[r], row + r, last[r]);
-            for (int j = row + r; j < p.n; j = rows.next(j)) {
-                if (!live) continue;
-                token(j, win[r], j == row + r ? x[r] : load16((const T *)p.x + j * C + c));
+            if (live) token(row + r, win[r], x[r]);
+            if (last[r] > row + r) {   // more tokens of the slot
+                Rows rows(p.slots, p.n, slot[r], row + r, last[r]);
+                for (int j = rows.next(row + r); j < p.n; j = rows.next(j)) {
+                    if (!live) continue;
+                    Raw4<T> more;
+                    more.load((const T *)p.x + j * C + c);
+                    token(j, win[r], more);
+                }
             }
             if (live) {
 #pragma unroll
                 for (int u = 0; u < W - 1; u++)
-                    *reinterpret_cast<uint4 *>((T *)p.state_out + ((int64_t)slot[r] * (W - 1) + u) * C + c) = win[r][u];
+                    win[r][u].store((T *)p.state_out + ((int64_t)slot[r] * (W - 1) + u) * C + c);
             }
         }
     }
@@ -566,10 +557,10 @@ __global__ void __launch_bounds__(kThreads) conv1d_step_kernel(ConvParams p) {
 
 template <typename T, int W>
 int conv_w(ConvParams p, bool silu, int sms, void *stream) {
-    constexpr int per = kThreads * kVecOf<T>;
-    const int blocks = (p.channels + per - 1) / per, groups = (p.n + kConvRows - 1) / kConvRows;
-    // several groups of rows for a block, which reads the weights once for them, as long as there are blocks for the GPU
-    p.groups = (int)std::max<int64_t>(1, std::min<int64_t>(4, (int64_t)groups * blocks / (4 * sms)));
+    constexpr int per = kThreads * 4, R = kConvRows<T>;
+    const int blocks = (p.channels + per - 1) / per, groups = (p.n + R - 1) / R;
+    // several groups of rows for a CTA, which reads the weights once for them, as long as there are CTAs for the GPU
+    p.groups = (int)std::max<int64_t>(1, std::min<int64_t>(4, (int64_t)groups * blocks / (8 * sms)));
     const dim3 grid((unsigned)blocks, (unsigned)((groups + p.groups - 1) / p.groups));
     return launch_early(silu ? conv1d_step_kernel<T, W, true> : conv1d_step_kernel<T, W, false>, grid, kThreads, 0, 1, stream, p);
 }
@@ -591,24 +582,27 @@ int conv_t(const ConvParams &p, int width, bool silu, int sms, void *stream) {
 static_assert(kMaxConvWidth == 8, "the dispatch covers widths 1..8");
 
 template <typename T, int D, bool KDA, int GP>
-int launch_g(const Params &p, bool vfirst, void *stream) {
-    const dim3 grid((unsigned)(p.H * (D / kSlice)), (unsigned)p.n);
+int launch_g(Params p, bool vfirst, int sms, void *stream) {
+    const int64_t slices = (int64_t)p.H * (D / (vfirst ? kSlice : kWide)), busy = 2 * sms * (vfirst ? kVfirstPerSm<T>[GP] : kStepPerSm<D>);
+    p.rows = (int)std::max<int64_t>(1, std::min<int64_t>(kMaxRows[vfirst], p.n * slices / busy));
+    const dim3 grid((unsigned)slices, (unsigned)((p.n + p.rows - 1) / p.rows));
     return launch_early(vfirst ? delta_step_vfirst_kernel<T, D, KDA, GP> : delta_step_kernel<T, D, KDA, GP>, grid, kThreads, 0, 1,
                         stream, p);
 }
 
 template <typename T, int D, bool KDA>
-int launch(const Params &p, bool vfirst, void *stream) {
-    if (p.G == 1) return launch_g<T, D, KDA, 1>(p, vfirst, stream);
-    if (p.G == 2) return launch_g<T, D, KDA, 2>(p, vfirst, stream);
-    return launch_g<T, D, KDA, 4>(p, vfirst, stream);
+int launch(const Params &p, bool vfirst, int sms, void *stream) {
+    if (p.G == 1) return launch_g<T, D, KDA, 1>(p, vfirst, sms, stream);
+    if (p.G == 2) return launch_g<T, D, KDA, 2>(p, vfirst, sms, stream);
+    return launch_g<T, D, KDA, 4>(p, vfirst, sms, stream);
 }
 
 template <typename T>
 int launch_t(const cpdr_ctx *c, const Params &p, void *stream) {
     const bool kda = c->plan.gate_kind == CPDR_GATE_PER_DIM, vf = c->plan.vfirst;
-    if (c->plan.dk == 128) return kda ? launch<T, 128, true>(p, vf, stream) : launch<T, 128, false>(p, vf, stream);
-    return kda ? launch<T, 64, true>(p, vf, stream) : launch<T, 64, false>(p, vf, stream);
+    const int sms = device_sms(c->device);
+    if (c->plan.dk == 128) return kda ? launch<T, 128, true>(p, vf, sms, stream) : launch<T, 128, false>(p, vf, sms, stream);
+    return kda ? launch<T, 64, true>(p, vf, sms, stream) : launch<T, 64, false>(p, vf, sms, stream);
 }
 
 }  // namespace
@@ -618,7 +612,7 @@ int launch_delta_step(const cpdr_ctx *c, const void *q, const void *k, const voi
                       void *stream) {
     if (n == 0) return 0;
     const auto &pl = c->plan;
-    const Params p{q, k, v, beta, g, state, state_out, slots, o, n, num_slots, pl.H, pl.G, pl.scale};
+    const Params p{q, k, v, beta, g, state, state_out, slots, o, n, num_slots, pl.H, pl.G, pl.scale, 1};
     return pl.in_dtype == CPDR_DTYPE_F32 ? launch_t<float>(c, p, stream) : launch_t<__nv_bfloat16>(c, p, stream);
 }
 

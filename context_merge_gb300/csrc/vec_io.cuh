@@ -95,5 +95,18 @@ __device__ __forceinline__ void store16(__nv_bfloat16 *p, const float (&v)[8]) {
     *reinterpret_cast<uint4 *>(p) = r;
 }
 
+// Asynchronous copies of 16 bytes into shared memory, in groups that a thread
+// waits for in turn; without `live` the place is filled with zeros and `from` not read.
+__device__ __forceinline__ void fetch16(void *to, const void *from, bool live = true) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
+                 "r"(live ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void fetch_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void fetch_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 }  // namespace vio
 }  // namespace cpdr
