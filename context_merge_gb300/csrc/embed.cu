@@ -8,6 +8,13 @@
 // first), so that a token's rows of dy stand together in the order of the
 // batch: sums run in a fixed order, without atomics, and every table row is
 // written once.
+//
+// Measured in graphs: the lookup of 262144 rows of 2048 in bf16, text-like
+// tokens, 216 us (6.0 TB/s with each row that occurs counted once; some are read again
+// from HBM).  The gradient of 131072 rows of 2048 to a table of 131072: 190
+// us for 1.07 GB (159 at the measured copy's rate): sums and zeros 150, the sort 28, the long runs 11;
+// of 1000 rows of 1360 in fp32 to 32003: 36 us (26), of which the sort takes 8.  One
+// warp's or block's sum for each table row instead of segments: 514 us, the frequent tokens' blocks long behind the others.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

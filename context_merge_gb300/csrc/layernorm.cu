@@ -19,6 +19,16 @@
 // (and the same for sum u (s - A)).  A fp32 mean is itself off by some half steps
 // of the row's size; the sum of the differences says by how much, and what
 // is subtracted is corrected by it.
+//
+// Measured over 0.25 GB a tensor, TB/s (the measured copy: 6.8): forward with a
+// residual 6.5 to 7.1 at 64 to 16384 columns of bf16 and 6.2 to 7.1 of fp32;
+// without one 5.0 to 6.4 (bf16, up to 4096; 3.8 to 5.1 beyond) and 6.3 to 7.0 (fp32);
+// to e4m3 from bf16 5.3 to 6.7 up to 4096 and 3.8 to 5.5 beyond; backward with the
+// residual's gradient 5.4 to 6.8 (bf16 up to 4096 columns; 3.2 to 5.4 beyond) and
+// 5.9 to 6.8 (fp32 up to 6144; 4.1 to 5.6 beyond).  What is below the copy's rate is
+// bound by the exchanges: rows of bf16 have half the bytes for them, and the widest rows
+// leave one block an SM.  With two exchanges of sums a row (mean, then
+// squares) and scalar arithmetic: forward 5.8 to 6.6, backward 4.6 at 2048.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -482,7 +482,9 @@ cpdr_status cpdr_embed_bwd(const cpdr_ctx *ctx, const int32_t *tokens, int64_t n
  * they were.  Rows whose slot is outside 0 .. num_slots - 1 (padding, -1) do
  * nothing: their o is left as it was.  Rows of the same slot are consecutive
  * tokens of its sequence, in row order; its states stay on the chip between
- * them.  0 <= n <= 65535.  States and sums are fp32, o is rounded once.
+ * them.  0 <= n <= 65535.  States and sums are fp32, o is rounded once; states
+ * and inputs are finite (a dropped infinity is 0 times infinity).  All rows'
+ * slots are looked through for each row: past some thousand rows that shows.
  */
 cpdr_status cpdr_delta_step(const cpdr_ctx *ctx, const void *q, const void *k, const void *v, const void *beta,
                             const float *gate, const float *state, float *state_out, const int32_t *slots, int32_t n,
