@@ -366,13 +366,16 @@ __global__ void __launch_bounds__(kSortThreads) sort_few_kernel(Pass p) {
 // ------------------------------------------------------------------ sums
 // The sorted list is cut into segments, so that a token in every place costs no
 // more than one in few.  A segment sums the runs of one token that begin in it,
-// to their ends, which may lie up to kBeyond pairs behind it.  A run that goes
+// to their ends, which may lie up to `beyond` pairs behind it.  A run that goes
 // on further is long: each of its segments puts its part of the sum into `part`,
 // and a second kernel adds those up.  Table rows that do not occur are
 // filled by blocks of their own, among the segments'.
 constexpr int kSegment = 32;   // a warp's lanes
-constexpr int kBeyond = 128;
-constexpr int kMaxGroups = 32;   // segments of a block, at most
+// `beyond`, with so many segments that HBM bounds the sums, and with fewer, where
+// the longest segment does: 131072 rows of 2048 (27 blocks of segments an SM) 190 us
+// with 128 and 202 with 16; 100000 rows of 256, text-like tokens, 81 and 56.
+constexpr int kBeyondMany = 128, kBeyondFew = 16;
+constexpr int kMaxGroups = 16;   // segments of a block, at most
 
 struct Sums {
     const int2 *pair;           // (key, position), sorted
@@ -382,6 +385,7 @@ struct Sums {
     float *part;                // [segments][2][width]: a long run that comes from before, one that begins here
     int n, vocab, width;
     float scale;
+    int beyond;
     int cols, groups;           // segments' blocks: vectors of a row (two for each thread), segments of a block
     int seg_blocks, zero_blocks, col_blocks;
     Split split;                // of the table, for the blocks that fill it
@@ -465,20 +469,20 @@ __device__ __forceinline__ Plan plan_of(const Sums &p, const int2 *pair, int seg
     const int before = a ? p.pair[a - 1].x : -1, behind = b < p.n ? p.pair[b].x : -1;
     if (before == first && first < p.vocab) {
         // where it began, and whether it is long
-        const int w0 = a - kBeyond - kSegment;
+        const int w0 = a - p.beyond - kSegment;
         bool is_long = w0 >= 0 && p.pair[w0 >= 0 ? w0 : 0].x == first;
         if (!is_long) {
             const int from = max(0, w0), start = from + lower_bound(p.pair + from, a - from, first);
-            const int64_t limit = (int64_t)(start / kSegment + 1) * kSegment + kBeyond;
+            const int64_t limit = (int64_t)(start / kSegment + 1) * kSegment + p.beyond;
             is_long = limit < p.n && p.pair[limit].x == first;
         }
         s.from_before = is_long;
         if (!is_long) s.begin = a + __popc(alike);
     }
     if (behind == last && last < p.vocab && s.begin < b && !(s.from_before && last == first)) {
-        const int64_t limit = (int64_t)b + kBeyond;
+        const int64_t limit = (int64_t)b + p.beyond;
         s.goes_on = limit < p.n && p.pair[limit].x == last;
-        if (!s.goes_on) s.end = b + lower_bound(p.pair + b, (int)min((int64_t)kBeyond, (int64_t)p.n - b), last + 1);
+        if (!s.goes_on) s.end = b + lower_bound(p.pair + b, (int)min((int64_t)p.beyond, (int64_t)p.n - b), last + 1);
     }
     return s;
 }
@@ -704,7 +708,7 @@ Space space(int64_t n, int width) {
     s.list = round256((size_t)n * sizeof(int2));
     s.counts = (n > kSub ? 2 : 1) * s.list;
     s.longs = s.counts + (n > kSub ? (size_t)kMaxPasses * kMaxTiles * kMaxBins * 4 : 0);
-    s.part = s.longs + round256((size_t)(1 + n / (kBeyond + 1)) * 4);
+    s.part = s.longs + round256((size_t)(1 + n / (kBeyondFew + 1)) * 4);
     s.bytes = s.part + (size_t)segments_of(n) * 2 * (size_t)width * 4;
     return s;
 }
@@ -755,11 +759,12 @@ int backward(const int32_t *tokens, int n, int vocab, int width, float scale, co
     }
     if (rc) return rc;
     const int vecs = width / V;
-    Sums q{p.out, dy, dtable, p.longs, (float *)(ws + s.part), n, vocab, width, scale};
+    Sums q{p.out, dy, dtable, p.longs, (float *)(ws + s.part), n, vocab, width, scale, 0};
     q.cols = std::min(vecs, 2 * kThreads);
     q.groups = std::min(kThreads / ((q.cols + 1) / 2), kMaxGroups);
     q.col_blocks = (vecs + q.cols - 1) / q.cols;
     const int64_t segments = segments_of(n), seg_blocks = (segments + q.groups - 1) / q.groups * q.col_blocks;
+    q.beyond = seg_blocks >= 8 * sms ? kBeyondMany : kBeyondFew;
     q.split = split_of(vocab, vecs, kBlockVecs, kTableRows, sms);
     const dim3 fill = grid_of(q.split, vocab, vecs);
     const int64_t zero_blocks = (int64_t)fill.x * fill.y;
@@ -767,9 +772,9 @@ int backward(const int32_t *tokens, int n, int vocab, int width, float scale, co
     q.seg_blocks = (int)seg_blocks;
     q.zero_blocks = (int)zero_blocks;
     rc = launch_early(segment_sums_kernel<T>, dim3((unsigned)(seg_blocks + zero_blocks)), kThreads, 0, 1, stream, q);
-    if (rc || n <= kSegment + kBeyond) return rc;   // no run can be long
+    if (rc || n <= kSegment + q.beyond) return rc;   // no run can be long
     // no more blocks than the longest possible list has items, and a wave of them
-    const int64_t most = n / (kBeyond + 1) * ((width + 127) / 128);
+    const int64_t most = n / (q.beyond + 1) * ((width + 127) / 128);
     return launch_early(long_runs_kernel<T>, dim3((unsigned)std::min<int64_t>(most, 6 * sms)), kThreads, 0, 1, stream, q);
 }
 

@@ -459,7 +459,7 @@ cpdr_status cpdr_embed_fwd(const cpdr_ctx *ctx, const int32_t *tokens, int64_t n
  * not occur; rows whose token lies outside the table add nothing.  dy [n,
  * width] and dtable in the input dtype; sums in fp32, rounded once.  A token's
  * rows are added in the order of the batch, in groups that depend on the
- * tokens alone.  workspace: cpdr_embed_bwd_workspace_bytes() bytes, 16-byte
+ * tokens and the sizes alone.  workspace: cpdr_embed_bwd_workspace_bytes() bytes, 16-byte
  * aligned.
  */
 cpdr_status cpdr_embed_bwd_workspace_bytes(const cpdr_ctx *ctx, int64_t n, int32_t vocab, int32_t width, size_t *bytes);

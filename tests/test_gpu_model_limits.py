@@ -84,7 +84,7 @@ def test_batches_around_the_sorts_tiles(ctx, n):
     assert torch.equal(out, torch.bincount(tok.long(), minlength=V).bfloat16()[:, None].expand(V, D))
 
 
-@pytest.mark.parametrize("run", [129, 160, 161, 192, 193, 300, 8192, 8193])
+@pytest.mark.parametrize("run", [17, 47, 48, 49, 63, 64, 65, 80, 81, 129, 160, 161, 192, 193, 300, 8192, 8193])
 def test_runs_around_the_sums_segments(ctx, run):
     """One token in `run` places among others, from every place of a segment on: whole sums, and those in parts."""
     for before in (0, 1, 31, 32, 33):
@@ -111,3 +111,22 @@ def test_no_rows(ctx):
     ctx.conv1d_step(e((0, 16), **bf), torch.ones((16, 4), device="cuda"), None, win, e((0, 16), **bf))
     torch.cuda.synchronize()
     assert (state == 1).all() and (win == 1).all()
+
+
+@pytest.mark.parametrize("run", [120, 128, 129, 159, 160, 161, 162, 300, 70000])
+def test_runs_around_the_sums_segments_of_large_batches(ctx, run):
+    """The same in a batch of so many segments that runs may go on further: 1400 blocks of them."""
+    n, D, V = 45000, 2048, 400
+    if run > n:
+        n = run + 5000
+    gen = torch.Generator(device="cuda").manual_seed(run)
+    tok = torch.randint(8, V, (n,), generator=gen, device="cuda").to(torch.int32)
+    tok[torch.randperm(n, generator=gen, device="cuda")[:run]] = 7
+    tok[tok == 8] = 7 if run > 1000 else 9
+    dy = torch.randint(-4, 5, (n, D), generator=gen, device="cuda").float()
+    f32 = cpdr.Context(1, 1, 1, 64, 1, dtype="fp32")
+    out = torch.empty((V, D), device="cuda")
+    f32.embed_bwd(tok, dy, out)
+    torch.cuda.synchronize()
+    # whole numbers: no rounding, in any order
+    assert torch.equal(out, torch.zeros((V, D), device="cuda").index_add_(0, tok, dy))
