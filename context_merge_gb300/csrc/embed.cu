@@ -491,18 +491,6 @@ __device__ __forceinline__ Plan plan_of(const Sums &p, const int2 *pair, int seg
 // of each: 5 blocks of an SM have 160 KB in flight.
 constexpr int kStages = 4;
 
-// The values of a vector, in pairs.
-__device__ __forceinline__ void pairs_of(const uint4 &r, float2 (&v)[2], float) {
-    v[0] = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
-    v[1] = make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
-}
-__device__ __forceinline__ void pairs_of(const uint4 &r, float2 (&v)[4], __nv_bfloat16) {
-    v[0] = widen(Raw2<__nv_bfloat16>{r.x});
-    v[1] = widen(Raw2<__nv_bfloat16>{r.y});
-    v[2] = widen(Raw2<__nv_bfloat16>{r.z});
-    v[3] = widen(Raw2<__nv_bfloat16>{r.w});
-}
-
 // grid: the segments' and the filling blocks in turn
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 5) segment_sums_kernel(Sums p) {
@@ -603,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 5) segment_sums_kernel(Sums p) {
             for (int c = 0; c < 2; c++) {
                 if (c && !two) continue;
                 float2 f[H];
-                pairs_of(stage[u][c][threadIdx.x], f, T());
+                widen_pairs(stage[u][c][threadIdx.x], f);
 #pragma unroll
                 for (int e = 0; e < H; e++) acc[c][e] = add2(acc[c][e], f[e]);
             }

@@ -137,16 +137,6 @@ __device__ __forceinline__ void row_max(float (&m)[R], float (*sh)[R]) {
 // A 16-byte vector's values in pairs: H of them.
 template <typename T>
 constexpr int kPairs = kVecOf<T> / 2;
-__device__ __forceinline__ void widen_pairs(const uint4 &r, float2 (&v)[2]) {
-    v[0] = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
-    v[1] = make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
-}
-__device__ __forceinline__ void widen_pairs(const uint4 &r, float2 (&v)[4]) {
-    v[0] = widen(Raw2<__nv_bfloat16>{r.x});
-    v[1] = widen(Raw2<__nv_bfloat16>{r.y});
-    v[2] = widen(Raw2<__nv_bfloat16>{r.z});
-    v[3] = widen(Raw2<__nv_bfloat16>{r.w});
-}
 template <typename T, int H>
 __device__ __forceinline__ void store_pairs(T *p, const float2 (&v)[H]) {
     float f[2 * H];

@@ -53,8 +53,6 @@ constexpr int kVfirstPerSm[5] = {0, sizeof(T) == 2 ? 5 : 4, sizeof(T) == 2 ? 5 :
 // takes 45 us instead of 42 and 41 with one.
 constexpr int kMaxRows[2] = {2, 4};
 
-__device__ __forceinline__ float at(const float *p, int64_t i) { return p[i]; }
-__device__ __forceinline__ float at(const __nv_bfloat16 *p, int64_t i) { return __bfloat162float(p[i]); }
 __device__ __forceinline__ void put(float *p, int64_t i, float v) { p[i] = v; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, int64_t i, float v) { p[i] = __float2bfloat16_rn(v); }
 

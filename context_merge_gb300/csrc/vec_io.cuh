@@ -80,6 +80,17 @@ __device__ __forceinline__ void widen16(const uint4 &r, float (&v)[8]) {
         v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
 }
+// The same in pairs, for packed arithmetic.
+__device__ __forceinline__ void widen_pairs(const uint4 &r, float2 (&v)[2]) {
+    v[0] = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
+    v[1] = make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
+}
+__device__ __forceinline__ void widen_pairs(const uint4 &r, float2 (&v)[4]) {
+    v[0] = widen(Raw2<__nv_bfloat16>{r.x});
+    v[1] = widen(Raw2<__nv_bfloat16>{r.y});
+    v[2] = widen(Raw2<__nv_bfloat16>{r.z});
+    v[3] = widen(Raw2<__nv_bfloat16>{r.w});
+}
 __device__ __forceinline__ void store16(float *p, const float (&v)[4]) {
     *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
