@@ -130,3 +130,22 @@ def test_runs_around_the_sums_segments_of_large_batches(ctx, run):
     torch.cuda.synchronize()
     # whole numbers: no rounding, in any order
     assert torch.equal(out, torch.zeros((V, D), device="cuda").index_add_(0, tok, dy))
+
+
+@pytest.mark.parametrize("n", [3000, 5000])
+@pytest.mark.parametrize("V", [1023, 1024, 2 ** 20 - 1, 2 ** 20, 2 ** 21 + 3, 2 ** 30])
+def test_vocabularies_of_one_to_four_sorting_passes(ctx, V, n):
+    """Tokens at both ends of the vocabulary and between, padding on either side of it; everything else is zero."""
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    some = torch.cat([torch.randint(0, V, (40,), generator=gen, device="cuda"), torch.tensor([0, V - 1, -1, V], device="cuda")])
+    tok = some[torch.randint(0, 44, (n,), generator=gen, device="cuda")].to(torch.int32)
+    dy = torch.randint(0, 2, (n, 8), generator=gen, device="cuda").bfloat16()
+    out = torch.full((V, 8), 3.0, **bf)
+    ctx.embed_bwd(tok, dy, out)
+    torch.cuda.synchronize()
+    live = (tok >= 0) & (tok < V)
+    ids, at = torch.unique(tok[live].long(), return_inverse=True)
+    want = torch.zeros((len(ids), 8), device="cuda").index_add_(0, at, dy[live].float())
+    assert torch.equal(out[ids], want.bfloat16())
+    out[ids] = 0
+    assert not out.view(torch.int64).any()
