@@ -80,34 +80,68 @@ struct Rows {
     }
 };
 
-// For each of R rows and their slots: the last row of the slot, or kEarlier where a row
-// before it has the slot, which that one then takes along.  The whole block calls it; `sh`
-// holds R ints per warp.
+// For each of R rows, from `row` on, and their slots (negative: a row that does not count): the
+// last row of the slot, or kEarlier where a row before it has the slot, which that one then takes
+// along.  The whole block searches, kScan slots of a thread at first.
 constexpr int kEarlier = 0x7fffffff;
-template <int R>
-__device__ __forceinline__ void last_rows(const int32_t *slots, int n, const int (&slot)[R], int row, int (&last)[R],
-                                          int (*sh)[R]) {
+constexpr int kScan = 4;
+__device__ __forceinline__ void first_slots(const int32_t *slots, int n, int (&s)[kScan]) {
 #pragma unroll
-    for (int r = 0; r < R; r++) last[r] = row + r;
-#pragma unroll 4
-    for (int j = threadIdx.x; j < n; j += kThreads) {
-        const int s = slots[j];
+    for (int u = 0; u < kScan; u++) {
+        const int j = u * kThreads + threadIdx.x;
+        s[u] = j < n ? slots[j] : -1;
+    }
+}
+template <int R>
+struct alignas(4 * R) Lasts {
+    int x[R];
+};
+template <int R>
+struct Search {
+    int slot[R], last[R], row;
+
+    __device__ __forceinline__ void run(const int32_t *slots, int n, const int (&s)[kScan], Lasts<R> (*sh)[kWarps]) {
+#pragma unroll
+        for (int r = 0; r < R; r++) last[r] = row + r;
+#pragma unroll
+        for (int r = 1; r < R; r++)
+#pragma unroll
+            for (int e = 0; e < r; e++)
+                if (slot[e] == slot[r]) last[r] = kEarlier;
+#pragma unroll
+        for (int u = 0; u < kScan; u++) look(u * kThreads + threadIdx.x, s[u]);
+        // long batches: with tokens of few sequences in turn most rows are known to be kEarlier by now
+        if (n <= kScan * kThreads || join(sh[0])) return;
+#pragma unroll 8
+        for (int j = kScan * kThreads + threadIdx.x; j < n; j += kThreads) look(j, slots[j]);
+    }
+    // What the warps found; true where no row is left that counts and may be the first of its slot.
+    __device__ __forceinline__ bool join(Lasts<R> *sh) {
+        Lasts<R> own;
+#pragma unroll
+        for (int r = 0; r < R; r++) own.x[r] = __reduce_max_sync(0xffffffffu, last[r]);
+        if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = own;
+        __syncthreads();
+        bool done = true;
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) {
+            const Lasts<R> v = sh[w];
+#pragma unroll
+            for (int r = 0; r < R; r++) last[r] = max(last[r], v.x[r]);
+        }
+#pragma unroll
+        for (int r = 0; r < R; r++) done = done && (slot[r] < 0 || last[r] == kEarlier);
+        return done;
+    }
+
+  private:
+    __device__ __forceinline__ void look(int j, int s) {   // row j has slot s; the rows themselves have been compared
+        const int what = j < row ? kEarlier : j;
 #pragma unroll
         for (int r = 0; r < R; r++)
-            if (s == slot[r]) last[r] = max(last[r], j < row + r ? kEarlier : j);
+            if (s == slot[r]) last[r] = max(last[r], what);
     }
-#pragma unroll
-    for (int r = 0; r < R; r++) last[r] = __reduce_max_sync(0xffffffffu, last[r]);
-    if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-        for (int r = 0; r < R; r++) sh[threadIdx.x >> 5][r] = last[r];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; w++)
-#pragma unroll
-        for (int r = 0; r < R; r++) last[r] = max(last[r], sh[w][r]);
-}
+};
 
 struct Params {
     const void *q, *k, *v, *beta;
@@ -121,16 +155,63 @@ struct Params {
     int rows;   // of a CTA
 };
 
-// The rows of a CTA that may be the first of their slot: they have one, and the
-// row before has another.  Bit i: row `row0` + i; `slot` is lane i's.
-__device__ __forceinline__ uint32_t first_rows(const Params &p, int row0, int &slot) {
+// The rows of a CTA that are the first of their slot, which take its other rows along (bit i: row `row0` + i),
+// and those that another CTA's row takes along and that the row before does not tell of (bit 16 + i).
+// `own` gets the rows' slots, sh[1] the slots' last rows.  The whole block calls it, before a state is
+// read: a row that is taken along must cost no state's bytes, and in place the other CTA may be writing it.
+// All rows of a CTA in one search, the first slots on their way with the rows' own: 512 x 16 states take as
+// long as with the search behind the states' loads (158 us), which took 495 us for 256 sequences of 8 tokens in turn
+// (335 now) and 309 for 32 of 64 (215); the drafted tokens above 34 (35).  What comes back is the same in every lane and
+// the compiler has to know (a ballot): else the tokens' steps take more registers.
+template <int R>
+__device__ __forceinline__ uint32_t first_rows(const Params &p, int row0, int *own, Lasts<R> (*sh)[kWarps]) {
     const int lane = threadIdx.x & 31, row = row0 + lane;
-    const bool mine = lane < p.rows && row < p.n;
-    slot = row;
-    if (!p.slots) return __ballot_sync(0xffffffffu, mine);
-    slot = mine ? p.slots[row] : -1;
-    const int before = mine && row ? p.slots[row - 1] : -1;
-    return __ballot_sync(0xffffffffu, slot >= 0 && slot < p.num_slots && slot != before);
+    const bool there = lane < p.rows && row < p.n;
+    uint32_t may = __ballot_sync(0xffffffffu, there);
+    Search<R> f;
+    f.row = row0;
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+        f.slot[r] = -1 - r;
+        f.last[r] = row0 + r;
+    }
+    if (p.slots) {
+        int s[kScan];
+        first_slots(p.slots, p.n, s);
+        const int slot = there ? p.slots[row] : -1, before = there && row ? p.slots[row - 1] : -1;
+        // most rows that do not count are told by the row before
+        may = __ballot_sync(0xffffffffu, slot >= 0 && slot < p.num_slots && slot != before);
+        if (!may) return 0;
+        if (p.n > 1) {
+#pragma unroll
+            for (int r = 0; r < R; r++) {
+                const int x = __shfl_sync(0xffffffffu, slot, r);
+                f.slot[r] = may >> r & 1 ? x : -1 - r;
+            }
+            f.run(p.slots, p.n, s, sh);
+        }
+        if (threadIdx.x < R) own[lane] = slot;
+    }
+    f.join(sh[1]);
+    uint32_t others = 0;
+#pragma unroll
+    for (int r = 0; r < R; r++)
+        if (may >> r & 1 && f.last[r] == kEarlier) others |= 1u << r;
+    return __ballot_sync(0xffffffffu, ((may & ~others) | others << 16) >> lane & 1);
+}
+
+// What head x % H of row x / H reads, into the L2: the CTA that takes the row along finds it there (4
+// sequences of 256 tokens in turn 361 -> 274 us).
+template <typename T, int D, bool KDA>
+__device__ __forceinline__ void fetch_token(const Params &p, int64_t x) {
+    constexpr int per = 128 / (int)sizeof(T);   // values of a line
+    auto warm = [](const void *a) { asm volatile("prefetch.global.L2 [%0];" ::"l"(a)); };
+    for (int i = threadIdx.x * per; i < p.G * D; i += kThreads * per) warm((const T *)p.q + x * p.G * D + i);
+    if ((int)threadIdx.x < D / per) {
+        warm((const T *)p.k + x * D + threadIdx.x * per);
+        warm((const T *)p.v + x * D + threadIdx.x * per);
+    }
+    if (KDA && threadIdx.x < D / 32) warm(p.g + x * D + threadIdx.x * 32);
 }
 
 // Four columns of a row.
@@ -194,7 +275,8 @@ template <typename T, int D, bool KDA, int GP>
 __global__ void __launch_bounds__(kThreads, kVfirstPerSm<T>[GP]) delta_step_vfirst_kernel(Params p) {
     constexpr int L = D / 4, PER = 32 / L;        // lanes of a value dim, value dims of one load
     constexpr int N = 8 / PER;                    // value dims of a thread
-    __shared__ int shared_last[2][kWarps][1];
+    __shared__ Lasts<kMaxRows[1]> shared_last[2][kWarps];
+    __shared__ int own_slots[kMaxRows[1]];
     next_grid_may_start();
     previous_grid_done();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -217,22 +299,24 @@ __global__ void __launch_bounds__(kThreads, kVfirstPerSm<T>[GP]) delta_step_vfir
         if (KDA) f.a = *reinterpret_cast<const float4 *>(p.g + hk * D + k0);
         else f.a.x = p.g[hk];
     };
-    int slots, par = 0;
-    for (uint32_t firsts = first_rows(p, blockIdx.y * p.rows, slots); firsts; firsts &= firsts - 1, par ^= 1) {
-        const int at_bit = __ffs(firsts) - 1, row = blockIdx.y * p.rows + at_bit;
-        const int slot[1] = {__shfl_sync(0xffffffffu, slots, at_bit)};
+    const int row0 = blockIdx.y * p.rows;
+    const uint32_t found = first_rows<kMaxRows[1]>(p, row0, own_slots, shared_last);
+    for (uint32_t others = blockIdx.x % (D / kSlice) ? 0 : found >> 16; others; others &= others - 1)
+        fetch_token<T, D, KDA>(p, (int64_t)(row0 + __ffs(others) - 1) * p.H + h);
+    for (uint32_t firsts = found & 0xffff; firsts; firsts &= firsts - 1) {
+        const int at_bit = __ffs(firsts) - 1, row = row0 + at_bit, slot = p.slots ? own_slots[at_bit] : row;
+        int last = row;
+#pragma unroll
+        for (int x = 0; x < kWarps; x++) last = max(last, shared_last[1][x].x[at_bit]);
         load(row);
-        const int64_t so = (((int64_t)slot[0] * p.H + h) * D + v0) * D + k0;
+        const int64_t so = (((int64_t)slot * p.H + h) * D + v0) * D + k0;
         Quad S[N];
 #pragma unroll
         for (int i = 0; i < N; i++) {
             const float4 x = *reinterpret_cast<const float4 *>(p.state + so + PER * i * D);
             S[i] = Quad{make_float2(x.x, x.y), make_float2(x.z, x.w)};
         }
-        int last[1] = {row};
-        if (p.slots) last_rows<1>(p.slots, p.n, slot, row, last, shared_last[par]);
-        if (last[0] == kEarlier) continue;
-        Rows rows(p.slots, p.n, slot[0], row, last[0]);
+        Rows rows(p.slots, p.n, slot, row, last);
         for (int j = row; j < p.n;) {
             const int64_t hq = ((int64_t)j * p.H + h) * p.G;
             const Quad k = f.k.wide();
@@ -312,7 +396,8 @@ template <typename T, int D, bool KDA, int GP>
 __global__ void __launch_bounds__(kThreads, kStepPerSm<D>) delta_step_kernel(Params p) {
     using Tok = Token<D, KDA, GP>;
     constexpr int N = Tok::N;                     // key dims of a lane
-    __shared__ int shared_last[2][kWarps][1];
+    __shared__ Lasts<kMaxRows[0]> shared_last[2][kWarps];
+    __shared__ int own_slots[kMaxRows[0]];
     __shared__ Tok toks[kWarps];
     next_grid_may_start();
     previous_grid_done();
@@ -360,22 +445,24 @@ __global__ void __launch_bounds__(kThreads, kStepPerSm<D>) delta_step_kernel(Par
         float r = (odd ? keep.y : keep.x) + __shfl_xor_sync(0xffffffffu, odd ? keep.x : keep.y, 8);
         return r + __shfl_xor_sync(0xffffffffu, r, 4);
     };
-    int slots, par = 0;
-    for (uint32_t firsts = first_rows(p, blockIdx.y * p.rows, slots); firsts; firsts &= firsts - 1, par ^= 1) {
-        const int at_bit = __ffs(firsts) - 1, row = blockIdx.y * p.rows + at_bit;
-        const int slot[1] = {__shfl_sync(0xffffffffu, slots, at_bit)};
+    const int row0 = blockIdx.y * p.rows;
+    const uint32_t found = first_rows<kMaxRows[0]>(p, row0, own_slots, shared_last);
+    for (uint32_t others = blockIdx.x % (D / kWide) ? 0 : found >> 16; others; others &= others - 1)
+        fetch_token<T, D, KDA>(p, (int64_t)(row0 + __ffs(others) - 1) * p.H + h);
+    for (uint32_t firsts = found & 0xffff; firsts; firsts &= firsts - 1) {
+        const int at_bit = __ffs(firsts) - 1, row = row0 + at_bit, slot = p.slots ? own_slots[at_bit] : row;
+        int last = row;
+#pragma unroll
+        for (int x = 0; x < kWarps; x++) last = max(last, shared_last[1][x].x[at_bit]);
         load(row);
-        const int64_t so = (((int64_t)slot[0] * p.H + h) * D + k0) * D + v0;
+        const int64_t so = (((int64_t)slot * p.H + h) * D + k0) * D + v0;
         Quad S[N];
 #pragma unroll
         for (int i = 0; i < N; i++) {
             const float4 x = *reinterpret_cast<const float4 *>(p.state + so + i * D);
             S[i] = Quad{make_float2(x.x, x.y), make_float2(x.z, x.w)};
         }
-        int last[1] = {row};
-        if (p.slots) last_rows<1>(p.slots, p.n, slot, row, last, shared_last[par]);
-        if (last[0] == kEarlier) continue;
-        Rows rows(p.slots, p.n, slot[0], row, last[0]);
+        Rows rows(p.slots, p.n, slot, row, last);
         for (int j = row; j < p.n;) {
             const int64_t hq = ((int64_t)j * p.H + h) * p.G;
             T *out = (T *)p.o + hq * D + v0 + own;
@@ -457,6 +544,34 @@ __global__ void __launch_bounds__(kThreads, kStepPerSm<D>) delta_step_kernel(Par
         for (int i = 0; i < N; i++)
             *reinterpret_cast<float4 *>(p.state_out + so + i * D) = make_float4(S[i].x.x, S[i].x.y, S[i].y.x, S[i].y.y);
     }
+}
+
+// For each of R rows and their slots: the last row of the slot, or kEarlier where a row
+// before it has the slot, which that one then takes along.  The whole block calls it; `sh`
+// holds R ints per warp.
+template <int R>
+__device__ __forceinline__ void last_rows(const int32_t *slots, int n, const int (&slot)[R], int row, int (&last)[R],
+                                          int (*sh)[R]) {
+#pragma unroll
+    for (int r = 0; r < R; r++) last[r] = row + r;
+#pragma unroll 4
+    for (int j = threadIdx.x; j < n; j += kThreads) {
+        const int s = slots[j];
+#pragma unroll
+        for (int r = 0; r < R; r++)
+            if (s == slot[r]) last[r] = max(last[r], j < row + r ? kEarlier : j);
+    }
+#pragma unroll
+    for (int r = 0; r < R; r++) last[r] = __reduce_max_sync(0xffffffffu, last[r]);
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+        for (int r = 0; r < R; r++) sh[threadIdx.x >> 5][r] = last[r];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; w++)
+#pragma unroll
+        for (int r = 0; r < R; r++) last[r] = max(last[r], sh[w][r]);
 }
 
 // The causal conv's tokens: y = act(b + sum_i w_i x_i) over a slot's W - 1 kept
