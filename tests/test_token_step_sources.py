@@ -12,7 +12,7 @@ import pytest
 
 from test_early_launch_sources import kernels, sources
 
-READS = r"p\.state\s*\+|\bstate\s*\+\s*\(\(int64_t\)|load\(state\b"
+READS = r"p\.state\s*\+\s*so|load\(state\b"
 SEARCH = r"(?:first_rows|last_rows)\s*<"
 
 
@@ -21,7 +21,7 @@ def body(kernel):
     return found[kernel]
 
 
-@pytest.mark.parametrize("kernel", ["delta_step_kernel", "delta_step_vfirst_kernel"])
+@pytest.mark.parametrize("kernel", ["delta_step_kernel", "delta_step_vfirst_kernel", "conv1d_step_kernel"])
 def test_states_are_read_behind_the_rows_search(kernel):
     text = body(kernel)
     searches = [m.start() for m in re.finditer(SEARCH, text)]
