@@ -1,13 +1,13 @@
 """The mixers' token steps where a CTA has several rows, as a full batch has:
 delta rule with two rows a CTA ([dk, dv] states) and two to four ([dv, dk]
-ones), against the fp64 oracle: rows of one slot inside a CTA, next to one
-another and in turn, in several CTAs, empty rows among them, in place and into
-another pool.
+ones), the conv with two to four groups of rows, against the fp64 oracle: rows
+of one slot inside a CTA, next to one another and in turn, in several CTAs,
+empty rows among them, in place and into another pool.
 """
 import pytest
 import torch
 
-from test_gpu_token_step import _cuda, check_delta, draw_delta, run_delta  # noqa: F401  (_cuda: the GPU or a skip)
+from test_gpu_token_step import _cuda, check_conv, check_delta, conv_case, draw_delta, run_delta  # noqa: F401  (_cuda: the GPU or a skip)
 
 pytestmark = pytest.mark.gpu
 
@@ -93,3 +93,34 @@ def test_long_batches_of_tokens_in_turn(vfirst):
     case = draw_delta(n, 1, 1, 64, "kda", "fp32", 8, seed=1)
     o, out = run_delta(case, slots, "fp32", "kda", vfirst)
     check_delta(case, slots, o, out, "fp32")
+
+
+# ------------------------------------------------------------------ conv
+def conv_batch(dtype, channels, groups):
+    """The smallest odd batch whose CTAs have `groups` groups of rows each (conv_w's choice)."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rows, blocks = 4 if dtype == "bf16" else 2, -(-channels // 512)
+    return rows * -(-groups * 8 * sms // blocks) - 1
+
+
+@pytest.mark.parametrize("groups", [2, 3, 4])
+@pytest.mark.parametrize("order", ORDERS)
+def test_several_groups_of_conv_rows(order, groups):
+    for dtype, W, act, bias, in_place in (("bf16", 4, "silu", True, True), ("fp32", 3, None, False, False)):
+        C = 6152                                   # the last CTA of a row has two threads with channels
+        n = conv_batch(dtype, C, groups)
+        slots = slots_of(order, n)
+        S = n // 3 if order == "in no order" else max(slots) + 2
+        check_conv(conv_case(n, C, W, S, dtype, seed=groups), slots, dtype, act, bias, in_place)
+
+
+def test_conv_groups_without_slots():
+    n = conv_batch("bf16", 6152, 4)
+    check_conv(conv_case(n, 6152, 4, n + 1, "bf16"), None, "bf16")
+
+
+def test_conv_long_batches_of_tokens_in_turn():
+    n = 1501
+    slots = [i % 5 for i in range(n - 1)] + [6]
+    slots[700:1300] = [-1] * 600
+    check_conv(conv_case(n, 40, 4, 8, "bf16"), slots, "bf16")
