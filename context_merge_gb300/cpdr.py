@@ -609,6 +609,8 @@ class Context:
         ``fwd`` leaves ``final_state``), updated in place or into
         ``state_out``.  Rows with a slot outside 0 .. S - 1 are left alone;
         rows of one slot are its consecutive tokens."""
+        if k.dim() != 3 or state.dim() != 4:
+            raise ValueError("k must be [n, H, d] and state [S, H, d, d]")
         n, H, d = k.shape[0], self.H, self.d
         dt, dev = self.torch_dtype, self._dev
         wide, kv = (n, self.Hq, d), (n, H, d)
