@@ -21,14 +21,20 @@
 // is subtracted is corrected by it.
 //
 // Measured over 0.25 GB a tensor, TB/s (the measured copy: 6.8): forward with a
-// residual 6.5 to 7.1 at 64 to 16384 columns of bf16 and 6.2 to 7.1 of fp32;
-// without one 5.0 to 6.4 (bf16, up to 4096; 3.8 to 5.1 beyond) and 6.3 to 7.0 (fp32);
-// to e4m3 from bf16 5.3 to 6.7 up to 4096 and 3.8 to 5.5 beyond; backward with the
-// residual's gradient 5.4 to 6.8 (bf16 up to 4096 columns; 3.2 to 5.4 beyond) and
-// 5.9 to 6.8 (fp32 up to 6144; 4.1 to 5.6 beyond).  What is below the copy's rate is
-// bound by the exchanges: rows of bf16 have half the bytes for them, and the widest rows
-// leave one block an SM.  With two exchanges of sums a row (mean, then
-// squares) and scalar arithmetic: forward 5.8 to 6.6, backward 4.6 at 2048.
+// residual 6.4 to 7.0 at 64 to 16384 columns of bf16 and 6.2 to 7.0 of fp32;
+// without one 5.0 to 6.4 (bf16, up to 4096; 3.7 to 5.0 beyond) and 6.3 to 6.9 (fp32);
+// to e4m3 from bf16 5.2 to 6.8 up to 4096 and 3.8 to 5.5 beyond; backward with the
+// residual's gradient 5.4 to 6.8 (bf16 up to 4096 columns, but 4.6 at 776; 3.1 to 5.4
+// beyond) and 5.9 to 6.9 (fp32 up to 6144; 4.1 to 5.6 beyond).  What is below the
+// copy's rate is bound by the exchanges up to 4096 columns: rows of bf16 have half the
+// bytes for them.  Wide rows: forward, a row's loads are not on their way during the
+// exchanges of the one before (three and four vectors a thread do not stream), and
+// beyond 8192 columns of bf16 one block fills an SM; backward, beyond 12288 columns of
+// bf16 and 6144 of fp32 there is room for one stage alone, so that loads and arithmetic
+// take turns, the forms of bf16 with 512 x 3 and 512 x 4 and of fp32 with 512 x 8 spill
+// 132, 464 and 288 bytes a thread, and fp32 rows beyond 8192 read their weights from
+// the L2 three times.  With two exchanges of sums a row (mean, then squares) and scalar
+// arithmetic: forward 5.8 to 6.6, backward 4.6 at 2048.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -178,17 +184,20 @@ constexpr int kFwdRows = NV > (RES ? 0 : 4) ? 1 : 2;
 // the vectors of a thread.
 template <int TPR>
 constexpr int kFwdBlock = TPR < 128 ? 128 : TPR;
-constexpr int kFwdRegs[2][2][9] = {{{0, 48, 80, 104, 128, 0, 104, 0, 128}, {0, 40, 48, 64, 72, 0, 64, 0, 80}},
-                                   {{0, 40, 56, 72, 88, 0, 128, 0, 128}, {0, 32, 40, 48, 56, 0, 72, 0, 96}}};
+constexpr int kFwdRegs[2][2][9] = {{{0, 48, 0, 104, 128}, {0, 40, 48, 64, 72, 0, 0, 0, 80}},
+                                   {{0, 40, 56, 72, 88}, {0, 32, 40, 48, 56, 0, 0, 0, 96}}};
 template <typename T, int TPR, int NV, bool RES>
 constexpr int fwd_per_sm() {
-    constexpr int n = 65536 / (kFwdRegs[RES][kVecOf<T> == 4][NV] * kFwdBlock<TPR>);
+    constexpr int regs = kFwdRegs[RES][kVecOf<T> == 4][NV];
+    static_assert(regs > 0, "a form that no width runs");
+    constexpr int n = 65536 / (regs * kFwdBlock<TPR>);
     return n < 1 ? 1 : n;
 }
 
 // grid: row blocks.  A group of threads takes one row, or without a residual two,
 // whose loads take that one's place: both rows share the weights, and twice the
-// bytes are in flight (bf16 rows of 2048: 4.5 -> 5.9 TB/s).
+// bytes are in flight (TB/s with one row and with two: bf16 rows of 64 4.0 and 6.2, of
+// 1360 4.9 and 5.5; fp32 of 128 4.0 and 6.7, of 776 5.9 and 6.7; of fp32 2048 6.9 both).
 template <typename T, int TPR, int NV, bool E4M3, bool RES>
 __global__ void __launch_bounds__(kFwdBlock<TPR>, fwd_per_sm<T, TPR, NV, RES>()) layernorm_fwd_kernel(FwdParams p) {
     constexpr int V = kVecOf<T>, H = kPairs<T>, W = kFwdBlock<TPR> / 32, L = TPR < 32 ? TPR : 32;
@@ -645,8 +654,10 @@ int fwd(const FwdParams &p, int sms, void *st) {
             return launch_early(p.y8 ? layernorm_stream_kernel<T, TPR, NV, true> : layernorm_stream_kernel<T, TPR, NV, false>,
                                 dim3((unsigned)std::min<int64_t>((p.rows + per - 1) / per, (int64_t)sms * kept_per_sm<T, TPR, NV>())),
                                 kRowBlock<T, TPR, NV>, (size_t)kStages * (p.res ? 2 : 1) * NV * kRowBlock<T, TPR, NV> * 16, 1, st, p);
+        return fwd_as<T, TPR, NV, true>(p, st);
+    } else {
+        return p.res ? fwd_as<T, TPR, NV, true>(p, st) : fwd_as<T, TPR, NV, false>(p, st);
     }
-    return p.res ? fwd_as<T, TPR, NV, true>(p, st) : fwd_as<T, TPR, NV, false>(p, st);
 }
 
 template <typename T, int TPR, int NV>
@@ -664,27 +675,20 @@ int bwd(const BwdParams &p, int grid, float *dw, float *db, void *st) {
 template <typename T, typename F>
 int by_width_fwd(int width, F f) {
     const int vecs = (width + kVecOf<T> - 1) / kVecOf<T>;
-    if (vecs <= 1024) return by_width<T>(width, f);
+    if (vecs <= 768) return narrow_row<T>(vecs, f);
+    if (vecs <= 1024) return with<256, 4>(f);
     if (vecs <= 1536) return with<512, 3>(f);
     if constexpr (kVecOf<T> == 4) {
         if (vecs > 2048) return with<512, 8>(f);
     }
     return with<512, 4>(f);
 }
-// Threads and vectors of a row of the backward, which holds dw and db: two bf16
-// vectors a thread from 48 on (one vector, half of the loads for each exchange
-// between warps: rows of 1024 at 5.2 instead of 6.2 TB/s, of 4096 at 4.2
-// instead of 5.7).
+// Threads and vectors of a row of the backward, which holds dw and db: 512 threads
+// beyond 768 vectors (of bf16 with two vectors where that does; one vector, half of the loads for each
+// exchange between warps: rows of 1024 at 5.2 instead of 6.2 TB/s, of 4096 at 4.2 instead of 5.7).
 template <typename T, typename F>
 int by_width_bwd(int width, F f) {
     const int vecs = (width + kVecOf<T> - 1) / kVecOf<T>;
-    if constexpr (kVecOf<T> == 8) {
-        if (vecs > 48 && vecs <= 64) return with<32, 2>(f);
-        if (vecs > 96 && vecs <= 128) return with<64, 2>(f);
-        if (vecs > 192 && vecs <= 256) return with<128, 2>(f);
-        if (vecs > 384 && vecs <= 512) return with<256, 2>(f);
-        if (vecs > 768 && vecs <= 1024) return with<512, 2>(f);
-    }
     if (vecs <= 768) return narrow_row<T>(vecs, f);
     if (vecs <= 1024) return with<512, 2>(f);
     if (vecs <= 1536) return with<512, 3>(f);

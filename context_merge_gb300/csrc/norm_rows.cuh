@@ -51,7 +51,7 @@ int with(F f) {
 // Threads per row, and 16-byte vectors for each of them: groups of up to 256
 // threads with one or two vectors, three where two would leave a quarter of
 // the threads idle or more (bf16 rows of 264, forward 6.1 -> 7.0 TB/s and
-// backward 3.3 -> 5.1), and up to eight for wide rows.
+// backward 3.3 -> 5.1).  Wider rows are each norm's own.
 template <typename T, typename F>
 int narrow_row(int vecs, F f) {
     if (vecs <= 1) return with<1, 1>(f);
@@ -71,17 +71,6 @@ int narrow_row(int vecs, F f) {
     if (vecs <= 384) return with<128, 3>(f);
     if (vecs <= 512) return with<256, 2>(f);
     return with<256, 3>(f);
-}
-template <typename T, typename F>
-int by_width(int width, F f) {
-    const int vecs = (width + kVecOf<T> - 1) / kVecOf<T>;
-    if (vecs <= 768) return narrow_row<T>(vecs, f);
-    if (vecs <= 1024) return with<256, 4>(f);
-    if (vecs <= 1536) return with<256, 6>(f);
-    if constexpr (kVecOf<T> == 4) {
-        if (vecs > 2048) return with<512, 8>(f);
-    }
-    return with<256, 8>(f);
 }
 
 }  // namespace norm

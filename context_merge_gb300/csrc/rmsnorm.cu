@@ -354,6 +354,18 @@ int bwd(const BwdParams &p, int grid, float *dw, cudaStream_t st) {
     return launch_column_sums(p.part, grid, p.width, dw, st);
 }
 
+// Threads and vectors of a row: as narrow_row, and up to eight vectors for wide rows.
+template <typename T, typename F>
+int by_width(int width, F f) {
+    const int vecs = (width + kVecOf<T> - 1) / kVecOf<T>;
+    if (vecs <= 768) return narrow_row<T>(vecs, f);
+    if (vecs <= 1024) return with<256, 4>(f);
+    if (vecs <= 1536) return with<256, 6>(f);
+    if constexpr (kVecOf<T> == 4) {
+        if (vecs > 2048) return with<512, 8>(f);
+    }
+    return with<256, 8>(f);
+}
 // The same for the backward, whose thread holds dw besides: 512 threads a row
 // where the eight values of a bf16 vector, or eight vectors, would take too
 // many registers (fp32 rows of 6144 run at 6.6 TB/s as 256 x 6, at 4.9 as
