@@ -372,10 +372,14 @@ __global__ void __launch_bounds__(kSortThreads) sort_few_kernel(Pass p) {
 // filled by blocks of their own, among the segments'.
 constexpr int kSegment = 32;   // a warp's lanes
 // `beyond`, with so many segments that HBM bounds the sums, and with fewer, where
-// the longest segment does: 131072 rows of 2048 (27 blocks of segments an SM) 190 us
-// with 128 and 202 with 16; 100000 rows of 256, text-like tokens, 81 and 56.
+// the longest segment does: from 8 blocks of segments an SM on.  Text-like tokens, us with 128 and with 16, by
+// blocks an SM: rows of 2048 at 1.7 119 and 111, at 3.4 134 and 127, at 5 141 and 142, at 6.7 144 and 149, at 8.4 155 and
+// 163, at 13.5 190 and 202; rows of 256 at 1.3 80 and 55, at 3.4 96 and 79, at 6.7 138 and 130, at 10.3 194 and
+// 192, at 13.5 220 and 222; rows of 64 at 13.5 179 and 164.  (It is by the sizes alone: where every token has runs of
+// some 65, at 6.7 blocks, 128 takes 80 and 16 121.)
 constexpr int kBeyondMany = 128, kBeyondFew = 16;
-constexpr int kMaxGroups = 16;   // segments of a block, at most
+// Segments of a block, at most.  With 16 or 32: 100000 rows of 256 55 and 54 us, 262144 of 64 61 and 67, 1048576 of 64 164 and 156.
+constexpr int kMaxGroups = 16;
 
 struct Sums {
     const int2 *pair;           // (key, position), sorted
