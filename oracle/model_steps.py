@@ -22,8 +22,12 @@ def delta_steps(q, k, v, beta, g, state, slots, scale=1.0):
     column.  A column's error passes (I - beta k k^T) Diag(a), whose norm is at
     most max(1, |1 - beta |k|^2|) max a; a token adds, in norms of the column P
     behind the gate: 5 U32 |P| (exp, 4 U32, and its product), a dot product of
-    up to 16 roundings along a path, 16 U32 |k| |P| (Cauchy), times beta |k|,
-    three roundings of beta (v - .) k and one of the new column."""
+    up to 19 roundings along a path (of 128 key dims 16 multiply-adds in a lane
+    and three sums over lanes; where a lane has four of them, 3 and five), 19 U32
+    |k| |P| (Cauchy), times beta |k|, three roundings of beta (v - .) k and one of
+    the new column.  An output: 19 of P^T q and one of adding (q . k) D, whose own
+    are fewer (3 and five, one of D); the scale's is half a step of fp32 at most,
+    which the output's type adds."""
     q, k, v, beta, g, state = (as64(t) for t in (q, k, v, beta, g, state))
     state = state.copy()
     n, H, d = k.shape
@@ -42,7 +46,7 @@ def delta_steps(q, k, v, beta, g, state, slots, scale=1.0):
             state[s, h] = P + beta[i, h] * np.outer(k[i, h], x)
             new = np.linalg.norm(state[s, h], axis=0)
             E[s, h] = (max(1.0, abs(1 - beta[i, h] * kk * kk)) * a.max() * E[s, h]
-                       + U32 * (5 * c + 16 * b * kk * kk * c + 3 * b * kk * np.abs(x) + new))
+                       + U32 * (5 * c + 19 * b * kk * kk * c + 3 * b * kk * np.abs(x) + new))
             for j in range(h * G, (h + 1) * G):
                 qq = np.linalg.norm(q[i, j])
                 o[i, j] = scale * (state[s, h].T @ q[i, j])
