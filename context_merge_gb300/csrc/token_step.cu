@@ -11,17 +11,17 @@
 // for.  Products and sums are fp32; o is rounded once.
 //
 // Bound by HBM: a state is read and written once, however many tokens of its
-// sequence the call brings; it stays in registers between them.  The columns of
+// sequence the call brings and in whatever order; it stays in registers between them.  The columns of
 // S (the value dims) do not depend on one another, so a state head is cut into
 // slices of them, one CTA each, and a CTA's into its warps'.  No warp waits for another one
 // inside a token: sums that went through shared memory and a barrier (four warps
 // to 32 value dims) took 166 us where these take 157, and 97 with drafted tokens
 // instead of 35.
 //
-// Measured, bf16, d = 128, in graphs: 512 sequences of 16 states 157 us (6.9 TB/s,
-// the measured copy's rate; [dv, dk] states 156), 61 of 32 states with per-dim gates 42 us (6.1
-// TB/s), one of 16 states 3.5 us (latency).  1 to 8 drafted tokens of 48
-// sequences, 32 query heads on 16 states: 34 to 36 us where the states' bytes take 16: bound by
+// Measured, bf16, d = 128, in graphs: 512 sequences of 16 states 159 us (6.8 TB/s,
+// the measured copy's rate; [dv, dk] states the same), 61 of 32 states with per-dim gates 43 us (6.0
+// TB/s), one of 16 states 3.7 us (latency).  1 to 8 drafted tokens of 48
+// sequences, 32 query heads on 16 states: 35 to 36 us where the states' bytes take 16: bound by
 // instructions (70% of the issue slots), 250 a token and warp.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -47,10 +47,11 @@ template <int D>
 constexpr int kStepPerSm = D == 128 ? 3 : 4;
 template <typename T>
 constexpr int kVfirstPerSm[5] = {0, sizeof(T) == 2 ? 5 : 4, sizeof(T) == 2 ? 5 : 4, 0, sizeof(T) == 2 ? 4 : 3};
-// Rows of a CTA with [dk, dv] and [dv, dk] states, at most (a warp's lanes).  Drafted
+// Rows of a CTA with [dk, dv] and [dv, dk] states, at most.  Drafted
 // tokens leave most rows nothing to do: with one row each, 14000 CTAs come and
-// go for 3000 that work (37 us instead of 34); with four, the per-dim case above
-// takes 45 us instead of 42 and 41 with one.
+// go for 3000 that work (40 us instead of 36; 256 sequences of 1 to 8 tokens 238 instead of 194, but
+// 512 of one token 156 instead of 159).  [dk, dv] states: with one row the 256 sequences 210
+// us instead of 192 and 512 of one token 161 instead of 159; with four the per-dim case above 45 instead of 43.
 constexpr int kMaxRows[2] = {2, 4};
 
 __device__ __forceinline__ void put(float *p, int64_t i, float v) { p[i] = v; }
@@ -578,8 +579,10 @@ __device__ __forceinline__ void last_rows(const int32_t *slots, int n, const int
 // inputs (oldest first) and the row's own, which then is the newest one kept.  A
 // thread owns four channels, whose weights stay in registers for the rows of its
 // CTA; the loads of kConvRows rows are in flight at once.  512 rows of 6144 channels,
-// W = 4, bf16: 11.4 us (eight channels a thread 14, rows of their own 54), of which
-// the bytes take 7.3; the rest is a launch that fills the GPU little more than once.
+// W = 4, bf16: 11.5 us (eight channels a thread 14, rows of their own 54), of which
+// the bytes take 7.3; the rest is a launch and 1.7 waves (80 registers: 912 CTAs at once of
+// 1536), each waiting for slots, then windows.  More tokens of a slot come one after the other from HBM,
+// some 0.8 us each next to one another and up to 1.7 in turn.
 struct ConvParams {
     const void *x;
     const float *weight, *bias;
