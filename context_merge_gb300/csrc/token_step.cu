@@ -85,7 +85,7 @@ struct Rows {
 // last row of the slot, or kEarlier where a row before it has the slot, which that one then takes
 // along.  The whole block searches, kScan slots of a thread at first.
 constexpr int kEarlier = 0x7fffffff;
-constexpr int kScan = 4;
+constexpr int kScan = 4, kMore = 12;
 __device__ __forceinline__ void first_slots(const int32_t *slots, int n, int (&s)[kScan]) {
 #pragma unroll
     for (int u = 0; u < kScan; u++) {
@@ -113,8 +113,15 @@ struct Search {
         for (int u = 0; u < kScan; u++) look(u * kThreads + threadIdx.x, s[u]);
         // long batches: with tokens of few sequences in turn most rows are known to be kEarlier by now
         if (n <= kScan * kThreads || join(sh[0])) return;
-#pragma unroll 8
-        for (int j = kScan * kThreads + threadIdx.x; j < n; j += kThreads) look(j, slots[j]);
+        // a dozen on their way at once: up to 2048 rows cost one more latency (256 sequences of 8 tokens next to one
+        // another 207 -> 200 us)
+        for (int j = kScan * kThreads + threadIdx.x; j < n; j += kMore * kThreads) {
+            int x[kMore];
+#pragma unroll
+            for (int u = 0; u < kMore; u++) x[u] = j + u * kThreads < n ? slots[j + u * kThreads] : -1;
+#pragma unroll
+            for (int u = 0; u < kMore; u++) look(j + u * kThreads, x[u]);
+        }
     }
     // What the warps found; true where no row is left that counts and may be the first of its slot.
     __device__ __forceinline__ bool join(Lasts<R> *sh) {
@@ -162,7 +169,7 @@ struct Params {
 // read: a row that is taken along must cost no state's bytes, and in place the other CTA may be writing it.
 // All rows of a CTA in one search, the first slots on their way with the rows' own: 512 x 16 states take as
 // long as with the search behind the states' loads (158 us), which took 495 us for 256 sequences of 8 tokens in turn
-// (335 now) and 309 for 32 of 64 (215); the drafted tokens above 34 (35).  What comes back is the same in every lane and
+// (329 now) and 309 for 32 of 64 (214); the drafted tokens above 34 (35).  What comes back is the same in every lane and
 // the compiler has to know (a ballot): else the tokens' steps take more registers.
 template <int R>
 __device__ __forceinline__ uint32_t first_rows(const Params &p, int row0, int *own, Lasts<R> (*sh)[kWarps]) {
@@ -202,7 +209,7 @@ __device__ __forceinline__ uint32_t first_rows(const Params &p, int row0, int *o
 }
 
 // What head x % H of row x / H reads, into the L2: the CTA that takes the row along finds it there (4
-// sequences of 256 tokens in turn 361 -> 274 us).
+// sequences of 256 tokens in turn 361 -> 270 us).
 template <typename T, int D, bool KDA>
 __device__ __forceinline__ void fetch_token(const Params &p, int64_t x) {
     constexpr int per = 128 / (int)sizeof(T);   // values of a line

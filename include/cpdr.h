@@ -486,7 +486,7 @@ cpdr_status cpdr_embed_bwd(const cpdr_ctx *ctx, const int32_t *tokens, int64_t n
  * and inputs are finite (a dropped infinity is 0 times infinity).  All rows'
  * slots are looked through for each row that the one before does not tell of:
  * past some thousand rows that shows (one token a slot, H = 1, dk = 64: 4096
- * rows 30 us and 24 without slots, 65535 rows 1170 and 320).  A state is read
+ * rows 29 us and 24 without slots, 65535 rows 1170 and 320).  A state is read
  * by one row of its slot alone, whatever the rows' order.
  */
 cpdr_status cpdr_delta_step(const cpdr_ctx *ctx, const void *q, const void *k, const void *v, const void *beta,
